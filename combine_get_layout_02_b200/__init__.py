@@ -15,6 +15,14 @@ combine ("merge the expert outputs back, accumulating") of the DeepEP pages
 (GitHub-issue mirror "Technical Overview of DeepEP"; brainleap "Day2 DeepEP",
 "DeepEP是什么" and "All-to-All通信"), with FP8 dispatch and BF16 combine as in
 their benchmark settings, run inside one GPU with ranks as expert partitions.
+
+Between the two, with rows and weights in MXFP4 (four bits a value, one
+power-of-two scale per 32), and for training the loss that keeps the routing even:
+
+    wq, ws = quantize_mxfp4(w)                       # once; w [E, out, H]
+    recv_x, recv_scale = dispatch_mxfp4(x, lay.dst_pos, lay.num_recv_rows)
+    y = matmul_mxfp4(recv_x, recv_scale, wq, ws, lay.expert_offset, lay.capacity)
+    aux = balance_loss(logits, topk_idx, alpha=1e-3, grad_loss=g)   # .loss, .counts, .grad_logits
 """
 
 from __future__ import annotations
@@ -28,6 +36,8 @@ import torch
 __all__ = [
     "CglError", "Layout", "RankLayout", "lib", "get_layout", "get_rank_layout", "dispatch_fp8", "dispatch_bf16", "combine",
     "combine_backward", "decode_dispatch_fp8", "layout_workspace_bytes", "layout_kernel_count", "status_bits", "check_status", "new_status",
+    "quantize_mxfp4", "dequantize_mxfp4", "dispatch_mxfp4", "matmul_mxfp4", "BalanceLoss", "balance_loss",
+    "balance_loss_backward", "balance_loss_workspace_bytes",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -96,6 +106,20 @@ def lib():
         L.cgl_layout_dispatch_fp8.restype = I
         L.cgl_combine_backward.argtypes = [P, P, I64, P, P, I64, I, I, P, P, OP, P, P]
         L.cgl_combine_backward.restype = I
+        L.cgl_quantize_mxfp4.argtypes = [P, I, I64, I64, P, P, OP, P]
+        L.cgl_quantize_mxfp4.restype = I
+        L.cgl_dequantize_mxfp4.argtypes = [P, P, I64, I64, P, I, OP, P]
+        L.cgl_dequantize_mxfp4.restype = I
+        L.cgl_dispatch_mxfp4.argtypes = [P, I64, I, I, P, P, P, I64, OP, P, P]
+        L.cgl_dispatch_mxfp4.restype = I
+        L.cgl_matmul_mxfp4.argtypes = [P, P, I64, P, P, I, I, I, P, P, OP, P, P]
+        L.cgl_matmul_mxfp4.restype = I
+        L.cgl_balance_loss_workspace_bytes.argtypes = [I64, I, I, I64]
+        L.cgl_balance_loss_workspace_bytes.restype = C.c_size_t
+        L.cgl_balance_loss.argtypes = [P, I, P, I64, I, I, I64, C.c_float, I, P, P, P, P, P, P, C.c_size_t, P, P]
+        L.cgl_balance_loss.restype = I
+        L.cgl_balance_loss_backward.argtypes = [P, P, I, P, I64, I, I, I64, C.c_float, I, P, P, P, P]
+        L.cgl_balance_loss_backward.restype = I
         _lib = L
     return _lib
 
@@ -432,3 +456,214 @@ def layout_dispatch_fp8(topk_idx: torch.Tensor, x: torch.Tensor, num_experts: in
         workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
     _check(code, "cgl_layout_dispatch_fp8")
     return out, recv_x, recv_scale
+
+
+# ---- MXFP4 rows, the experts' product, the balance loss ----------------------------------------
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # cgl_dtype
+_SCORES = {"softmax": 0, "sigmoid": 1}                              # cgl_score
+
+
+def _launch(where: str, fn, device, stream, *args):
+    """fn(*args, stream) with `device` current (its own current stream unless one is given)."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            code = fn(*args, _stream(stream))
+    else:
+        code = fn(*args, _stream(stream))
+    if code != OK:
+        raise CglError(code, where)
+
+
+def _buf(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
+    """An output the caller may have passed: checked, or allocated."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
+        raise TypeError(f"{name} must be {dtype} on {device}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _same(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _float_type(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def quantize_mxfp4(x: torch.Tensor, *, codes: Optional[torch.Tensor] = None,
+                   scales: Optional[torch.Tensor] = None, num_sms: int = 0, stream=None):
+    """MXFP4 codes and scales of x [..., C], C % 32 == 0 (cgl_quantize_mxfp4).
+
+    Returns (codes uint8 [..., C/2], two codes a byte with the lower index in the low half;
+    scales uint8 [..., C/32], 2^(byte - 127)).  Blocks with an infinity or NaN get scale byte 255 (NaN)."""
+    x = _dev(x, "x")
+    dt = _float_type(x, "x")
+    if x.dim() < 1 or x.shape[-1] % 32 or x.shape[-1] == 0:
+        raise ValueError(f"x must have a last dimension that is a multiple of 32, got {tuple(x.shape)}")
+    c, lead = x.shape[-1], x.shape[:-1]
+    codes = _buf(codes, "codes", (*lead, c // 2), torch.uint8, x.device)
+    scales = _buf(scales, "scales", (*lead, c // 32), torch.uint8, x.device)
+    _launch("cgl_quantize_mxfp4", lib().cgl_quantize_mxfp4, x.device, stream, _ptr(x), dt, x.numel() // c, c,
+            _ptr(codes), _ptr(scales), _opts(num_sms))
+    return codes, scales
+
+
+def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16, *,
+                     out: Optional[torch.Tensor] = None, num_sms: int = 0, stream=None) -> torch.Tensor:
+    """The values MXFP4 codes [..., C/2] and scales [..., C/32] stand for, [..., C] (cgl_dequantize_mxfp4)."""
+    codes = _dev(codes, "codes", torch.uint8)
+    scales = _dev(scales, "scales", torch.uint8)
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    _same(codes.device, scales=scales)
+    c = 2 * codes.shape[-1] if codes.dim() else 0
+    if c == 0 or c % 32 or tuple(scales.shape) != (*codes.shape[:-1], c // 32):
+        raise ValueError(f"codes [..., C/2] and scales [..., C/32] expected, got {tuple(codes.shape)}, {tuple(scales.shape)}")
+    out = _buf(out, "out", (*codes.shape[:-1], c), dtype, codes.device)
+    _launch("cgl_dequantize_mxfp4", lib().cgl_dequantize_mxfp4, codes.device, stream, _ptr(codes), _ptr(scales),
+            out.numel() // c, c, _ptr(out), _DTYPES[dtype], _opts(num_sms))
+    return out
+
+
+def dispatch_mxfp4(x: torch.Tensor, dst_pos: torch.Tensor, num_recv_rows: int, *,
+                   recv_x: Optional[torch.Tensor] = None, recv_scale: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, num_sms: int = 0,
+                   scratch: Optional[torch.Tensor] = None, stream=None):
+    """MXFP4 dispatch: each token quantised once, its row written to its receive rows (cgl_dispatch_mxfp4).
+
+    scratch: new_scratch() (cgl_opts.scratch): tokens handed out dynamically, same results.
+    Returns (recv_x uint8 [rows, H/2], recv_scale uint8 [rows, H/32]); rows that receive no copy
+    are left as they were (uninitialised when allocated here)."""
+    x = _dev(x, "x", torch.bfloat16, 2)
+    dst = _dev(dst_pos, "dst_pos", torch.int32, 2)
+    n, h = x.shape
+    if dst.shape[0] != n:
+        raise ValueError(f"dst_pos must have {n} rows, got {dst.shape[0]}")
+    _same(x.device, dst_pos=dst, status=status, scratch=scratch)
+    if h == 0 or h % 32 or num_recv_rows < 0:
+        raise CglError(EINVAL, "dispatch_mxfp4", "hidden must be a multiple of 32")
+    recv_x = _buf(recv_x, "recv_x", (num_recv_rows, h // 2), torch.uint8, x.device)
+    recv_scale = _buf(recv_scale, "recv_scale", (num_recv_rows, h // 32), torch.uint8, x.device)
+    _launch("cgl_dispatch_mxfp4", lib().cgl_dispatch_mxfp4, x.device, stream, _ptr(x), n, h, dst.shape[1], _ptr(dst),
+            _ptr(recv_x), _ptr(recv_scale), int(num_recv_rows), _opts(num_sms, 0, False, scratch), _ptr(status))
+    return recv_x, recv_scale
+
+
+def matmul_mxfp4(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                 expert_offset: Optional[torch.Tensor] = None, capacity: int = 0, *,
+                 y: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                 num_sms: int = 0, stream=None) -> torch.Tensor:
+    """The experts' product on MXFP4 rows, y[r] = a[r] @ w[expert of r].T in BF16 (cgl_matmul_mxfp4).
+
+    a uint8 [rows, in/2], a_scale uint8 [rows, in/32] (dispatch_mxfp4 or quantize_mxfp4);
+    w uint8 [E, out, in/2], w_scale uint8 [E, out, in/32].  expert_offset int32 [E + 1] and
+    capacity as get_layout gives them; without expert_offset w has one expert (or is [out, in/2])
+    and takes every row.  Rows of no expert are left as they were."""
+    a = _dev(a, "a", torch.uint8, 2)
+    a_scale = _dev(a_scale, "a_scale", torch.uint8, 2)
+    w = _dev(w, "w", torch.uint8)
+    w_scale = _dev(w_scale, "w_scale", torch.uint8)
+    if expert_offset is None and w.dim() == 2 and w_scale.dim() == 2:
+        w, w_scale = w.unsqueeze(0), w_scale.unsqueeze(0)
+    if w.dim() != 3:
+        raise ValueError(f"w must have 3 dims, got {w.dim()}")
+    (rows, kb), (E, F) = a.shape, w.shape[:2]
+    K = 2 * kb
+    if (w.shape[2] != kb or K == 0 or K % 32 or tuple(a_scale.shape) != (rows, K // 32)
+            or tuple(w_scale.shape) != (E, F, K // 32)):
+        raise ValueError(f"a [rows, in/2], a_scale [rows, in/32], w [E, out, in/2], w_scale [E, out, in/32] expected, got "
+                         f"{tuple(a.shape)}, {tuple(a_scale.shape)}, {tuple(w.shape)}, {tuple(w_scale.shape)}")
+    if expert_offset is not None:
+        _dev(expert_offset, "expert_offset", torch.int32, 1)
+        if expert_offset.shape[0] != E + 1:
+            raise ValueError(f"expert_offset must have {E + 1} entries, got {expert_offset.shape[0]}")
+    _same(a.device, a_scale=a_scale, w=w, w_scale=w_scale, expert_offset=expert_offset, status=status)
+    y = _buf(y, "y", (rows, F), torch.bfloat16, a.device)
+    _launch("cgl_matmul_mxfp4", lib().cgl_matmul_mxfp4, a.device, stream, _ptr(a), _ptr(a_scale), rows, _ptr(w),
+            _ptr(w_scale), E, F, K, _ptr(expert_offset), _ptr(y), _opts(num_sms, capacity), _ptr(status))
+    return y
+
+
+class BalanceLoss(NamedTuple):
+    loss: torch.Tensor                    # fp32 [1]
+    counts: torch.Tensor                  # int32 [S, E]: slots per expert of each sequence
+    num_routed: torch.Tensor              # int32 [S]: tokens of each sequence with a copy somewhere
+    grad_logits: Optional[torch.Tensor]   # [N, E] in the logits' type, if grad_loss was given
+
+
+def balance_loss_workspace_bytes(num_tokens: int, num_topk: int, num_experts: int, num_sequences: int = 1) -> int:
+    return int(lib().cgl_balance_loss_workspace_bytes(num_tokens, num_topk, num_experts, num_sequences))
+
+
+def _balance_args(logits, topk_idx, score, num_sequences, where):
+    logits = _dev(logits, "logits", None, 2)
+    idx = _dev(topk_idx, "topk_idx", torch.int32, 2)
+    dt = _float_type(logits, "logits")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    if idx.shape[0] != logits.shape[0]:
+        raise ValueError(f"topk_idx must have {logits.shape[0]} rows, got {idx.shape[0]}")
+    _same(logits.device, topk_idx=idx)
+    n, E = logits.shape
+    ws_bytes = balance_loss_workspace_bytes(n, idx.shape[1], E, num_sequences)
+    if ws_bytes == 0:
+        raise CglError(EINVAL, where, "invalid sizes")
+    return logits, idx, dt, n, idx.shape[1], E, ws_bytes
+
+
+def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, *, num_sequences: int = 1, alpha: float = 1.0,
+                 score: str = "softmax", grad_loss: Optional[torch.Tensor] = None,
+                 loss: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                 num_routed: Optional[torch.Tensor] = None, grad_logits: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                 stream=None) -> BalanceLoss:
+    """Balance loss of a routing, its per-expert counts and, with grad_loss, its gradient (cgl_balance_loss).
+
+    logits [N, E] (bfloat16, float16 or float32), topk_idx int32 [N, k] (-1 = no copy; a token with no copy
+    takes no part).  score: "softmax", or "sigmoid" (normalised over the experts).  grad_loss: fp32 [1] on the
+    device, the gradient that arrives at the loss; without it, balance_loss_backward gives grad_logits later."""
+    logits, idx, dt, n, k, E, ws_bytes = _balance_args(logits, topk_idx, score, num_sequences, "balance_loss")
+    dev = logits.device
+    if grad_loss is not None:
+        _buf(_dev(grad_loss, "grad_loss", torch.float32), "grad_loss", (1,), torch.float32, dev)
+    elif grad_logits is not None:
+        raise ValueError("grad_logits needs grad_loss")
+    _same(dev, status=status)
+    loss = _buf(loss, "loss", (1,), torch.float32, dev)
+    counts = _buf(counts, "counts", (num_sequences, E), torch.int32, dev)
+    num_routed = _buf(num_routed, "num_routed", (num_sequences,), torch.int32, dev)
+    if grad_loss is not None:
+        grad_logits = _buf(grad_logits, "grad_logits", (n, E), logits.dtype, dev)
+    if workspace is None:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    else:
+        _same(dev, workspace=_dev(workspace, "workspace"))
+    _launch("cgl_balance_loss", lib().cgl_balance_loss, dev, stream, _ptr(logits), dt, _ptr(idx), n, k, E,
+            num_sequences, float(alpha), _SCORES[score], _ptr(grad_loss), _ptr(loss), _ptr(counts), _ptr(num_routed),
+            _ptr(grad_logits), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status))
+    return BalanceLoss(loss, counts, num_routed, grad_logits)
+
+
+def balance_loss_backward(grad_loss: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor,
+                          counts: torch.Tensor, num_routed: torch.Tensor, *, num_sequences: int = 1,
+                          alpha: float = 1.0, score: str = "softmax", grad_logits: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """Gradient of balance_loss for the logits, from the forward's counts and num_routed (cgl_balance_loss_backward)."""
+    logits, idx, dt, n, k, E, _ = _balance_args(logits, topk_idx, score, num_sequences, "balance_loss_backward")
+    dev = logits.device
+    _buf(_dev(grad_loss, "grad_loss", torch.float32), "grad_loss", (1,), torch.float32, dev)
+    _buf(_dev(counts, "counts", torch.int32), "counts", (num_sequences, E), torch.int32, dev)
+    _buf(_dev(num_routed, "num_routed", torch.int32), "num_routed", (num_sequences,), torch.int32, dev)
+    grad_logits = _buf(grad_logits, "grad_logits", (n, E), logits.dtype, dev)
+    _launch("cgl_balance_loss_backward", lib().cgl_balance_loss_backward, dev, stream, _ptr(grad_loss), _ptr(logits),
+            dt, _ptr(idx), n, k, E, num_sequences, float(alpha), _SCORES[score], _ptr(counts), _ptr(num_routed),
+            _ptr(grad_logits))
+    return grad_logits

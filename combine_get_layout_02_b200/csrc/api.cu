@@ -131,7 +131,7 @@ using namespace cgl;
 
 extern "C" {
 
-int cgl_version(void) { return 300; }
+int cgl_version(void) { return 400; }
 
 const char *cgl_status_string(int s) {
     switch (s) {
@@ -336,6 +336,106 @@ cgl_status cgl_selftest_bounded_wait(uint64_t *workspace, int nflags, uint32_t *
     if (!workspace || !status_dev || nflags < 1 || nflags > 4096) return CGL_EINVAL;
     if (!aligned(workspace, 8) || !aligned(status_dev, 4)) return CGL_EALIGN;
     return launch_wait_probe(workspace, nflags, status_dev, static_cast<cudaStream_t>(stream));
+}
+
+static bool dtype_ok(int dtype) { return dtype == CGL_BF16 || dtype == CGL_F16 || dtype == CGL_F32; }
+
+// Rows of MXFP4: codes (cols / 2 bytes a row) at most 2^62 values in all.
+static bool mx_sizes_ok(int64_t rows, int64_t cols) {
+    return rows >= 0 && cols > 0 && cols % 32 == 0 && cols <= ((int64_t)1 << 30) && rows <= ((int64_t)1 << 32) &&
+           rows <= ((int64_t)1 << 48) / cols;
+}
+
+cgl_status cgl_quantize_mxfp4(const void *x, int dtype, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scales,
+                              const cgl_opts *opts, void *stream) {
+    if (!mx_sizes_ok(rows, cols) || !dtype_ok(dtype) || opt_sms(opts) < 0 || !flags_ok(opts)) return CGL_EINVAL;
+    if (rows > 0 && (!x || !codes || !scales)) return CGL_EINVAL;
+    if (!aligned(x, 16) || !aligned(codes, 16)) return CGL_EALIGN;
+    return launch_quantize_mxfp4(x, dtype, rows, cols, codes, scales, opt_sms(opts), static_cast<cudaStream_t>(stream));
+}
+
+cgl_status cgl_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
+                                int dtype, const cgl_opts *opts, void *stream) {
+    if (!mx_sizes_ok(rows, cols) || !dtype_ok(dtype) || opt_sms(opts) < 0 || !flags_ok(opts)) return CGL_EINVAL;
+    if (rows > 0 && (!out || !codes || !scales)) return CGL_EINVAL;
+    if (!aligned(out, 16) || !aligned(codes, 16)) return CGL_EALIGN;
+    return launch_dequantize_mxfp4(codes, scales, rows, cols, out, dtype, opt_sms(opts),
+                                   static_cast<cudaStream_t>(stream));
+}
+
+cgl_status cgl_dispatch_mxfp4(const uint16_t *x, int64_t n, int h, int k, const int32_t *dst_pos, uint8_t *recv_x,
+                              uint8_t *recv_scale, int64_t recv_rows, const cgl_opts *opts, uint32_t *status_dev,
+                              void *stream) {
+    if (!mx_sizes_ok(n, h) || k < 1 || k > kMaxTopk || n * (int64_t)k >= ((int64_t)1 << 31) || recv_rows < 0)
+        return CGL_EINVAL;
+    if (opt_sms(opts) < 0 || !flags_ok(opts)) return CGL_EINVAL;
+    if (n > 0 && (!x || !dst_pos)) return CGL_EINVAL;
+    if (n > 0 && recv_rows > 0 && (!recv_x || !recv_scale)) return CGL_EINVAL;
+    if (!aligned(x, 16) || !aligned(recv_x, 16) || !aligned(dst_pos, 4) || !aligned(status_dev, 4) ||
+        !aligned(opt_scratch(opts), 8))
+        return CGL_EALIGN;
+    return launch_dispatch_mxfp4(x, n, h, k, dst_pos, recv_x, recv_scale, recv_rows, opt_sms(opts), status_dev,
+                                 static_cast<cudaStream_t>(stream), opt_scratch(opts));
+}
+
+cgl_status cgl_matmul_mxfp4(const uint8_t *a, const uint8_t *a_scale, int64_t num_rows, const uint8_t *w,
+                            const uint8_t *w_scale, int E, int F, int K, const int32_t *expert_offset, uint16_t *y,
+                            const cgl_opts *opts, uint32_t *status_dev, void *stream) {
+    if (E < 1 || E > kMaxExperts || F < 1 || F > (1 << 20) || K < 32 || K % 32 != 0 || K > (1 << 20) || num_rows < 0 ||
+        num_rows >= ((int64_t)1 << 31))
+        return CGL_EINVAL;
+    const int cap = opt_cap(opts);
+    if (cap < 0 || opt_sms(opts) < 0 || !flags_ok(opts)) return CGL_EINVAL;
+    if (!expert_offset && (E != 1 || cap != 0)) return CGL_EINVAL;
+    if (cap > 0 && num_rows < (int64_t)E * cap) return CGL_EINVAL;
+    if (!w || !w_scale) return CGL_EINVAL;
+    if (num_rows > 0 && (!a || !a_scale || !y)) return CGL_EINVAL;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(y, 2) || !aligned(expert_offset, 4) || !aligned(status_dev, 4))
+        return CGL_EALIGN;
+    return launch_matmul_mxfp4(a, a_scale, num_rows, w, w_scale, E, F, K, expert_offset, cap, y, opt_sms(opts),
+                               status_dev, static_cast<cudaStream_t>(stream));
+}
+
+static bool balance_sizes_ok(int64_t n, int k, int E, int64_t S) {
+    return n >= 0 && k >= 1 && k <= kMaxTopk && E >= 1 && E <= kMaxExperts && S >= 1 && S <= ((int64_t)1 << 24) &&
+           n % S == 0 && n * (int64_t)k < ((int64_t)1 << 31);
+}
+
+size_t cgl_balance_loss_workspace_bytes(int64_t n, int k, int E, int64_t S) {
+    return balance_sizes_ok(n, k, E, S) ? balance_workspace_bytes(n, k, E, S) : 0;
+}
+
+cgl_status cgl_balance_loss(const void *logits, int dtype, const int32_t *topk_idx, int64_t n, int k, int E, int64_t S,
+                            float alpha, int score, const float *grad_loss, float *loss, int32_t *counts,
+                            int32_t *num_routed, void *grad_logits, void *workspace, size_t workspace_bytes,
+                            uint32_t *status_dev, void *stream) {
+    if (!balance_sizes_ok(n, k, E, S) || !dtype_ok(dtype)) return CGL_EINVAL;
+    if (score != CGL_SCORE_SOFTMAX && score != CGL_SCORE_SIGMOID) return CGL_EINVAL;
+    if (!loss || !counts || !num_routed || !workspace) return CGL_EINVAL;
+    if (n > 0 && (!logits || !topk_idx)) return CGL_EINVAL;
+    if (workspace_bytes < balance_workspace_bytes(n, k, E, S)) return CGL_EINVAL;
+    const size_t item = dtype == CGL_F32 ? 4 : 2;
+    if (!aligned(logits, item) || !aligned(grad_logits, item) || !aligned(topk_idx, 4) || !aligned(grad_loss, 4) ||
+        !aligned(loss, 4) || !aligned(counts, 4) || !aligned(num_routed, 4) || !aligned(workspace, 16) ||
+        !aligned(status_dev, 4))
+        return CGL_EALIGN;
+    return launch_balance_loss(logits, dtype, topk_idx, n, k, E, S, alpha, score, grad_loss, loss, counts, num_routed,
+                               grad_logits, workspace, status_dev, static_cast<cudaStream_t>(stream));
+}
+
+cgl_status cgl_balance_loss_backward(const float *grad_loss, const void *logits, int dtype, const int32_t *topk_idx,
+                                     int64_t n, int k, int E, int64_t S, float alpha, int score, const int32_t *counts,
+                                     const int32_t *num_routed, void *grad_logits, void *stream) {
+    if (!balance_sizes_ok(n, k, E, S) || !dtype_ok(dtype)) return CGL_EINVAL;
+    if (score != CGL_SCORE_SOFTMAX && score != CGL_SCORE_SIGMOID) return CGL_EINVAL;
+    if (!counts || !num_routed) return CGL_EINVAL;
+    if (n > 0 && (!logits || !topk_idx || !grad_logits)) return CGL_EINVAL;
+    const size_t item = dtype == CGL_F32 ? 4 : 2;
+    if (!aligned(logits, item) || !aligned(grad_logits, item) || !aligned(topk_idx, 4) || !aligned(grad_loss, 4) ||
+        !aligned(counts, 4) || !aligned(num_routed, 4))
+        return CGL_EALIGN;
+    return launch_balance_loss_backward(grad_loss, logits, dtype, topk_idx, n, k, E, S, alpha, score, counts,
+                                        num_routed, grad_logits, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

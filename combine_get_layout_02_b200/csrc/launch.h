@@ -110,4 +110,27 @@ cgl_status launch_combine_backward(const uint16_t *g, const uint16_t *y, int64_t
                                    uint16_t *grad_y, float *grad_w, int num_sms, uint32_t *status,
                                    cudaStream_t stream);
 
+// MXFP4 rows (dtype: a cgl_dtype; cols a multiple of 32).
+cgl_status launch_quantize_mxfp4(const void *x, int dtype, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scales,
+                                 int num_sms, cudaStream_t stream);
+cgl_status launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
+                                   int dtype, int num_sms, cudaStream_t stream);
+cgl_status launch_dispatch_mxfp4(const uint16_t *x, int64_t n, int h, int k, const int32_t *dst_pos, uint8_t *recv_x,
+                                 uint8_t *recv_scale, int64_t recv_rows, int num_sms, uint32_t *status,
+                                 cudaStream_t stream, unsigned long long *claim);
+
+// The experts' product on MXFP4 rows (off null: one expert, all rows).
+cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows, const uint8_t *w, const uint8_t *sw,
+                               int E, int F, int K, const int32_t *off, int64_t cap, uint16_t *y, int num_sms,
+                               uint32_t *status, cudaStream_t stream);
+
+// Balance loss (score: 0 softmax, 1 normalised sigmoid; grad null: loss and counts only).
+size_t balance_workspace_bytes(int64_t n, int k, int E, int64_t S);
+cgl_status launch_balance_loss(const void *logits, int dtype, const int32_t *idx, int64_t n, int k, int E, int64_t S,
+                               float alpha, int score, const float *grad_loss, float *loss, int32_t *counts,
+                               int32_t *routed, void *grad, void *ws, uint32_t *status, cudaStream_t stream);
+cgl_status launch_balance_loss_backward(const float *grad_loss, const void *logits, int dtype, const int32_t *idx,
+                                        int64_t n, int k, int E, int64_t S, float alpha, int score,
+                                        const int32_t *counts, const int32_t *routed, void *grad, cudaStream_t stream);
+
 }  // namespace cgl

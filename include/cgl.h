@@ -111,7 +111,7 @@ typedef struct cgl_opts {
 
 /* Library version (major * 10000 + minor * 100 + patch).  0.2.0 added
  * cgl_opts.flags and 0.3.0 cgl_opts.scratch: C callers built against an older
- * cgl.h must be rebuilt. */
+ * cgl.h must be rebuilt.  0.4.0 added the MXFP4 calls and the balance loss. */
 int cgl_version(void);
 
 /* A static string naming a cgl_status value (or "unknown status"). */
@@ -424,6 +424,127 @@ cgl_status cgl_combine_backward(const uint16_t *grad_out, const uint16_t *y, int
  * nflags in [1, 4096].  The pages have no counterpart.
  */
 cgl_status cgl_selftest_bounded_wait(uint64_t *workspace, int nflags, uint32_t *status_dev, void *stream);
+
+/* Element types of the calls that take more than one. */
+typedef enum cgl_dtype { CGL_BF16 = 0, CGL_F16 = 1, CGL_F32 = 2 } cgl_dtype;
+
+/*
+ * MXFP4 rows (the OCP microscaling format).  Blocks of 32 consecutive values of
+ * a row share one scale 2^(byte - 127) (UE8M0; byte 255 is NaN); each value is a
+ * 4-bit E2M1 code: bit 3 the sign, bits 2:0 one of 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ * A row of C values (C % 32 == 0) is C/2 bytes of codes, two a byte with the
+ * lower index in bits 3:0, and C/32 scale bytes.  A value is code * scale.
+ * The pages name low-precision dispatch only as FP8; this is the next format
+ * down, with an exponent-only scale like CGL_OPT_UE8M0_SCALES.
+ *
+ * cgl_quantize_mxfp4 -- per block: scale = 2^e for the smallest e >= -127 with
+ * 6 * 2^e >= max |x| (no value saturates; an all-zero block has e = -127), codes
+ * = x * 2^-e rounded to the nearest E2M1 value, ties to the even code (a zero or
+ * a value that rounds to zero keeps its sign).  A block that holds an infinity
+ * or a NaN gets scale byte 255 and codes 0: all 32 values read back as NaN.
+ * In (device): x [rows, cols], a cgl_dtype.  Out (device, written in full):
+ *   codes uint8 [rows, cols/2]; scales uint8 [rows, cols/32].
+ * Requires cols % 32 == 0, cols <= 2^30, rows <= 2^32, rows * cols <= 2^48; x
+ * and codes 16-byte aligned, scales any.  opts: num_sms.
+ */
+cgl_status cgl_quantize_mxfp4(const void *x, int dtype, int64_t rows, int64_t cols, uint8_t *codes,
+                              uint8_t *scales, const cgl_opts *opts, void *stream);
+
+/*
+ * cgl_dequantize_mxfp4 -- out = code * scale in the given type (exact in binary32
+ * and, inside its range, BF16; rounded to nearest in FP16, past its range an
+ * infinity).  Sizes, alignment and opts as for cgl_quantize_mxfp4 (out 16-byte
+ * aligned).
+ */
+cgl_status cgl_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols,
+                                void *out, int dtype, const cgl_opts *opts, void *stream);
+
+/*
+ * cgl_dispatch_mxfp4 -- cgl_dispatch_fp8 with MXFP4 rows: each token's row is
+ * quantised once, as cgl_quantize_mxfp4 does it, and written to its receive rows.
+ * In (device): x BF16 [num_tokens, hidden]; dst_pos int32 [num_tokens, num_topk].
+ * Out (device): recv_x uint8 [num_recv_rows, hidden/2], recv_scale uint8
+ *   [num_recv_rows, hidden/32].  Rows that receive no copy are NOT written.
+ * Requires hidden % 32 == 0; x and recv_x 16-byte aligned; dst_pos 4-byte.
+ * opts: num_sms, scratch (as for cgl_dispatch_fp8; same results).
+ * Device errors: CGL_ERANGE if some dst_pos >= num_recv_rows (that copy is skipped).
+ */
+cgl_status cgl_dispatch_mxfp4(const uint16_t *x, int64_t num_tokens, int hidden, int num_topk,
+                              const int32_t *dst_pos, uint8_t *recv_x, uint8_t *recv_scale,
+                              int64_t num_recv_rows, const cgl_opts *opts, uint32_t *status_dev, void *stream);
+
+/*
+ * cgl_matmul_mxfp4 -- the experts' product between dispatch and combine:
+ *   y[r, f] = bf16_rn( sum_k a[r, k] * w[e, f, k] )   for every row r of expert e,
+ * a and w MXFP4, the sum in binary32 (the order of its terms is this library's;
+ * the same for the same sizes and options on the same kind of GPU).  Forward
+ * only: a product with weights held in four bits is a serving call.
+ * Rows of expert e: [expert_offset[e], expert_offset[e + 1]) (compact), or with
+ * opts.capacity > 0 the first min(expert_offset[e + 1] - expert_offset[e], capacity)
+ * rows from e * capacity (padded): what cgl_get_layout gives in either form.
+ * expert_offset NULL: one expert (num_experts = 1) with all num_rows rows.
+ * In (device): a uint8 [num_rows, in/2], a_scale uint8 [num_rows, in/32] (rows of
+ *   no expert may hold anything); w uint8 [E, out, in/2], w_scale uint8
+ *   [E, out, in/32]; expert_offset int32 [E + 1].
+ * Out (device): y BF16 [num_rows, out]; rows of no expert are NOT written.
+ * Requires in % 32 == 0; in, out <= 2^20; num_rows < 2^31, and >= E * capacity
+ * when padded; a and w 16-byte aligned, y 2-byte.  opts: capacity, num_sms.
+ * Device errors: CGL_ERANGE when offsets run backwards or past num_rows (clamped).
+ */
+cgl_status cgl_matmul_mxfp4(const uint8_t *a, const uint8_t *a_scale, int64_t num_rows, const uint8_t *w,
+                            const uint8_t *w_scale, int num_experts, int out_features, int in_features,
+                            const int32_t *expert_offset, uint16_t *y, const cgl_opts *opts,
+                            uint32_t *status_dev, void *stream);
+
+/* How logits become the probabilities that the balance loss weighs. */
+typedef enum cgl_score {
+    CGL_SCORE_SOFTMAX = 0,   /* p = softmax(logits) */
+    CGL_SCORE_SIGMOID = 1    /* p = sigmoid(logits) / their sum over the experts */
+} cgl_score;
+
+/* Bytes of device workspace cgl_balance_loss needs; host-only, 0 for invalid sizes. */
+size_t cgl_balance_loss_workspace_bytes(int64_t num_tokens, int num_topk, int num_experts,
+                                        int64_t num_sequences);
+
+/*
+ * cgl_balance_loss -- the auxiliary loss that keeps the experts' loads even, the
+ * per-expert counts it rests on and, if asked for, its gradient.  The pages
+ * describe the dispatch of a routing that training has balanced; the loss is
+ * the commonly used product of load and mean probability.
+ * The batch is num_sequences sequences of num_tokens / num_sequences tokens
+ * (1: the loss of the whole batch).  A token is routed if one of its slots
+ * holds an id in [0, E); T_s routed tokens in sequence s, others (padding, all
+ * ids -1) take no part.  With c[s, e] the slots of s with id e, S sequences:
+ *   loss = alpha / S * sum_s sum_e (E * c[s, e] / (k * T_s)) * (1 / T_s) * sum_t p[t, e]
+ * (0 from a sequence with T_s = 0).  A token whose logits are all -inf has
+ * p = 0; a NaN logit makes its token's p, the loss and its gradient row NaN, as
+ * does +inf with the softmax.
+ * In (device): logits [num_tokens, E], a cgl_dtype; topk_idx int32 [num_tokens,
+ *   num_topk] as for cgl_get_layout; grad_loss binary32 [1] (NULL: 1).
+ * Out (device, written in full): loss binary32 [1]; counts int32 [S, E];
+ *   num_routed int32 [S] (T_s); grad_logits [num_tokens, E] in the logits' type =
+ *   grad_loss * dloss/dlogits (0 for tokens not routed), or NULL for none.
+ * The counts carry no gradient.  Sums are binary32 or wider, in a fixed order.
+ * workspace: device, 16-byte aligned, any contents, scratch for the call.
+ * Limits: num_tokens % num_sequences == 0, num_sequences <= 2^24, and the
+ * library's own.  Device errors: CGL_ERANGE for ids < -1 or >= E (not counted).
+ */
+cgl_status cgl_balance_loss(const void *logits, int dtype, const int32_t *topk_idx, int64_t num_tokens,
+                            int num_topk, int num_experts, int64_t num_sequences, float alpha, int score,
+                            const float *grad_loss, float *loss, int32_t *counts, int32_t *num_routed,
+                            void *grad_logits, void *workspace, size_t workspace_bytes,
+                            uint32_t *status_dev, void *stream);
+
+/*
+ * cgl_balance_loss_backward -- grad_logits alone, from the counts and num_routed
+ * that cgl_balance_loss gave for the same inputs (which then was called with
+ * grad_logits NULL, before grad_loss was known).  Same arguments and limits.
+ */
+cgl_status cgl_balance_loss_backward(const float *grad_loss, const void *logits, int dtype,
+                                     const int32_t *topk_idx, int64_t num_tokens, int num_topk,
+                                     int num_experts, int64_t num_sequences, float alpha, int score,
+                                     const int32_t *counts, const int32_t *num_routed, void *grad_logits,
+                                     void *stream);
 
 #ifdef __cplusplus
 }
