@@ -1,5 +1,26 @@
 // The experts' product on MXFP4 rows: y[r, :] = A[r, :] W[e(r), :, :]^T, sums in
 // binary32, BF16 out (format in mxfp4.cuh).
+//
+// Tensor cores: tcgen05.mma kind::mxf4 with block scales (32 values a scale,
+// 64 values an instruction).  The weights are the M side (128 output features a
+// tile) and the tokens the N side, whose width goes by the expert's rows, 16 at
+// a time: few rows cost few columns, and each weight tile is read once for up
+// to `nt` rows.  Persistent blocks, one per SM, walk the list of (expert, rows,
+// features) tiles; each block makes the list's prefix sums from expert_offset
+// for itself.  One block:
+//   warp 0      TMA: a ring of stages of 256 values (128 bytes) a row, 128-byte swizzle
+//   warp 1      TMEM, and the MMA thread: scales smem -> TMEM (tcgen05.cp), 4 MMAs a stage
+//   warp 2      the weights' scales, 3 and 8 the tokens': global rows -> the 512-byte
+//               blocks that tcgen05.cp wants (row r's word at (r % 32) * 16 + (r / 32) * 4)
+//   warps 4-7   TMEM -> registers -> BF16 rows, while the next tile's MMAs run
+// Scales stay in their rows in memory, [rows, in / 32], because a tile starts at
+// any row of the receive buffer; a warp reads 32 bytes of each row, four stages'
+// worth, one such chunk ahead.
+//
+// Every wait is bounded (about a second, then CGL_ETIMEOUT): the block's roles
+// leave their loops, copies and MMAs in flight are waited for, TMEM is freed.
+#include <cuda.h>
+
 #include "mxfp4.cuh"
 #include "launch.h"
 
@@ -7,97 +28,485 @@ namespace cgl {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 64;
+constexpr uint32_t kErrTimeout = 1u << CGL_ETIMEOUT;
+constexpr long long kWaitCycles = 1ll << 31;
+constexpr int kThreads = 288;
+constexpr int kStageK = 256;              // values a stage
+constexpr int kM = 128;                   // features a tile
+constexpr int kBoxRows = 32;              // token rows a TMA box
+constexpr int kMaxStages = 10;
+constexpr int kMaxNt = 208;               // 2 accumulators of 208 columns + 4 stages of scales = 512 columns
+constexpr size_t kSmemLimit = 226 * 1024; // dynamic part: 227 KiB less the static part
+constexpr uint32_t kABytes = kM * kStageK / 2;
+constexpr uint32_t kBoxBytes = kBoxRows * kStageK / 2;
 
-// Rows [r0, r1) of expert e.  Offsets that run backwards or out of the buffer
-// are clamped and reported.
-__device__ __forceinline__ void expert_rows(const int32_t *off, int e, int64_t rows, int64_t cap, int64_t &r0,
-                                            int64_t &r1, bool &bad) {
-    if (off == nullptr) {
-        r0 = 0;
-        r1 = rows;
-        return;
-    }
-    const int64_t a = __ldg(off + e), b = __ldg(off + e + 1);
-    if (a < 0 || b < a) bad = true;
-    if (cap > 0) {
-        const int64_t c = b - a;
-        r0 = e * cap;
-        r1 = r0 + (c < 0 ? 0 : c > cap ? cap : c);
-    } else {
-        if (b > rows) bad = true;
-        r0 = a < 0 ? 0 : a > rows ? rows : a;
-        r1 = b < r0 ? r0 : b > rows ? rows : b;
+struct Params {
+    const uint8_t *sa, *sw;
+    const int32_t *off;
+    uint16_t *y;
+    uint32_t *status;
+    int64_t rows, cap;
+    int E, F, K;
+    int nt;          // most token columns a tile
+    int nb;          // 128-row scale blocks of the token side (1 or 2)
+    int nbox;        // TMA boxes of the token side a stage has room for
+    int stages;
+    uint32_t stage_bytes;
+};
+
+// ---- barriers, TMA, tcgen05 ----------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded wait for a phase; false once this wait or another of the block has given up.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *status) {
+    if (bar_try(bar, parity)) return true;
+    const long long start = clock64();
+    for (;;) {
+        if (bar_try(bar, parity)) return true;
+        if (*abort) return false;
+        if (clock64() - start > kWaitCycles) {
+            *abort = 1;
+            report(status, kErrTimeout);
+            return false;
+        }
     }
 }
 
-__global__ void __launch_bounds__(kThreads)
-matmul_mxfp4_simple_kernel(const uint8_t *__restrict__ a, const uint8_t *__restrict__ sa, int64_t rows,
-                           const uint8_t *__restrict__ w, const uint8_t *__restrict__ sw, int E, int F, int K,
-                           const int32_t *__restrict__ off, int64_t cap, uint16_t *__restrict__ y, uint32_t *status) {
-    __shared__ float ta[kTile][33], tw[kTile][33];
-    __shared__ int64_t s_r0, s_r1;
-    __shared__ int s_e;
-    griddep_wait();
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// Shared-memory descriptors: rows of 128 bytes in the 128-byte swizzle (groups
+// of eight rows 1024 bytes apart), and the unswizzled 32 x 16-byte block of
+// scales (groups of eight rows 128 bytes apart).
+__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (8ull << 32) | (1ull << 46);
+}
+
+// Instruction descriptor: E2M1 x E2M1, UE8M0 scales, M = 128, N columns, the
+// scale bytes `id` and id + 1 of each word.
+__device__ __forceinline__ uint32_t instr_desc(int n, uint32_t id) {
+    return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | (1u << 27) | (id << 29);
+}
+
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t r[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ---- the list of tiles -----------------------------------------------------------------------
+
+// Rows [r0, r0 + m) of expert e.  Offsets that run backwards or out of the
+// buffer are clamped and reported.
+__device__ __forceinline__ void expert_rows(const Params &p, int e, int &r0, int &m, bool &bad) {
+    if (p.off == nullptr) {
+        r0 = 0;
+        m = (int)p.rows;
+        return;
+    }
+    const int64_t a = __ldg(p.off + e), b = __ldg(p.off + e + 1);
+    if (a < 0 || b < a) bad = true;
+    if (p.cap > 0) {
+        const int64_t c = b - a;
+        r0 = (int)(e * p.cap);
+        m = (int)(c < 0 ? 0 : c > p.cap ? p.cap : c);
+    } else {
+        if (b > p.rows) bad = true;
+        const int64_t x = a < 0 ? 0 : a > p.rows ? p.rows : a;
+        const int64_t z = b < x ? x : b > p.rows ? p.rows : b;
+        r0 = (int)x;
+        m = (int)(z - x);
+    }
+}
+
+// One tile: features [f0, f0 + 128) of expert e, token rows [row0, row0 + n).
+struct Tiles {
+    const int32_t *first, *row0s, *counts;   // shared: tiles' prefix sums over experts, rows
+    int ftiles, nt;
+    int64_t t, total;
+    int e;
+    int f0, row0, n;
+
+    __device__ __forceinline__ void start(const Params &p, const int32_t *tables) {
+        first = tables;
+        row0s = tables + p.E + 1;
+        counts = row0s + p.E;
+        ftiles = (p.F + kM - 1) / kM;
+        nt = p.nt;
+        total = (int64_t)first[p.E] * ftiles;
+        t = blockIdx.x;
+        e = 0;
+        place();
+    }
+    __device__ __forceinline__ bool valid() const { return t < total; }
+    __device__ __forceinline__ void next() {
+        t += gridDim.x;
+        place();
+    }
+    // Rows of a tile: the expert's, in equal parts of at most nt, rounded up to 16.
+    __device__ __forceinline__ void place() {
+        if (t >= total) return;
+        const int q = (int)(t / ftiles);
+        f0 = (int)(t - (int64_t)q * ftiles) * kM;
+        while (first[e + 1] <= q) ++e;
+        const int m = counts[e], parts = first[e + 1] - first[e];
+        const int per = ((m + parts - 1) / parts + 15) & ~15;
+        const int at = (q - first[e]) * per;
+        row0 = row0s[e] + at;
+        n = m - at < per ? m - at : per;
+    }
+    __device__ __forceinline__ int columns() const { return (n + 15) & ~15; }
+};
+
+// ---- scales ----------------------------------------------------------------------------------
+
+// 32 scale bytes of a row from byte `at` (those behind the row's end zero).
+__device__ __forceinline__ void load_scales(const uint8_t *row, int at, int bytes, bool there, uint32_t v[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0;
+    if (!there) return;
+    if ((bytes & 15) == 0 && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
+        if (at < bytes) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(row + at));
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        }
+        if (at + 16 < bytes) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(row + at + 16));
+            v[4] = a.x, v[5] = a.y, v[6] = a.z, v[7] = a.w;
+        }
+    } else if ((bytes & 3) == 0 && (reinterpret_cast<uintptr_t>(row) & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (at + 4 * i < bytes) v[i] = __ldg(reinterpret_cast<const uint32_t *>(row + at) + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (at + i < bytes) v[i / 4] |= (uint32_t)__ldg(row + at + i) << (8 * (i % 4));
+    }
+}
+
+// ---- the kernel ------------------------------------------------------------------------------
+
+__global__ void __launch_bounds__(kThreads, 1)
+matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t s_tma[kMaxStages], s_sf[kMaxStages], s_empty[kMaxStages], s_accfull[2], s_accfree[2], s_drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort_word;
+    volatile int *abort = &s_abort_word;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
+    int32_t *tables = reinterpret_cast<int32_t *>(ring_ptr + (size_t)p.stages * p.stage_bytes);
+    const uint32_t off_b = kABytes, off_sa = kABytes + p.nbox * kBoxBytes, off_sb = off_sa + 1024;
+
     if (threadIdx.x == 0) {
-        int64_t left = blockIdx.y, r0, r1;
-        bool bad = false;
-        s_e = -1;
-        for (int e = 0; e < E; ++e) {
-            expert_rows(off, e, rows, cap, r0, r1, bad);
-            const int64_t tiles = (r1 - r0 + kTile - 1) / kTile;
-            if (s_e < 0 && left < tiles) {
-                s_e = e;
-                s_r0 = r0 + left * kTile;
-                s_r1 = r1;
-            }
-            left -= tiles;
+        s_abort_word = 0;
+        for (int i = 0; i < p.stages; ++i) {
+            bar_init(smem_u32(&s_tma[i]), 1);
+            bar_init(smem_u32(&s_sf[i]), 1 + p.nb);
+            bar_init(smem_u32(&s_empty[i]), 1);
         }
-        if (bad) report(status, kErrRange);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(smem_u32(&s_accfull[i]), 1);
+            bar_init(smem_u32(&s_accfree[i]), 4);
+        }
+        bar_init(smem_u32(&s_drain), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
     }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    griddep_wait();
+
+    // tables: first[E + 1] (tiles of nt rows before each expert), row0[E], rows[E]
+    bool bad = false;
+    for (int e = threadIdx.x; e < p.E; e += kThreads) {
+        int r0, m;
+        expert_rows(p, e, r0, m, bad);
+        tables[p.E + 1 + e] = r0;
+        tables[2 * p.E + 1 + e] = m;
+    }
+    if (bad && blockIdx.x == 0) report(p.status, kErrRange);
     __syncthreads();
-    const int e = s_e;
-    if (e < 0) return;
-    const int64_t r0 = s_r0, r1 = s_r1;
-    const int f0 = blockIdx.x * kTile;
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    float acc[4][4] = {};
-    const int per_row = K / 8;
-    for (int k0 = 0; k0 < K; k0 += 32) {
-        const int r = threadIdx.x >> 2, c = threadIdx.x & 3;
-        float v[8] = {};
-        if (r0 + r < r1) {
-            cvt_f32x8_e2m1(__ldg(reinterpret_cast<const uint32_t *>(a) + (r0 + r) * per_row + k0 / 8 + c), v);
-            const float s = mx_scale(__ldg(sa + (r0 + r) * (K / 32) + k0 / 32));
-            for (int j = 0; j < 8; ++j) v[j] *= s;
+    if (warp == 0) {
+        const int per = (p.E + 31) / 32, e0 = lane * per, e1 = e0 + per < p.E ? e0 + per : p.E;
+        int sum = 0;
+        for (int e = e0; e < e1; ++e) sum += (tables[2 * p.E + 1 + e] + p.nt - 1) / p.nt;
+        int before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, before, o);
+            if (lane >= o) before += v;
         }
-        for (int j = 0; j < 8; ++j) ta[r][c * 8 + j] = v[j];
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        if (f0 + r < F) {
-            const int64_t row = (int64_t)e * F + f0 + r;
-            cvt_f32x8_e2m1(__ldg(reinterpret_cast<const uint32_t *>(w) + row * per_row + k0 / 8 + c), v);
-            const float s = mx_scale(__ldg(sw + row * (K / 32) + k0 / 32));
-            for (int j = 0; j < 8; ++j) v[j] *= s;
+        before -= sum;
+        for (int e = e0; e < e1; ++e) {
+            tables[e] = before;
+            before += (tables[2 * p.E + 1 + e] + p.nt - 1) / p.nt;
         }
-        for (int j = 0; j < 8; ++j) tw[r][c * 8 + j] = v[j];
-        __syncthreads();
-#pragma unroll 8
-        for (int kk = 0; kk < 32; ++kk) {
-            float x[4], z[4];
-            for (int i = 0; i < 4; ++i) x[i] = ta[ty + 16 * i][kk];
-            for (int i = 0; i < 4; ++i) z[i] = tw[tx + 16 * i][kk];
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], z[j], acc[i][j]);
-        }
-        __syncthreads();
+        if (e0 < p.E && e1 == p.E) tables[p.E] = before;
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + ty + 16 * i;
-            const int f = f0 + tx + 16 * j;
-            if (r < r1 && f < F) y[r * F + f] = (uint16_t)cvt_bf16x2(acc[i][j], 0.0f);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int ksteps = (p.K + kStageK - 1) / kStageK;
+
+    Tiles tile;
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (tile.start(p, tables); ok && tile.valid(); tile.next()) {
+                const int boxes = (tile.columns() + kBoxRows - 1) / kBoxRows;
+                for (int k = 0; k < ksteps; ++k) {
+                    ok = bar_wait(smem_u32(&s_empty[s]), phase ^ 1, abort, p.status);
+                    if (!ok) break;
+                    const uint32_t base = ring + s * p.stage_bytes, bar = smem_u32(&s_tma[s]);
+                    bar_expect(bar, kABytes + boxes * kBoxBytes);
+                    tma_3d(base, &map_w, k * (kStageK / 2), tile.f0, tile.e, bar);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_2d(base + off_b + b * kBoxBytes, &map_a, k * (kStageK / 2), tile.row0 + b * kBoxRows, bar);
+                    if (issued < p.stages) ++issued;
+                    if (++s == p.stages) s = 0, phase ^= 1;
+                }
+            }
+            // the copies still in flight land before the block ends (all have where the MMAs waited for them)
+            for (int i = 0; i < issued; ++i) {
+                if (s == 0) s = p.stages, phase ^= 1;
+                --s;
+                const long long start = clock64();
+                while (!bar_try(smem_u32(&s_tma[s]), phase) && clock64() - start < kWaitCycles) {}
+            }
         }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int s = 0, acc = 0;
+            uint32_t phase = 0, accphase = 0;
+            bool ok = true, any = false;
+            const uint32_t sf_cols = 8 + 8 * p.nb;
+            for (tile.start(p, tables); ok && tile.valid(); tile.next()) {
+                const int n = tile.columns();
+                const int blocks = (n + 127) / 128;
+                const uint32_t i0 = instr_desc(n, 0), i2 = instr_desc(n, 2);
+                ok = bar_wait(smem_u32(&s_accfree[acc]), accphase ^ 1, abort, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tmem + acc * p.nt;
+                for (int k = 0; k < ksteps; ++k) {
+                    ok = bar_wait(smem_u32(&s_sf[s]), phase, abort, p.status) &&
+                         bar_wait(smem_u32(&s_tma[s]), phase, abort, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    any = true;
+                    const uint32_t base = ring + s * p.stage_bytes;
+                    const uint32_t ta = tmem + 2 * p.nt + s * sf_cols, tb = ta + 8;
+                    const int steps = p.K - k * kStageK < kStageK ? (p.K - k * kStageK + 63) / 64 : 4;
+                    for (int w = 0; w < 2; ++w) {
+                        scales_to_tmem(ta + 4 * w, desc_scales(base + off_sa + 512 * w));
+                        for (int b = 0; b < blocks; ++b)
+                            scales_to_tmem(tb + 4 * (w * p.nb + b), desc_scales(base + off_sb + 512 * (w * p.nb + b)));
+                    }
+                    for (int i = 0; i < steps; ++i)
+                        mma_mxf4(d, desc_rows(base + 32 * i), desc_rows(base + off_b + 32 * i), (i & 1) ? i2 : i0,
+                                 ta + 4 * (i >> 1), tb + 4 * (i >> 1) * p.nb, (k | i) != 0);
+                    mma_commit(smem_u32(&s_empty[s]));
+                    if (++s == p.stages) s = 0, phase ^= 1;
+                }
+                if (!ok) break;
+                mma_commit(smem_u32(&s_accfull[acc]));
+                acc ^= 1;
+                if (acc == 0) accphase ^= 1;
+            }
+            if (any) {   // every MMA has ended before TMEM is freed
+                mma_commit(smem_u32(&s_drain));
+                const long long start = clock64();
+                while (!bar_try(smem_u32(&s_drain), 0) && clock64() - start < kWaitCycles) {}
+            }
+        }
+    } else if (warp == 2 || warp == 3 || warp == 8) {
+        const bool weights = warp == 2;
+        const int block = warp == 8 ? 1 : 0;   // 128-row block of the token side
+        if (weights || block < p.nb) {
+            const int row_bytes = p.K / 32, chunks = (ksteps + 3) / 4;
+            int s = 0, chunk = 0;
+            uint32_t phase = 0;
+            uint32_t v[4][8], nv[4][8];
+            const auto load = [&](const Tiles &t, int c, uint32_t (&to)[4][8]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = (weights ? 0 : block * 128) + i * 32 + lane;
+                    const uint8_t *row;
+                    bool there;
+                    if (weights) {
+                        there = t.f0 + r < p.F;
+                        row = p.sw + ((int64_t)t.e * p.F + t.f0 + r) * row_bytes;
+                    } else {
+                        there = r < t.n;
+                        row = p.sa + ((int64_t)t.row0 + r) * row_bytes;
+                    }
+                    load_scales(row, c * 32, row_bytes, there, to[i]);
+                }
+            };
+            bool ok = true;
+            tile.start(p, tables);
+            if (tile.valid()) load(tile, 0, v);
+            while (ok && tile.valid()) {
+                Tiles ahead = tile;
+                int ahead_chunk = chunk + 1;
+                if (ahead_chunk == chunks) {
+                    ahead_chunk = 0;
+                    ahead.next();
+                }
+                if (ahead.valid()) load(ahead, ahead_chunk, nv);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (ok && chunk * 4 + j < ksteps) {
+                        ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_empty[s]), phase ^ 1, abort, p.status));
+                        if (ok) {
+                            uint8_t *to = ring_ptr + (size_t)s * p.stage_bytes + (weights ? off_sa : off_sb + 512 * block) + lane * 16;
+                            const int step = 512 * (weights ? 1 : p.nb);
+                            *reinterpret_cast<uint4 *>(to) = make_uint4(v[0][2 * j], v[1][2 * j], v[2][2 * j], v[3][2 * j]);
+                            *reinterpret_cast<uint4 *>(to + step) =
+                                make_uint4(v[0][2 * j + 1], v[1][2 * j + 1], v[2][2 * j + 1], v[3][2 * j + 1]);
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) bar_arrive(smem_u32(&s_sf[s]));
+                            if (++s == p.stages) s = 0, phase ^= 1;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][j] = nv[i][j];
+                tile = ahead;
+                chunk = ahead_chunk;
+            }
+        }
+    } else {
+        const int quarter = warp & 3;
+        int acc = 0;
+        uint32_t accphase = 0;
+        for (tile.start(p, tables); tile.valid(); tile.next()) {
+            if (!__all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_accfull[acc]), accphase, abort, p.status))) break;
+            tc_fence_after();
+            const int f = tile.f0 + quarter * 32 + lane;
+            const uint32_t d = tmem + acc * p.nt + ((uint32_t)(quarter * 32) << 16);
+            const int columns = tile.columns();
+            for (int c = 0; c < columns; c += 16) {
+                uint32_t r[16];
+                __syncwarp();
+                tmem_ld16(d + c, r);
+                tmem_ld_wait();
+                if (f < p.F) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c + j < tile.n)
+                            p.y[((int64_t)tile.row0 + c + j) * p.F + f] = (uint16_t)cvt_bf16x2(__uint_as_float(r[j]), 0.0f);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(smem_u32(&s_accfree[acc]));
+            acc ^= 1;
+            if (acc == 0) accphase ^= 1;
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
+
+// Rows of codes as bytes: [planes][rows][row_bytes], boxes of 128 bytes x box_rows, zeros outside.
+bool make_map(CUtensorMap *map, const void *p, int64_t row_bytes, int64_t rows, int64_t planes, int box_rows) {
+    const cuuint64_t dims[3] = {(cuuint64_t)row_bytes, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)(row_bytes * rows)};
+    const cuuint32_t box[3] = {kStageK / 2, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+    const EncodeTiled fn = encode_tiled();
+    return fn != nullptr && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, planes > 0 ? 3 : 2, const_cast<void *>(p), dims, strides, box,
+                               step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -105,13 +514,35 @@ matmul_mxfp4_simple_kernel(const uint8_t *__restrict__ a, const uint8_t *__restr
 cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows, const uint8_t *w, const uint8_t *sw,
                                int E, int F, int K, const int32_t *off, int64_t cap, uint16_t *y, int num_sms,
                                uint32_t *status, cudaStream_t stream) {
-    (void)num_sms;
     if (rows == 0) return CGL_OK;
-    const int64_t tiles = rows / kTile + E;
-    if (tiles > 65535) return CGL_EINVAL;
-    const dim3 grid((F + kTile - 1) / kTile, (unsigned)tiles);
-    return launch_pdl(matmul_mxfp4_simple_kernel, grid, dim3(kThreads), 0, stream, a, sa, rows, w, sw, E, F, K, off, cap,
-                      y, status) == cudaSuccess ? CGL_OK : CGL_ECUDA;
+    Params p = {};
+    p.sa = sa, p.sw = sw, p.off = off, p.y = y, p.status = status;
+    p.rows = rows, p.cap = cap, p.E = E, p.F = F, p.K = K;
+    // Columns a tile: twice the mean rows of an expert (a padded one's capacity), so that few experts need two tiles.
+    const int64_t want = cap > 0 ? cap : 2 * ((rows + E - 1) / E);
+    p.nt = want >= kMaxNt ? kMaxNt : want <= 32 ? 32 : (int)((want + 15) / 16 * 16);
+    p.nb = p.nt > 128 ? 2 : 1;
+    p.nbox = (p.nt + kBoxRows - 1) / kBoxRows;
+    p.stage_bytes = kABytes + p.nbox * kBoxBytes + 1024 + 1024 * p.nb;
+    const size_t tables = (size_t)(3 * E + 1) * 4;
+    int stages = (int)((kSmemLimit - 1024 - tables) / p.stage_bytes);
+    const int by_tmem = (512 - 2 * p.nt) / (8 + 8 * p.nb);
+    if (stages > by_tmem) stages = by_tmem;
+    if (stages > kMaxStages) stages = kMaxStages;
+    p.stages = stages;
+    const size_t smem = 1024 + (size_t)stages * p.stage_bytes + tables;
+
+    CUtensorMap map_a, map_w;
+    if (!make_map(&map_a, a, K / 2, rows, 0, kBoxRows) || !make_map(&map_w, w, K / 2, F, E, kM)) return CGL_ECUDA;
+    if (!ensure_smem_attr((const void *)matmul_mxfp4_kernel, smem)) return CGL_ECUDA;
+    const int sms = device_sm_count();
+    if (sms <= 0) return CGL_ECUDA;
+    const int64_t ftiles = (F + kM - 1) / kM;
+    const int64_t most = ((rows + p.nt - 1) / p.nt + (rows < E ? rows : E)) * ftiles;   // tiles there can be
+    int64_t grid = num_sms > 0 && num_sms < sms ? num_sms : sms;
+    if (grid > most) grid = most;
+    return launch_pdl(matmul_mxfp4_kernel, dim3((unsigned)grid), dim3(kThreads), smem, stream, map_a, map_w, p) == cudaSuccess
+               ? CGL_OK : CGL_ECUDA;
 }
 
 }  // namespace cgl
