@@ -94,6 +94,16 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     }
 }
 
+// One lane of a converged warp, always the same.  What the elected lane issues
+// takes its operands from uniform registers: inside `if (lane == 0)` the
+// compiler makes them uniform one by one, 1300 cycles a stage where the elected
+// lane needs (see the kernel's comment) a tenth of that.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
@@ -313,76 +323,82 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
 
     Tiles tile;
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0, issued = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (tile.start(p, tables); ok && tile.valid(); tile.next()) {
-                const int boxes = (tile.columns() + kBoxRows - 1) / kBoxRows;
-                for (int k = 0; k < ksteps; ++k) {
-                    ok = bar_wait(smem_u32(&s_empty[s]), phase ^ 1, abort, p.status);
-                    if (!ok) break;
+        int s = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (tile.start(p, tables); ok && tile.valid(); tile.next()) {
+            const int boxes = (tile.columns() + kBoxRows - 1) / kBoxRows;
+            for (int k = 0; k < ksteps; ++k) {
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_empty[s]), phase ^ 1, abort, p.status));
+                if (!ok) break;
+                if (elect_one()) {
                     const uint32_t base = ring + s * p.stage_bytes, bar = smem_u32(&s_tma[s]);
                     bar_expect(bar, kABytes + boxes * kBoxBytes);
                     tma_3d(base, &map_w, k * (kStageK / 2), tile.f0, tile.e, bar);
                     for (int b = 0; b < boxes; ++b)
                         tma_2d(base + off_b + b * kBoxBytes, &map_a, k * (kStageK / 2), tile.row0 + b * kBoxRows, bar);
-                    if (issued < p.stages) ++issued;
-                    if (++s == p.stages) s = 0, phase ^= 1;
                 }
-            }
-            // the copies still in flight land before the block ends (all have where the MMAs waited for them)
-            for (int i = 0; i < issued; ++i) {
-                if (s == 0) s = p.stages, phase ^= 1;
-                --s;
-                const long long start = clock64();
-                while (!bar_try(smem_u32(&s_tma[s]), phase) && clock64() - start < kWaitCycles) {}
+                __syncwarp();
+                if (issued < p.stages) ++issued;
+                if (++s == p.stages) s = 0, phase ^= 1;
             }
         }
+        // the copies still in flight land before the block ends (all have where the MMAs waited for them)
+        for (int i = 0; i < issued; ++i) {
+            if (s == 0) s = p.stages, phase ^= 1;
+            --s;
+            const long long start = clock64();
+            while (!bar_try(smem_u32(&s_tma[s]), phase) && clock64() - start < kWaitCycles) {}
+        }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int s = 0, acc = 0;
-            uint32_t phase = 0, accphase = 0;
-            bool ok = true, any = false;
-            const uint32_t sf_cols = 8 + 8 * p.nb;
-            for (tile.start(p, tables); ok && tile.valid(); tile.next()) {
-                const int n = tile.columns();
-                const int blocks = (n + 127) / 128;
-                const uint32_t i0 = instr_desc(n, 0), i2 = instr_desc(n, 2);
-                ok = bar_wait(smem_u32(&s_accfree[acc]), accphase ^ 1, abort, p.status);
+        int s = 0, acc = 0;
+        uint32_t phase = 0, accphase = 0;
+        bool ok = true, any = false;
+        const uint32_t sf_cols = 8 + 8 * p.nb;
+        for (tile.start(p, tables); ok && tile.valid(); tile.next()) {
+            const int n = tile.columns();
+            const bool two = n > 128;
+            const uint32_t i0 = instr_desc(n, 0), i2 = instr_desc(n, 2);
+            ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_accfree[acc]), accphase ^ 1, abort, p.status));
+            if (!ok) break;
+            const uint32_t d = tmem + acc * p.nt;
+            for (int k = 0; k < ksteps; ++k) {
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_sf[s]), phase, abort, p.status) &&
+                                                 bar_wait(smem_u32(&s_tma[s]), phase, abort, p.status));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t d = tmem + acc * p.nt;
-                for (int k = 0; k < ksteps; ++k) {
-                    ok = bar_wait(smem_u32(&s_sf[s]), phase, abort, p.status) &&
-                         bar_wait(smem_u32(&s_tma[s]), phase, abort, p.status);
-                    if (!ok) break;
-                    tc_fence_after();
-                    any = true;
-                    const uint32_t base = ring + s * p.stage_bytes;
-                    const uint32_t ta = tmem + 2 * p.nt + s * sf_cols, tb = ta + 8;
-                    const int steps = p.K - k * kStageK < kStageK ? (p.K - k * kStageK + 63) / 64 : 4;
-                    for (int w = 0; w < 2; ++w) {
-                        scales_to_tmem(ta + 4 * w, desc_scales(base + off_sa + 512 * w));
-                        for (int b = 0; b < blocks; ++b)
-                            scales_to_tmem(tb + 4 * (w * p.nb + b), desc_scales(base + off_sb + 512 * (w * p.nb + b)));
+                any = true;
+                const uint32_t base = ring + s * p.stage_bytes;
+                const uint32_t ta = tmem + 2 * p.nt + s * sf_cols, tb = ta + 8;
+                const int left = p.K - k * kStageK;
+                if (elect_one()) {
+                    const uint64_t sa = desc_scales(base + off_sa), sb = desc_scales(base + off_sb);
+                    const uint64_t da = desc_rows(base), db = desc_rows(base + off_b);
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {   // 512 bytes (32 descriptor units) a block
+                        scales_to_tmem(ta + 4 * w, sa + 32 * w);
+                        scales_to_tmem(tb + 4 * w * p.nb, sb + 32 * w * p.nb);
+                        if (two) scales_to_tmem(tb + 4 * (w * p.nb + 1), sb + 32 * (w * p.nb + 1));
                     }
-                    for (int i = 0; i < steps; ++i)
-                        mma_mxf4(d, desc_rows(base + 32 * i), desc_rows(base + off_b + 32 * i), (i & 1) ? i2 : i0,
-                                 ta + 4 * (i >> 1), tb + 4 * (i >> 1) * p.nb, (k | i) != 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)     // 64 values: 32 bytes (two units) of each row
+                        if (left > 64 * i)
+                            mma_mxf4(d, da + 2 * i, db + 2 * i, (i & 1) ? i2 : i0, ta + 4 * (i >> 1),
+                                     tb + 4 * (i >> 1) * p.nb, (k | i) != 0);
                     mma_commit(smem_u32(&s_empty[s]));
-                    if (++s == p.stages) s = 0, phase ^= 1;
+                    if (left <= kStageK) mma_commit(smem_u32(&s_accfull[acc]));
                 }
-                if (!ok) break;
-                mma_commit(smem_u32(&s_accfull[acc]));
-                acc ^= 1;
-                if (acc == 0) accphase ^= 1;
+                __syncwarp();
+                if (++s == p.stages) s = 0, phase ^= 1;
             }
-            if (any) {   // every MMA has ended before TMEM is freed
-                mma_commit(smem_u32(&s_drain));
-                const long long start = clock64();
-                while (!bar_try(smem_u32(&s_drain), 0) && clock64() - start < kWaitCycles) {}
-            }
+            acc ^= 1;
+            if (acc == 0) accphase ^= 1;
+        }
+        if (any) {   // every MMA has ended before TMEM is freed
+            if (elect_one()) mma_commit(smem_u32(&s_drain));
+            __syncwarp();
+            const long long start = clock64();
+            while (!bar_try(smem_u32(&s_drain), 0) && clock64() - start < kWaitCycles) {}
         }
     } else if (warp == 2 || warp == 3 || warp == 8) {
         const bool weights = warp == 2;
@@ -408,15 +424,34 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                     load_scales(row, c * 32, row_bytes, there, to[i]);
                 }
             };
+            // the weights' scales of a tile lie in one piece: asked into L2 a tile
+            // ahead, since a load that has to queue behind the ring's own copies
+            // comes too late (one chunk in flight a warp)
+            const auto to_l2 = [&](const Tiles &t) {
+                if (!weights || lane != 0 || !t.valid()) return;
+                const int there = p.F - t.f0 < kM ? p.F - t.f0 : kM;
+                const uintptr_t a = reinterpret_cast<uintptr_t>(p.sw + ((int64_t)t.e * p.F + t.f0) * row_bytes);
+                const uintptr_t a0 = (a + 15) & ~(uintptr_t)15, a1 = (a + (int64_t)there * row_bytes) & ~(uintptr_t)15;
+                if (a1 > a0) prefetch_l2_bulk(reinterpret_cast<const void *>(a0), (uint32_t)(a1 - a0));
+            };
             bool ok = true;
             tile.start(p, tables);
-            if (tile.valid()) load(tile, 0, v);
+            to_l2(tile);
+            if (tile.valid()) {
+                Tiles second = tile;
+                second.next();
+                to_l2(second);
+                load(tile, 0, v);
+            }
             while (ok && tile.valid()) {
                 Tiles ahead = tile;
                 int ahead_chunk = chunk + 1;
                 if (ahead_chunk == chunks) {
                     ahead_chunk = 0;
                     ahead.next();
+                    Tiles after = ahead;
+                    after.next();
+                    to_l2(after);
                 }
                 if (ahead.valid()) load(ahead, ahead_chunk, nv);
 #pragma unroll
