@@ -2,17 +2,24 @@
 // binary32, BF16 out (format in mxfp4.cuh).
 //
 // Tensor cores: tcgen05.mma kind::mxf4 with block scales (32 values a scale,
-// 64 values an instruction).  The weights are the M side (128 output features a
-// tile) and the tokens the N side, whose width goes by the expert's rows, 16 at
-// a time: few rows cost few columns, and each weight tile is read once for up
-// to `nt` rows.  Persistent blocks, one per SM, walk the list of (expert, rows,
-// features) tiles; each block makes the list's prefix sums from expert_offset
-// for itself.  One block:
+// 64 values an instruction), cta_group::2: a pair of blocks on neighbouring SMs
+// works on one tile of 256 output features.  The weights are the M side, 128
+// features in each block; the tokens are the N side, half of the tile's rows in
+// each block's shared memory, whose width goes by the expert's rows, 16 at a
+// time: few rows cost few columns, and each weight tile is read once for up to
+// `nt` rows.  Persistent pairs walk the list of (expert, rows, features) tiles;
+// each block makes the list's prefix sums from expert_offset for itself.
+// One block:
 //   warp 0      TMA: a ring of stages of 256 values (128 bytes) a row, 128-byte swizzle
-//   warp 1      TMEM, and the MMA thread: scales smem -> TMEM (tcgen05.cp), 4 MMAs a stage
+//   warp 1      TMEM; in the pair's first block the MMA thread: scales smem -> TMEM
+//               (tcgen05.cp), 4 MMAs a stage
 //   warp 2      the weights' scales, 3 and 8 the tokens': global rows -> the 512-byte
 //               blocks that tcgen05.cp wants (row r's word at (r % 32) * 16 + (r / 32) * 4)
-//   warps 4-7   TMEM -> registers -> BF16 rows, while the next tile's MMAs run
+//   warps 4-7   TMEM -> registers -> transposed through shared memory -> BF16 rows,
+//               while the next tile's MMAs run
+// Why pairs: one block alone (128 x 208) moves 45 KB a stage into shared memory and
+// reads them out again in 700 cycles of its 128 bytes a cycle, where the MMAs need
+// 416; a pair holds half the tokens' rows each.
 // Scales stay in their rows in memory, [rows, in / 32], because a tile starts at
 // any row of the receive buffer; a warp reads 32 bytes of each row, four stages'
 // worth, one such chunk ahead.
@@ -33,9 +40,10 @@ constexpr long long kWaitCycles = 1ll << 31;
 constexpr int kThreads = 288;
 constexpr int kStageK = 256;              // values a stage
 constexpr int kM = 128;                   // features a tile
-constexpr int kBoxRows = 32;              // token rows a TMA box
-constexpr int kMaxStages = 10;
-constexpr int kMaxNt = 208;               // 2 accumulators of 208 columns + 4 stages of scales = 512 columns
+constexpr int kBoxRows = 16;              // token rows a TMA box
+constexpr int kMaxStages = 12;
+constexpr int kMaxNt = 208;               // 2 accumulators of 208 columns + 4 slots of scales = 512 columns
+constexpr int kOutBytes = 4 * 2048;       // the epilogue's 32 x 32 BF16 blocks, one a warp
 constexpr size_t kSmemLimit = 226 * 1024; // dynamic part: 227 KiB less the static part
 constexpr uint32_t kABytes = kM * kStageK / 2;
 constexpr uint32_t kBoxBytes = kBoxRows * kStageK / 2;
@@ -47,10 +55,12 @@ struct Params {
     uint32_t *status;
     int64_t rows, cap;
     int E, F, K;
-    int nt;          // most token columns a tile
+    int nt;          // most token columns a tile (of the pair)
     int nb;          // 128-row scale blocks of the token side (1 or 2)
     int nbox;        // TMA boxes of the token side a stage has room for
     int stages;
+    int slots;       // TMEM slots for a stage's scales
+    int wide;        // y's rows allow 16-byte stores
     uint32_t stage_bytes;
 };
 
@@ -61,9 +71,6 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)_
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -72,6 +79,33 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     asm volatile(
         "{\n.reg .pred p;\n"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// The same barrier in the pair's first block.
+__device__ __forceinline__ uint32_t in_first(uint32_t bar) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
+    return r;
+}
+// Arrive there.  What the arrival announces is read by the tensor core of the
+// arriving block's own SM (its shared memory, after a proxy fence) or was read
+// from its own TMEM, so the release need not reach past the block: at cluster
+// scope each arrival took 1000 cycles of its warp.
+__device__ __forceinline__ void bar_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Whether a phase has ended, without waiting.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         "selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -104,15 +138,16 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// Tile loads into this block; the barrier may be the first block's.
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
@@ -127,37 +162,61 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
     return (uint64_t)((addr >> 4) & 0x3FFFu) | (8ull << 32) | (1ull << 46);
 }
 
-// Instruction descriptor: E2M1 x E2M1, UE8M0 scales, M = 128, N columns, the
+// Instruction descriptor: E2M1 x E2M1, UE8M0 scales, M = 256, N columns, the
 // scale bytes `id` and id + 1 of each word.
 __device__ __forceinline__ uint32_t instr_desc(int n, uint32_t id) {
-    return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | (1u << 27) | (id << 29);
+    return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | (1u << 28) | (id << 29);
 }
 
 __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                          uint32_t accumulate) {
     asm volatile(
         "{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
 __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Arrive, once this thread's MMAs and copies so far have ended, at a barrier of both blocks or of this one.
+__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t r[16]) {
+// 16 lanes x 32 columns: of each eight columns, r[0], r[1] are row lane / 4 and
+// columns 2 (lane % 4) and the next, r[2], r[3] the same of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t r[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Four 8 x 8 blocks of 16-bit values, transposed: lane i gives the address of row i % 8 of block i / 8.
+__device__ __forceinline__ void stmatrix_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // ---- the list of tiles -----------------------------------------------------------------------
 
@@ -184,10 +243,11 @@ __device__ __forceinline__ void expert_rows(const Params &p, int e, int &r0, int
     }
 }
 
-// One tile: features [f0, f0 + 128) of expert e, token rows [row0, row0 + n).
+// One tile: features [f0, f0 + 128) of expert e in this block (the pair's 256
+// side by side; f0 may be past the last one), token rows [row0, row0 + n).
 struct Tiles {
     const int32_t *first, *row0s, *counts;   // shared: tiles' prefix sums over experts, rows
-    int ftiles, nt;
+    int ftiles, rank;
     int64_t t, total;
     int e;
     int f0, row0, n;
@@ -196,23 +256,23 @@ struct Tiles {
         first = tables;
         row0s = tables + p.E + 1;
         counts = row0s + p.E;
-        ftiles = (p.F + kM - 1) / kM;
-        nt = p.nt;
+        ftiles = (p.F + 2 * kM - 1) / (2 * kM);
+        rank = (int)(blockIdx.x & 1);
         total = (int64_t)first[p.E] * ftiles;
-        t = blockIdx.x;
+        t = blockIdx.x >> 1;
         e = 0;
         place();
     }
     __device__ __forceinline__ bool valid() const { return t < total; }
     __device__ __forceinline__ void next() {
-        t += gridDim.x;
+        t += gridDim.x >> 1;
         place();
     }
     // Rows of a tile: the expert's, in equal parts of at most nt, rounded up to 16.
     __device__ __forceinline__ void place() {
         if (t >= total) return;
         const int q = (int)(t / ftiles);
-        f0 = (int)(t - (int64_t)q * ftiles) * kM;
+        f0 = ((int)(t - (int64_t)q * ftiles) * 2 + rank) * kM;
         while (first[e + 1] <= q) ++e;
         const int m = counts[e], parts = first[e + 1] - first[e];
         const int per = ((m + parts - 1) / parts + 15) & ~15;
@@ -252,30 +312,33 @@ __device__ __forceinline__ void load_scales(const uint8_t *row, int at, int byte
 
 // ---- the kernel ------------------------------------------------------------------------------
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const Params p) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t s_tma[kMaxStages], s_sf[kMaxStages], s_empty[kMaxStages], s_accfull[2], s_accfree[2], s_drain;
+    // full and accfree count for the pair, in its first block; empty and accfull are told to both
+    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_accfull[2], s_accfree[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort_word;
     volatile int *abort = &s_abort_word;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool first = cluster_rank() == 0;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
-    int32_t *tables = reinterpret_cast<int32_t *>(ring_ptr + (size_t)p.stages * p.stage_bytes);
+    const uint32_t out = ring + p.stages * p.stage_bytes;
+    uint8_t *out_ptr = ring_ptr + (size_t)p.stages * p.stage_bytes;
+    int32_t *tables = reinterpret_cast<int32_t *>(out_ptr + kOutBytes);
     const uint32_t off_b = kABytes, off_sa = kABytes + p.nbox * kBoxBytes, off_sb = off_sa + 1024;
 
     if (threadIdx.x == 0) {
         s_abort_word = 0;
         for (int i = 0; i < p.stages; ++i) {
-            bar_init(smem_u32(&s_tma[i]), 1);
-            bar_init(smem_u32(&s_sf[i]), 1 + p.nb);
+            bar_init(smem_u32(&s_full[i]), 1 + 2 * (1 + p.nb));   // the bytes' announcement, both blocks' scale warps
             bar_init(smem_u32(&s_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_u32(&s_accfull[i]), 1);
-            bar_init(smem_u32(&s_accfree[i]), 4);
+            bar_init(smem_u32(&s_accfree[i]), 8);   // the epilogue warps of both blocks
         }
         bar_init(smem_u32(&s_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -283,8 +346,8 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     griddep_wait();
 
@@ -315,45 +378,45 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         }
         if (e0 < p.E && e1 == p.E) tables[p.E] = before;
     }
+    __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     const int ksteps = (p.K + kStageK - 1) / kStageK;
 
     Tiles tile;
     if (warp == 0) {
-        int s = 0, issued = 0;
+        int s = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (tile.start(p, tables); ok && tile.valid(); tile.next()) {
-            const int boxes = (tile.columns() + kBoxRows - 1) / kBoxRows;
+            const int half = tile.columns() / 2, boxes = (half + kBoxRows - 1) / kBoxRows;
+            const int row0 = tile.row0 + tile.rank * half;
             for (int k = 0; k < ksteps; ++k) {
                 ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_empty[s]), phase ^ 1, abort, p.status));
                 if (!ok) break;
                 if (elect_one()) {
-                    const uint32_t base = ring + s * p.stage_bytes, bar = smem_u32(&s_tma[s]);
-                    bar_expect(bar, kABytes + boxes * kBoxBytes);
+                    const uint32_t base = ring + s * p.stage_bytes, bar = in_first(smem_u32(&s_full[s]));
+                    if (first) bar_expect(smem_u32(&s_full[s]), 2 * (kABytes + boxes * kBoxBytes));
                     tma_3d(base, &map_w, k * (kStageK / 2), tile.f0, tile.e, bar);
                     for (int b = 0; b < boxes; ++b)
-                        tma_2d(base + off_b + b * kBoxBytes, &map_a, k * (kStageK / 2), tile.row0 + b * kBoxRows, bar);
+                        tma_2d(base + off_b + b * kBoxBytes, &map_a, k * (kStageK / 2), row0 + b * kBoxRows, bar);
                 }
                 __syncwarp();
-                if (issued < p.stages) ++issued;
                 if (++s == p.stages) s = 0, phase ^= 1;
             }
         }
-        // the copies still in flight land before the block ends (all have where the MMAs waited for them)
-        for (int i = 0; i < issued; ++i) {
-            if (s == 0) s = p.stages, phase ^= 1;
-            --s;
-            const long long start = clock64();
-            while (!bar_try(smem_u32(&s_tma[s]), phase) && clock64() - start < kWaitCycles) {}
-        }
-    } else if (warp == 1) {
-        int s = 0, acc = 0;
-        uint32_t phase = 0, accphase = 0;
-        bool ok = true, any = false;
+        // Without an error the MMA warp has waited for every copy.  With one, those
+        // in flight (issued at most a stage ring ago) get 2^28 cycles to land.
+        if (!ok)
+            for (const long long start = clock64(); clock64() - start < (1ll << 28);) {}
+    } else if (warp == 1 && first) {
+        // A stage's scales go to one of `slots` places in TMEM; the MMAs that read
+        // the place before have ended once the stage they belonged to is free.
+        int s = 0, acc = 0, slot = 0, behind = 0, s_behind = 0;
+        uint32_t phase = 0, accphase = 0, phase_behind = 0;
+        bool ok = true, any = false, ready = false;
         const uint32_t sf_cols = 8 + 8 * p.nb;
         for (tile.start(p, tables); ok && tile.valid(); tile.next()) {
             const int n = tile.columns();
@@ -363,13 +426,23 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             if (!ok) break;
             const uint32_t d = tmem + acc * p.nt;
             for (int k = 0; k < ksteps; ++k) {
-                ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_sf[s]), phase, abort, p.status) &&
-                                                 bar_wait(smem_u32(&s_tma[s]), phase, abort, p.status));
-                if (!ok) break;
+                if (!ready) ok = bar_wait(smem_u32(&s_full[s]), phase, abort, p.status);
+                if (behind < p.slots) {
+                    ++behind;
+                } else if (p.slots < p.stages) {
+                    ok = ok && bar_wait(smem_u32(&s_empty[s_behind]), phase_behind, abort, p.status);
+                    if (++s_behind == p.stages) s_behind = 0, phase_behind ^= 1;
+                }
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 any = true;
-                const uint32_t base = ring + s * p.stage_bytes;
-                const uint32_t ta = tmem + 2 * p.nt + s * sf_cols, tb = ta + 8;
+                const uint32_t base = ring + s * p.stage_bytes, empty = smem_u32(&s_empty[s]);
+                if (++s == p.stages) s = 0, phase ^= 1;
+                ready = bar_test(smem_u32(&s_full[s]), phase);   // the next stage, asked while this one is issued
+                const uint32_t ta = tmem + 2 * p.nt + slot * sf_cols, tb = ta + 8;
                 const int left = p.K - k * kStageK;
                 if (elect_one()) {
                     const uint64_t sa = desc_scales(base + off_sa), sb = desc_scales(base + off_sb);
@@ -385,11 +458,11 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                         if (left > 64 * i)
                             mma_mxf4(d, da + 2 * i, db + 2 * i, (i & 1) ? i2 : i0, ta + 4 * (i >> 1),
                                      tb + 4 * (i >> 1) * p.nb, (k | i) != 0);
-                    mma_commit(smem_u32(&s_empty[s]));
-                    if (left <= kStageK) mma_commit(smem_u32(&s_accfull[acc]));
+                    mma_commit_both(empty);
+                    if (left <= kStageK) mma_commit_both(smem_u32(&s_accfull[acc]));
                 }
                 __syncwarp();
-                if (++s == p.stages) s = 0, phase ^= 1;
+                if (++slot == p.slots) slot = 0;
             }
             acc ^= 1;
             if (acc == 0) accphase ^= 1;
@@ -430,6 +503,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             const auto to_l2 = [&](const Tiles &t) {
                 if (!weights || lane != 0 || !t.valid()) return;
                 const int there = p.F - t.f0 < kM ? p.F - t.f0 : kM;
+                if (there <= 0) return;
                 const uintptr_t a = reinterpret_cast<uintptr_t>(p.sw + ((int64_t)t.e * p.F + t.f0) * row_bytes);
                 const uintptr_t a0 = (a + 15) & ~(uintptr_t)15, a1 = (a + (int64_t)there * row_bytes) & ~(uintptr_t)15;
                 if (a1 > a0) prefetch_l2_bulk(reinterpret_cast<const void *>(a0), (uint32_t)(a1 - a0));
@@ -466,7 +540,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                                 make_uint4(v[0][2 * j + 1], v[1][2 * j + 1], v[2][2 * j + 1], v[3][2 * j + 1]);
                             fence_proxy_async();
                             __syncwarp();
-                            if (lane == 0) bar_arrive(smem_u32(&s_sf[s]));
+                            if (lane == 0) bar_arrive_remote(in_first(smem_u32(&s_full[s])));
                             if (++s == p.stages) s = 0, phase ^= 1;
                         }
                     }
@@ -479,42 +553,70 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 chunk = ahead_chunk;
             }
         }
-    } else {
+    } else if (warp >= 4) {
         const int quarter = warp & 3;
+        const uint32_t mine = out + quarter * 2048;
+        const uint8_t *mine_ptr = out_ptr + quarter * 2048;
         int acc = 0;
         uint32_t accphase = 0;
         for (tile.start(p, tables); tile.valid(); tile.next()) {
             if (!__all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_accfull[acc]), accphase, abort, p.status))) break;
             tc_fence_after();
-            const int f = tile.f0 + quarter * 32 + lane;
+            const int f = tile.f0 + quarter * 32;
             const uint32_t d = tmem + acc * p.nt + ((uint32_t)(quarter * 32) << 16);
             const int columns = tile.columns();
-            for (int c = 0; c < columns; c += 16) {
-                uint32_t r[16];
-                __syncwarp();
-                tmem_ld16(d + c, r);
+            for (int c = 0; c < columns; c += 32) {
+                // 32 features x 32 tokens -> [token][feature], 64 bytes a token, its
+                // 16-byte pieces exchanged by the token's number so that neither side
+                // meets a bank twice
+                uint32_t r[2][16];
+                tmem_ld_16x32(d + c, r[0]);
+                tmem_ld_16x32(d + c + (16u << 16), r[1]);
                 tmem_ld_wait();
-                if (f < p.F) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c + j < tile.n)
-                            p.y[((int64_t)tile.row0 + c + j) * p.F + f] = (uint16_t)cvt_bf16x2(__uint_as_float(r[j]), 0.0f);
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int u = 0; u < 4; u += 2) {
+                        const int token = 8 * (u + (lane >> 4)) + (lane & 7), piece = 2 * h + ((lane >> 3) & 1);
+                        uint32_t b[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            b[i] = cvt_bf16x2(__uint_as_float(r[h][4 * u + 2 * i]), __uint_as_float(r[h][4 * u + 2 * i + 1]));
+                        stmatrix_trans(mine + token * 64 + ((piece ^ ((token >> 1) & 3)) << 4), b[0], b[1], b[2], b[3]);
+                    }
+                __syncwarp();
+                const int there = tile.n - c < 32 ? tile.n - c : 32;
+                uint16_t *y = p.y + ((int64_t)tile.row0 + c) * p.F + f;
+                if (p.wide) {
+                    const int piece = lane & 3;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int token = 8 * i + (lane >> 2);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(mine_ptr + token * 64 + ((piece ^ ((token >> 1) & 3)) << 4));
+                        if (token < there && f + 8 * piece < p.F) *reinterpret_cast<uint4 *>(y + (int64_t)token * p.F + 8 * piece) = v;
+                    }
+                } else if (f + lane < p.F) {
+                    for (int token = 0; token < there; ++token)
+                        y[(int64_t)token * p.F + lane] = *reinterpret_cast<const uint16_t *>(
+                            mine_ptr + token * 64 + (((lane >> 3) ^ ((token >> 1) & 3)) << 4) + 2 * (lane & 7));
                 }
+                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(smem_u32(&s_accfree[acc]));
+            if (lane == 0) bar_arrive_remote(in_first(smem_u32(&s_accfree[acc])));
             acc ^= 1;
             if (acc == 0) accphase ^= 1;
         }
     }
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();   // the pair's memory and barriers stay until both are done
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
+    cluster_sync();   // neither block leaves while the other frees its half
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -557,26 +659,28 @@ cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows
     const int64_t want = cap > 0 ? cap : 2 * ((rows + E - 1) / E);
     p.nt = want >= kMaxNt ? kMaxNt : want <= 32 ? 32 : (int)((want + 15) / 16 * 16);
     p.nb = p.nt > 128 ? 2 : 1;
-    p.nbox = (p.nt + kBoxRows - 1) / kBoxRows;
+    p.nbox = (p.nt / 2 + kBoxRows - 1) / kBoxRows;
     p.stage_bytes = kABytes + p.nbox * kBoxBytes + 1024 + 1024 * p.nb;
     const size_t tables = (size_t)(3 * E + 1) * 4;
-    int stages = (int)((kSmemLimit - 1024 - tables) / p.stage_bytes);
-    const int by_tmem = (512 - 2 * p.nt) / (8 + 8 * p.nb);
-    if (stages > by_tmem) stages = by_tmem;
+    int stages = (int)((kSmemLimit - 1024 - kOutBytes - tables) / p.stage_bytes);
     if (stages > kMaxStages) stages = kMaxStages;
+    const int by_tmem = (512 - 2 * p.nt) / (8 + 8 * p.nb);
     p.stages = stages;
-    const size_t smem = 1024 + (size_t)stages * p.stage_bytes + tables;
+    p.slots = by_tmem < stages ? by_tmem : stages;
+    p.wide = F % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
+    const size_t smem = 1024 + (size_t)stages * p.stage_bytes + kOutBytes + tables;
 
     CUtensorMap map_a, map_w;
     if (!make_map(&map_a, a, K / 2, rows, 0, kBoxRows) || !make_map(&map_w, w, K / 2, F, E, kM)) return CGL_ECUDA;
     if (!ensure_smem_attr((const void *)matmul_mxfp4_kernel, smem)) return CGL_ECUDA;
     const int sms = device_sm_count();
     if (sms <= 0) return CGL_ECUDA;
-    const int64_t ftiles = (F + kM - 1) / kM;
+    const int64_t ftiles = (F + 2 * kM - 1) / (2 * kM);
     const int64_t most = ((rows + p.nt - 1) / p.nt + (rows < E ? rows : E)) * ftiles;   // tiles there can be
-    int64_t grid = num_sms > 0 && num_sms < sms ? num_sms : sms;
-    if (grid > most) grid = most;
-    return launch_pdl(matmul_mxfp4_kernel, dim3((unsigned)grid), dim3(kThreads), smem, stream, map_a, map_w, p) == cudaSuccess
+    int64_t pairs = (num_sms > 0 && num_sms < sms ? num_sms : sms) / 2;
+    if (pairs < 1) pairs = 1;
+    if (pairs > most) pairs = most;
+    return launch_pdl(matmul_mxfp4_kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), smem, stream, map_a, map_w, p) == cudaSuccess
                ? CGL_OK : CGL_ECUDA;
 }
 
