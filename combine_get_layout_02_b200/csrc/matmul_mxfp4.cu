@@ -10,7 +10,8 @@
 // `nt` rows.  Persistent pairs walk the list of (expert, rows, features) tiles;
 // each block makes the list's prefix sums from expert_offset for itself.
 // One block:
-//   warp 0      TMA: a ring of stages of 256 values (128 bytes) a row, 128-byte swizzle
+//   warp 0, 9   TMA: a ring of stages of 256 values (128 bytes) a row, 128-byte
+//               swizzle; 0 the weights, 9 the tokens
 //   warp 1      TMEM; in the pair's first block the MMA thread: scales smem -> TMEM
 //               (tcgen05.cp), 4 MMAs a stage
 //   warp 2      the weights' scales, 3 and 8 the tokens': global rows -> the 512-byte
@@ -37,16 +38,16 @@ namespace {
 
 constexpr uint32_t kErrTimeout = 1u << CGL_ETIMEOUT;
 constexpr long long kWaitCycles = 1ll << 31;
-constexpr int kThreads = 288;
+constexpr int kThreads = 320;
 constexpr int kStageK = 256;              // values a stage
+constexpr int kChunk = 4;                 // stages a chunk of scales (1024 values, 32 bytes a row)
 constexpr int kM = 128;                   // features a tile
-constexpr int kBoxRows = 16;              // token rows a TMA box
 constexpr int kMaxStages = 12;
-constexpr int kMaxNt = 208;               // 2 accumulators of 208 columns + 4 slots of scales = 512 columns
+constexpr int kMaxNt = 192;               // 2 accumulators of 192 columns + 5 stages' scales: 504 of 512 columns
 constexpr int kOutBytes = 4 * 2048;       // the epilogue's 32 x 32 BF16 blocks, one a warp
 constexpr size_t kSmemLimit = 226 * 1024; // dynamic part: 227 KiB less the static part
 constexpr uint32_t kABytes = kM * kStageK / 2;
-constexpr uint32_t kBoxBytes = kBoxRows * kStageK / 2;
+constexpr uint32_t kChunkA = kChunk * 1024;   // bytes of a chunk of the weights' scales, 512 for 128 rows x 4
 
 struct Params {
     const uint8_t *sa, *sw;
@@ -57,11 +58,11 @@ struct Params {
     int E, F, K;
     int nt;          // most token columns a tile (of the pair)
     int nb;          // 128-row scale blocks of the token side (1 or 2)
-    int nbox;        // TMA boxes of the token side a stage has room for
+    int box;         // token rows a TMA box
     int stages;
-    int slots;       // TMEM slots for a stage's scales
+    int chunks;      // chunks of scales in shared memory
     int wide;        // y's rows allow 16-byte stores
-    uint32_t stage_bytes;
+    uint32_t stage_bytes, chunk_bytes;
 };
 
 // ---- barriers, TMA, tcgen05 ----------------------------------------------------------------
@@ -218,6 +219,10 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// A value that is the same in all lanes, so that the compiler knows it too: what
+// depends on it, loops and descriptors alike, stays in uniform registers.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 // ---- the list of tiles -----------------------------------------------------------------------
 
 // Rows [r0, r0 + m) of expert e.  Offsets that run backwards or out of the
@@ -248,7 +253,8 @@ __device__ __forceinline__ void expert_rows(const Params &p, int e, int &r0, int
 struct Tiles {
     const int32_t *first, *row0s, *counts;   // shared: tiles' prefix sums over experts, rows
     int ftiles, rank;
-    int64_t t, total;
+    int64_t t;
+    int left;            // tiles this block has still to do, the present one among them
     int e;
     int f0, row0, n;
 
@@ -258,26 +264,29 @@ struct Tiles {
         counts = row0s + p.E;
         ftiles = (p.F + 2 * kM - 1) / (2 * kM);
         rank = (int)(blockIdx.x & 1);
-        total = (int64_t)first[p.E] * ftiles;
+        const int64_t total = (int64_t)first[p.E] * ftiles;
+        const int pairs = gridDim.x >> 1;
         t = blockIdx.x >> 1;
+        left = uniform((int)((total - t + pairs - 1) / pairs));   // at most 2^40 / 74 tiles... see the launcher
         e = 0;
         place();
     }
-    __device__ __forceinline__ bool valid() const { return t < total; }
+    __device__ __forceinline__ bool valid() const { return left > 0; }
     __device__ __forceinline__ void next() {
         t += gridDim.x >> 1;
+        --left;
         place();
     }
     // Rows of a tile: the expert's, in equal parts of at most nt, rounded up to 16.
     __device__ __forceinline__ void place() {
-        if (t >= total) return;
+        if (left <= 0) return;
         const int q = (int)(t / ftiles);
         f0 = ((int)(t - (int64_t)q * ftiles) * 2 + rank) * kM;
-        while (first[e + 1] <= q) ++e;
-        const int m = counts[e], parts = first[e + 1] - first[e];
+        while (uniform(first[e + 1]) <= q) ++e;
+        const int m = uniform(counts[e]), before = uniform(first[e]), parts = uniform(first[e + 1]) - before;
         const int per = ((m + parts - 1) / parts + 15) & ~15;
-        const int at = (q - first[e]) * per;
-        row0 = row0s[e] + at;
+        const int at = (q - before) * per;
+        row0 = uniform(row0s[e]) + at;
         n = m - at < per ? m - at : per;
     }
     __device__ __forceinline__ int columns() const { return (n + 15) & ~15; }
@@ -315,26 +324,29 @@ __device__ __forceinline__ void load_scales(const uint8_t *row, int at, int byte
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const Params p) {
     extern __shared__ uint8_t smem_raw[];
-    // full and accfree count for the pair, in its first block; empty and accfull are told to both
-    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_accfull[2], s_accfree[2], s_drain;
+    // full, sffull and accfree count for the pair, in its first block; empty, sffree and accfull are told to both
+    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_sffull[3], s_sffree[3], s_accfull[2], s_accfree[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort_word;
     volatile int *abort = &s_abort_word;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const bool first = cluster_rank() == 0;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
-    const uint32_t out = ring + p.stages * p.stage_bytes;
-    uint8_t *out_ptr = ring_ptr + (size_t)p.stages * p.stage_bytes;
+    const uint32_t sf_ring = ring + p.stages * p.stage_bytes, out = sf_ring + p.chunks * p.chunk_bytes;
+    uint8_t *sf_ptr = ring_ptr + (size_t)p.stages * p.stage_bytes, *out_ptr = sf_ptr + (size_t)p.chunks * p.chunk_bytes;
     int32_t *tables = reinterpret_cast<int32_t *>(out_ptr + kOutBytes);
-    const uint32_t off_b = kABytes, off_sa = kABytes + p.nbox * kBoxBytes, off_sb = off_sa + 1024;
 
     if (threadIdx.x == 0) {
         s_abort_word = 0;
         for (int i = 0; i < p.stages; ++i) {
-            bar_init(smem_u32(&s_full[i]), 1 + 2 * (1 + p.nb));   // the bytes' announcement, both blocks' scale warps
+            bar_init(smem_u32(&s_full[i]), 1);
             bar_init(smem_u32(&s_empty[i]), 1);
+        }
+        for (int i = 0; i < p.chunks; ++i) {
+            bar_init(smem_u32(&s_sffull[i]), 2 * (1 + p.nb));   // the scale warps of both blocks
+            bar_init(smem_u32(&s_sffree[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_u32(&s_accfull[i]), 1);
@@ -386,22 +398,26 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     const int ksteps = (p.K + kStageK - 1) / kStageK;
 
     Tiles tile;
-    if (warp == 0) {
+    if (warp == 0 || warp == 9) {
         int s = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (tile.start(p, tables); ok && tile.valid(); tile.next()) {
-            const int half = tile.columns() / 2, boxes = (half + kBoxRows - 1) / kBoxRows;
+            const int half = tile.columns() / 2, boxes = (half + p.box - 1) / p.box;
+            const uint32_t box_bytes = p.box * (kStageK / 2);
             const int row0 = tile.row0 + tile.rank * half;
             for (int k = 0; k < ksteps; ++k) {
                 ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_empty[s]), phase ^ 1, abort, p.status));
                 if (!ok) break;
-                if (elect_one()) {
-                    const uint32_t base = ring + s * p.stage_bytes, bar = in_first(smem_u32(&s_full[s]));
-                    if (first) bar_expect(smem_u32(&s_full[s]), 2 * (kABytes + boxes * kBoxBytes));
-                    tma_3d(base, &map_w, k * (kStageK / 2), tile.f0, tile.e, bar);
+                const uint32_t base = ring + s * p.stage_bytes, bar = in_first(smem_u32(&s_full[s]));
+                if (warp == 0) {
+                    if (elect_one()) {
+                        if (first) bar_expect(smem_u32(&s_full[s]), 2 * (kABytes + boxes * box_bytes));
+                        tma_3d(base, &map_w, k * (kStageK / 2), tile.f0, tile.e, bar);
+                    }
+                } else if (elect_one()) {
                     for (int b = 0; b < boxes; ++b)
-                        tma_2d(base + off_b + b * kBoxBytes, &map_a, k * (kStageK / 2), row0 + b * kBoxRows, bar);
+                        tma_2d(base + kABytes + b * box_bytes, &map_a, k * (kStageK / 2), row0 + b * p.box, bar);
                 }
                 __syncwarp();
                 if (++s == p.stages) s = 0, phase ^= 1;
@@ -412,58 +428,57 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         if (!ok)
             for (const long long start = clock64(); clock64() - start < (1ll << 28);) {}
     } else if (warp == 1 && first) {
-        // A stage's scales go to one of `slots` places in TMEM; the MMAs that read
-        // the place before have ended once the stage they belonged to is free.
-        int s = 0, acc = 0, slot = 0, behind = 0, s_behind = 0;
-        uint32_t phase = 0, accphase = 0, phase_behind = 0;
+        // The issue loop is what bounds small tiles: about 30 cycles an instruction
+        // that it issues and as much for each branch, so its waits are asked for a
+        // stage ahead, errors looked at once a chunk, and K's tail runs as zeros.
+        // A stage's scales have a place of their own in TMEM (slot = ring position):
+        // the MMAs that read it before had ended when the stage was filled again.
+        const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
+        const uint32_t sf0 = tmem + 2 * p.nt, sf_cols = 8 + 8 * p.nb, nb = p.nb, stages = p.stages, stage_bytes = p.stage_bytes;
+        uint32_t s = 0, base = ring, tsf = sf0, phase = 0;      // ring position
+        uint32_t ch = 0, chphase = 0, acc = 0, accphase = 0;
         bool ok = true, any = false, ready = false;
-        const uint32_t sf_cols = 8 + 8 * p.nb;
         for (tile.start(p, tables); ok && tile.valid(); tile.next()) {
             const int n = tile.columns();
             const bool two = n > 128;
             const uint32_t i0 = instr_desc(n, 0), i2 = instr_desc(n, 2);
-            ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_accfree[acc]), accphase ^ 1, abort, p.status));
-            if (!ok) break;
+            ok = bar_wait(smem_u32(&s_accfree[acc]), accphase ^ 1, abort, p.status);
             const uint32_t d = tmem + acc * p.nt;
-            for (int k = 0; k < ksteps; ++k) {
-                if (!ready) ok = bar_wait(smem_u32(&s_full[s]), phase, abort, p.status);
-                if (behind < p.slots) {
-                    ++behind;
-                } else if (p.slots < p.stages) {
-                    ok = ok && bar_wait(smem_u32(&s_empty[s_behind]), phase_behind, abort, p.status);
-                    if (++s_behind == p.stages) s_behind = 0, phase_behind ^= 1;
-                }
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                any = true;
-                const uint32_t base = ring + s * p.stage_bytes, empty = smem_u32(&s_empty[s]);
-                if (++s == p.stages) s = 0, phase ^= 1;
-                ready = bar_test(smem_u32(&s_full[s]), phase);   // the next stage, asked while this one is issued
-                const uint32_t ta = tmem + 2 * p.nt + slot * sf_cols, tb = ta + 8;
-                const int left = p.K - k * kStageK;
-                if (elect_one()) {
-                    const uint64_t sa = desc_scales(base + off_sa), sb = desc_scales(base + off_sb);
-                    const uint64_t da = desc_rows(base), db = desc_rows(base + off_b);
+            for (int k = 0; k < ksteps; k += kChunk) {
+                ok = ok && bar_wait(smem_u32(&s_sffull[ch]), chphase, abort, p.status);
+                const uint32_t sf = sf_ring + ch * p.chunk_bytes;
+                const uint64_t sa = desc_scales(sf), sb = desc_scales(sf + kChunkA);
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {   // 512 bytes (32 descriptor units) a block
-                        scales_to_tmem(ta + 4 * w, sa + 32 * w);
-                        scales_to_tmem(tb + 4 * w * p.nb, sb + 32 * w * p.nb);
-                        if (two) scales_to_tmem(tb + 4 * (w * p.nb + 1), sb + 32 * (w * p.nb + 1));
+                for (int j = 0; j < kChunk; ++j) {
+                    if (k + j >= ksteps) break;
+                    if (!ready) ok = ok && bar_wait(full0 + 8 * s, phase, abort, p.status);
+                    tc_fence_after();
+                    const uint32_t empty = empty0 + 8 * s, ta = tsf, tb = tsf + 8;
+                    const uint64_t da = desc_rows(base), db = desc_rows(base + kABytes);
+                    ++s, base += stage_bytes, tsf += sf_cols;
+                    if (s == stages) s = 0, base = ring, tsf = sf0, phase ^= 1;
+                    ready = bar_test(full0 + 8 * s, phase);
+                    if (elect_one() && ok) {
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {   // 512 bytes (32 descriptor units) a block
+                            scales_to_tmem(ta + 4 * w, sa + 32 * (2 * j + w));
+                            scales_to_tmem(tb + 4 * w * nb, sb + 32 * (2 * j + w) * nb);
+                            if (two) scales_to_tmem(tb + 4 * (w * nb + 1), sb + 32 * ((2 * j + w) * nb + 1));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)     // 64 values: 32 bytes (two units) of each row
+                            mma_mxf4(d, da + 2 * i, db + 2 * i, (i & 1) ? i2 : i0, ta + 4 * (i >> 1), tb + 4 * (i >> 1) * nb,
+                                     i > 0 || j > 0 || k > 0);
+                        mma_commit_both(empty);
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)     // 64 values: 32 bytes (two units) of each row
-                        if (left > 64 * i)
-                            mma_mxf4(d, da + 2 * i, db + 2 * i, (i & 1) ? i2 : i0, ta + 4 * (i >> 1),
-                                     tb + 4 * (i >> 1) * p.nb, (k | i) != 0);
-                    mma_commit_both(empty);
-                    if (left <= kStageK) mma_commit_both(smem_u32(&s_accfull[acc]));
                 }
-                __syncwarp();
-                if (++slot == p.slots) slot = 0;
+                if (elect_one() && ok) mma_commit_both(smem_u32(&s_sffree[ch]));
+                any = true;
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (++ch == p.chunks) ch = 0, chphase ^= 1;
             }
+            if (elect_one() && ok) mma_commit_both(smem_u32(&s_accfull[acc]));
             acc ^= 1;
             if (acc == 0) accphase ^= 1;
         }
@@ -477,8 +492,8 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         const bool weights = warp == 2;
         const int block = warp == 8 ? 1 : 0;   // 128-row block of the token side
         if (weights || block < p.nb) {
-            const int row_bytes = p.K / 32, chunks = (ksteps + 3) / 4;
-            int s = 0, chunk = 0;
+            const int row_bytes = p.K / 32, chunks = (ksteps + kChunk - 1) / kChunk;
+            int ch = 0, chunk = 0;
             uint32_t phase = 0;
             uint32_t v[4][8], nv[4][8];
             const auto load = [&](const Tiles &t, int c, uint32_t (&to)[4][8]) {
@@ -528,22 +543,17 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                     to_l2(after);
                 }
                 if (ahead.valid()) load(ahead, ahead_chunk, nv);
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_sffree[ch]), phase ^ 1, abort, p.status));
+                if (ok) {
+                    uint8_t *to = sf_ptr + (size_t)ch * p.chunk_bytes + (weights ? 0 : kChunkA + 512 * block) + lane * 16;
+                    const int step = 512 * (weights ? 1 : p.nb);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (ok && chunk * 4 + j < ksteps) {
-                        ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_empty[s]), phase ^ 1, abort, p.status));
-                        if (ok) {
-                            uint8_t *to = ring_ptr + (size_t)s * p.stage_bytes + (weights ? off_sa : off_sb + 512 * block) + lane * 16;
-                            const int step = 512 * (weights ? 1 : p.nb);
-                            *reinterpret_cast<uint4 *>(to) = make_uint4(v[0][2 * j], v[1][2 * j], v[2][2 * j], v[3][2 * j]);
-                            *reinterpret_cast<uint4 *>(to + step) =
-                                make_uint4(v[0][2 * j + 1], v[1][2 * j + 1], v[2][2 * j + 1], v[3][2 * j + 1]);
-                            fence_proxy_async();
-                            __syncwarp();
-                            if (lane == 0) bar_arrive_remote(in_first(smem_u32(&s_full[s])));
-                            if (++s == p.stages) s = 0, phase ^= 1;
-                        }
-                    }
+                    for (int j = 0; j < 8; ++j)   // 128 values each; past the row's end zeros that nothing reads
+                        *reinterpret_cast<uint4 *>(to + j * step) = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_remote(in_first(smem_u32(&s_sffull[ch])));
+                    if (++ch == p.chunks) ch = 0, phase ^= 1;
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -656,22 +666,25 @@ cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows
     p.sa = sa, p.sw = sw, p.off = off, p.y = y, p.status = status;
     p.rows = rows, p.cap = cap, p.E = E, p.F = F, p.K = K;
     // Columns a tile: twice the mean rows of an expert (a padded one's capacity), so that few experts need two tiles.
-    const int64_t want = cap > 0 ? cap : 2 * ((rows + E - 1) / E);
+    const int64_t mean = (rows + E - 1) / E, want = cap > 0 ? cap : mean + mean / 4 + 8;
     p.nt = want >= kMaxNt ? kMaxNt : want <= 32 ? 32 : (int)((want + 15) / 16 * 16);
     p.nb = p.nt > 128 ? 2 : 1;
-    p.nbox = (p.nt / 2 + kBoxRows - 1) / kBoxRows;
-    p.stage_bytes = kABytes + p.nbox * kBoxBytes + 1024 + 1024 * p.nb;
+    p.box = p.nt > 64 ? 32 : 16;
+    p.stage_bytes = kABytes + (p.nt / 2 + p.box - 1) / p.box * p.box * (kStageK / 2);
+    p.chunk_bytes = kChunkA * (1 + p.nb);
     const size_t tables = (size_t)(3 * E + 1) * 4;
-    int stages = (int)((kSmemLimit - 1024 - kOutBytes - tables) / p.stage_bytes);
-    if (stages > kMaxStages) stages = kMaxStages;
+    const size_t room = kSmemLimit - 1024 - kOutBytes - tables;
+    int stages = (int)((room - 2 * p.chunk_bytes) / p.stage_bytes);
     const int by_tmem = (512 - 2 * p.nt) / (8 + 8 * p.nb);
+    if (stages > by_tmem) stages = by_tmem;
+    if (stages > kMaxStages) stages = kMaxStages;
+    p.chunks = room - (size_t)stages * p.stage_bytes >= 3 * p.chunk_bytes ? 3 : 2;
     p.stages = stages;
-    p.slots = by_tmem < stages ? by_tmem : stages;
     p.wide = F % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
-    const size_t smem = 1024 + (size_t)stages * p.stage_bytes + kOutBytes + tables;
+    const size_t smem = 1024 + (size_t)stages * p.stage_bytes + (size_t)p.chunks * p.chunk_bytes + kOutBytes + tables;
 
     CUtensorMap map_a, map_w;
-    if (!make_map(&map_a, a, K / 2, rows, 0, kBoxRows) || !make_map(&map_w, w, K / 2, F, E, kM)) return CGL_ECUDA;
+    if (!make_map(&map_a, a, K / 2, rows, 0, p.box) || !make_map(&map_w, w, K / 2, F, E, kM)) return CGL_ECUDA;
     if (!ensure_smem_attr((const void *)matmul_mxfp4_kernel, smem)) return CGL_ECUDA;
     const int sms = device_sm_count();
     if (sms <= 0) return CGL_ECUDA;
