@@ -219,10 +219,6 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// A value that is the same in all lanes, so that the compiler knows it too: what
-// depends on it, loops and descriptors alike, stays in uniform registers.
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
-
 // ---- the list of tiles -----------------------------------------------------------------------
 
 // Rows [r0, r0 + m) of expert e.  Offsets that run backwards or out of the
@@ -252,11 +248,10 @@ __device__ __forceinline__ void expert_rows(const Params &p, int e, int &r0, int
 // side by side; f0 may be past the last one), token rows [row0, row0 + n).
 struct Tiles {
     const int32_t *first, *row0s, *counts;   // shared: tiles' prefix sums over experts, rows
-    int ftiles, rank;
-    int64_t t;
-    int left;            // tiles this block has still to do, the present one among them
-    int e;
-    int f0, row0, n;
+    int ftiles, rank, last;                  // last: tiles of rows in all
+    int q, ft, dq, dft;                      // the tile of rows and of features, and the step from one tile to the next
+    int e, end, per, at0;                    // expert; first tile of rows behind it, rows a tile, row0 of a tile q: at0 + q * per
+    int f0, row0, n, stop;
 
     __device__ __forceinline__ void start(const Params &p, const int32_t *tables) {
         first = tables;
@@ -264,30 +259,37 @@ struct Tiles {
         counts = row0s + p.E;
         ftiles = (p.F + 2 * kM - 1) / (2 * kM);
         rank = (int)(blockIdx.x & 1);
-        const int64_t total = (int64_t)first[p.E] * ftiles;
-        const int pairs = gridDim.x >> 1;
-        t = blockIdx.x >> 1;
-        left = uniform((int)((total - t + pairs - 1) / pairs));   // at most 2^40 / 74 tiles... see the launcher
-        e = 0;
+        last = first[p.E];
+        const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+        q = pair / ftiles, ft = pair % ftiles;
+        dq = pairs / ftiles, dft = pairs % ftiles;
+        e = -1, end = 0;
         place();
     }
-    __device__ __forceinline__ bool valid() const { return left > 0; }
+    __device__ __forceinline__ bool valid() const { return q < last; }
     __device__ __forceinline__ void next() {
-        t += gridDim.x >> 1;
-        --left;
+        q += dq;
+        ft += dft;
+        if (ft >= ftiles) ft -= ftiles, ++q;
         place();
     }
     // Rows of a tile: the expert's, in equal parts of at most nt, rounded up to 16.
     __device__ __forceinline__ void place() {
-        if (left <= 0) return;
-        const int q = (int)(t / ftiles);
-        f0 = ((int)(t - (int64_t)q * ftiles) * 2 + rank) * kM;
-        while (uniform(first[e + 1]) <= q) ++e;
-        const int m = uniform(counts[e]), before = uniform(first[e]), parts = uniform(first[e + 1]) - before;
-        const int per = ((m + parts - 1) / parts + 15) & ~15;
-        const int at = (q - before) * per;
-        row0 = uniform(row0s[e]) + at;
-        n = m - at < per ? m - at : per;
+        if (q >= last) return;
+        if (q >= end) {
+            int begin = end;
+            do {
+                begin = end;
+                end = first[++e + 1];
+            } while (end <= q);
+            const int m = counts[e];
+            per = ((m + end - begin - 1) / (end - begin) + 15) & ~15;
+            at0 = row0s[e] - begin * per;
+            stop = row0s[e] + m;
+        }
+        f0 = (2 * ft + rank) * kM;
+        row0 = at0 + q * per;
+        n = stop - row0 < per ? stop - row0 : per;
     }
     __device__ __forceinline__ int columns() const { return (n + 15) & ~15; }
 };
