@@ -12,8 +12,8 @@
 // One block:
 //   warp 0, 9   TMA: a ring of stages of 256 values (128 bytes) a row, 128-byte
 //               swizzle; 0 the weights, 9 the tokens
-//   warp 1      TMEM; in the pair's first block the MMA thread: scales smem -> TMEM
-//               (tcgen05.cp), 4 MMAs a stage
+//   warp 1, 10  in the pair's first block, for both: 1 issues the MMAs, 4 a stage,
+//               10 the copies of the scales from shared memory to TMEM (tcgen05.cp)
 //   warp 2      the weights' scales, 3 and 8 the tokens': global rows -> the 512-byte
 //               blocks that tcgen05.cp wants (row r's word at (r % 32) * 16 + (r / 32) * 4)
 //   warps 4-7   TMEM -> registers -> transposed through shared memory -> BF16 rows,
@@ -38,7 +38,7 @@ namespace {
 
 constexpr uint32_t kErrTimeout = 1u << CGL_ETIMEOUT;
 constexpr long long kWaitCycles = 1ll << 31;
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kStageK = 256;              // values a stage
 constexpr int kChunk = 4;                 // stages a chunk of scales (1024 values, 32 bytes a row)
 constexpr int kM = 128;                   // features a tile
@@ -327,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     // full, sffull and accfree count for the pair, in its first block; empty, sffree and accfull are told to both
-    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_sffull[3], s_sffree[3], s_accfull[2], s_accfree[2], s_drain;
+    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_sffull[3], s_sffree[3], s_accfull[2], s_accfree[2], s_drain[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort_word;
     volatile int *abort = &s_abort_word;
@@ -343,7 +343,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     if (threadIdx.x == 0) {
         s_abort_word = 0;
         for (int i = 0; i < p.stages; ++i) {
-            bar_init(smem_u32(&s_full[i]), 1);
+            bar_init(smem_u32(&s_full[i]), 2);   // the copies' bytes, the scales in TMEM
             bar_init(smem_u32(&s_empty[i]), 1);
         }
         for (int i = 0; i < p.chunks; ++i) {
@@ -354,7 +354,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             bar_init(smem_u32(&s_accfull[i]), 1);
             bar_init(smem_u32(&s_accfree[i]), 8);   // the epilogue warps of both blocks
         }
-        bar_init(smem_u32(&s_drain), 1);
+        for (int i = 0; i < 2; ++i) bar_init(smem_u32(&s_drain[i]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
@@ -429,30 +429,26 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         // in flight (issued at most a stage ring ago) get 2^28 cycles to land.
         if (!ok)
             for (const long long start = clock64(); clock64() - start < (1ll << 28);) {}
-    } else if (warp == 1 && first) {
-        // The issue loop is what bounds small tiles: about 30 cycles an instruction
-        // that it issues and as much for each branch, so its waits are asked for a
-        // stage ahead, errors looked at once a chunk, and K's tail runs as zeros.
-        // A stage's scales have a place of their own in TMEM (slot = ring position):
-        // the MMAs that read it before had ended when the stage was filled again.
+    } else if ((warp == 1 || warp == 10) && first) {
+        // What bounds this loop is its instructions: 20 to 30 cycles for each that it
+        // issues, as much for each branch.  Hence two warps, a wait that is asked for
+        // a stage ahead, and K's tail run as zeros.  A stage's scales have a place of
+        // their own in TMEM (its place in the ring): the MMAs that read it before had
+        // ended when the stage was free.
+        const bool mma = warp == 1;
         const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
         const uint32_t sf0 = tmem + 2 * p.nt, sf_cols = 8 + 8 * p.nb, nb = p.nb, stages = p.stages, stage_bytes = p.stage_bytes;
         uint32_t s = 0, base = ring, tsf = sf0, phase = 0;      // ring position
-        uint32_t ch = 0, chphase = 0, acc = 0, accphase = 0;
-        bool ok = true, any = false, ready = false;
-        for (tile.start(p, tables); ok && tile.valid(); tile.next()) {
-            const int n = tile.columns();
-            const bool two = n > 128;
-            const uint32_t i0 = instr_desc(n, 0), i2 = instr_desc(n, 2);
-            ok = bar_wait(smem_u32(&s_accfree[acc]), accphase ^ 1, abort, p.status);
-            const uint32_t d = tmem + acc * p.nt;
-            for (int k = 0; k < ksteps; k += kChunk) {
-                ok = ok && bar_wait(smem_u32(&s_sffull[ch]), chphase, abort, p.status);
-                const uint32_t sf = sf_ring + ch * p.chunk_bytes;
-                const uint64_t sa = desc_scales(sf), sb = desc_scales(sf + kChunkA);
-#pragma unroll
-                for (int j = 0; j < kChunk; ++j) {
-                    if (k + j >= ksteps) break;
+        bool ok = true, any = false;
+        tile.start(p, tables);
+        if (mma) {
+            uint32_t acc = 0, accphase = 0;
+            bool ready = false;
+            for (; ok && tile.valid(); tile.next()) {
+                const uint32_t i0 = instr_desc(tile.columns(), 0), i2 = instr_desc(tile.columns(), 2);
+                ok = bar_wait(smem_u32(&s_accfree[acc]), accphase ^ 1, abort, p.status);
+                const uint32_t d = tmem + acc * p.nt;
+                for (int k = 0; k < ksteps; ++k) {
                     if (!ready) ok = ok && bar_wait(full0 + 8 * s, phase, abort, p.status);
                     tc_fence_after();
                     const uint32_t empty = empty0 + 8 * s, ta = tsf, tb = tsf + 8;
@@ -462,33 +458,58 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                     ready = bar_test(full0 + 8 * s, phase);
                     if (elect_one() && ok) {
 #pragma unroll
-                        for (int w = 0; w < 2; ++w) {   // 512 bytes (32 descriptor units) a block
-                            scales_to_tmem(ta + 4 * w, sa + 32 * (2 * j + w));
-                            scales_to_tmem(tb + 4 * w * nb, sb + 32 * (2 * j + w) * nb);
-                            if (two) scales_to_tmem(tb + 4 * (w * nb + 1), sb + 32 * ((2 * j + w) * nb + 1));
-                        }
-#pragma unroll
                         for (int i = 0; i < 4; ++i)     // 64 values: 32 bytes (two units) of each row
                             mma_mxf4(d, da + 2 * i, db + 2 * i, (i & 1) ? i2 : i0, ta + 4 * (i >> 1), tb + 4 * (i >> 1) * nb,
-                                     i > 0 || j > 0 || k > 0);
+                                     i > 0 || k > 0);
                         mma_commit_both(empty);
                     }
                 }
-                if (elect_one() && ok) mma_commit_both(smem_u32(&s_sffree[ch]));
+                if (elect_one() && ok) mma_commit_both(smem_u32(&s_accfull[acc]));
                 any = true;
                 ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                if (++ch == p.chunks) ch = 0, chphase ^= 1;
+                acc ^= 1;
+                if (acc == 0) accphase ^= 1;
             }
-            if (elect_one() && ok) mma_commit_both(smem_u32(&s_accfull[acc]));
-            acc ^= 1;
-            if (acc == 0) accphase ^= 1;
+        } else {
+            uint32_t ch = 0, chphase = 0;
+            for (; ok && tile.valid(); tile.next()) {
+                const bool two = tile.columns() > 128;
+                for (int k = 0; k < ksteps; k += kChunk) {
+                    ok = ok && bar_wait(smem_u32(&s_sffull[ch]), chphase, abort, p.status);
+                    const uint32_t sf = sf_ring + ch * p.chunk_bytes;
+                    const uint64_t sa = desc_scales(sf), sb = desc_scales(sf + kChunkA);
+#pragma unroll
+                    for (int j = 0; j < kChunk; ++j) {
+                        if (k + j >= ksteps) break;
+                        ok = ok && bar_wait(empty0 + 8 * s, phase ^ 1, abort, p.status);
+                        tc_fence_after();
+                        if (elect_one() && ok) {
+#pragma unroll
+                            for (int w = 0; w < 2; ++w) {   // 512 bytes (32 descriptor units) a block
+                                scales_to_tmem(tsf + 4 * w, sa + 32 * (2 * j + w));
+                                scales_to_tmem(tsf + 8 + 4 * w * nb, sb + 32 * (2 * j + w) * nb);
+                                if (two) scales_to_tmem(tsf + 8 + 4 * (w * nb + 1), sb + 32 * ((2 * j + w) * nb + 1));
+                            }
+                            mma_commit(full0 + 8 * s);
+                        }
+                        ++s, tsf += sf_cols;
+                        if (s == stages) s = 0, tsf = sf0, phase ^= 1;
+                    }
+                    if (elect_one() && ok) mma_commit_both(smem_u32(&s_sffree[ch]));
+                    any = true;
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    if (++ch == p.chunks) ch = 0, chphase ^= 1;
+                }
+            }
         }
-        if (any) {   // every MMA has ended before TMEM is freed
-            if (elect_one()) mma_commit(smem_u32(&s_drain));
+        if (any) {   // every MMA and copy has ended before TMEM is freed
+            const uint32_t drain = smem_u32(&s_drain[mma ? 0 : 1]);
+            __syncwarp();
+            if (elect_one()) mma_commit(drain);
             __syncwarp();
             const long long start = clock64();
-            while (!bar_try(smem_u32(&s_drain), 0) && clock64() - start < kWaitCycles) {}
+            while (!bar_try(drain, 0) && clock64() - start < kWaitCycles) {}
         }
     } else if (warp == 2 || warp == 3 || warp == 8) {
         const bool weights = warp == 2;
@@ -565,7 +586,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 chunk = ahead_chunk;
             }
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
         const int quarter = warp & 3;
         const uint32_t mine = out + quarter * 2048;
         const uint8_t *mine_ptr = out_ptr + quarter * 2048;

@@ -80,6 +80,18 @@ def test_scales_over_a_wide_range(k):
     _check(*_case([100, 3, 64], k, 200, k, lo=90, hi=164), exact=False)
 
 
+@pytest.mark.parametrize("counts,k,f,cap", [([40] * 20, 7168, 512, 0), ([150, 0, 3] * 8, 2048, 768, 0), ([9] * 60, 4096, 256, 16)])
+def test_many_tiles_a_pair(counts, k, f, cap):
+    """One pair of blocks walks every tile: rings and accumulators wrap many times."""
+    a, sa, w, sw, off, cap = _case(counts, k, f, k, cap=cap, lo=127, hi=127)
+    st = cgl.new_status()
+    y = torch.full((a.shape[0], f), -7.0, dtype=torch.bfloat16, device="cuda")
+    cgl.matmul_mxfp4(a, sa, w, sw, off, cap, y=y, status=st, num_sms=2)
+    assert cgl.status_bits(st) == []
+    ref, _ = mxref.product(a, sa, w, sw, mxref.spans(off, cap, a.shape[0]))
+    assert torch.equal(y, torch.where(ref.isnan(), -7.0, ref).float().bfloat16())
+
+
 def test_random_sizes():
     g = np.random.Generator(np.random.PCG64(7))
     for i in range(25):
