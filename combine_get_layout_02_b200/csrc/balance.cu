@@ -10,12 +10,19 @@
 // its mean, u (E c[e] - sum c) with u = alpha / (S k T_s^2), whose bracket is
 // an exact integer, so near-equal counts lose nothing to cancellation.
 //
-// Kernels: histograms of id chunks (shared-memory integer atomics, order
-// without effect) -> one warp per token, the chunks' counts summed by every
-// block for itself -> the blocks' loss sums in a fixed order.
-#include <cuda_fp16.h>
-
-#include "common.cuh"
+// Two kernels: histograms of id chunks (shared-memory integer atomics, whose
+// order has no effect), then the pass over the logits, where every block first
+// sums the chunks' counts for itself and the last block to finish adds up the
+// blocks' loss sums in their order.  The grid goes by the sizes alone, so equal
+// inputs give equal bits.
+//
+// The pass is bound by the bytes of the logits and the gradient, and close
+// behind by its instructions: a lane holds 8 neighbouring experts (one 16-byte
+// load of 16-bit logits) and their weights in registers, 2 to 32 lanes share a
+// token, the exponential is one ex2, and the next token's logits are loaded
+// ahead.  Where E % 8 != 0 or the rows are not 16-byte aligned a lane holds
+// experts l, l + 32, ... instead.
+#include "mxfp4.cuh"
 #include "launch.h"
 
 namespace cgl {
@@ -26,6 +33,8 @@ constexpr int kCountThreads = 512;
 constexpr int kMainThreads = 256;
 constexpr int kMainWarps = kMainThreads / 32;
 constexpr int64_t kMaxBlocks = 1184;   // 148 SMs x 8 blocks; a constant, so sums do not depend on the device
+constexpr int64_t kChunkIds = 4096;    // ids a histogram block
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct Shape {
     int64_t tokens;      // per sequence
@@ -36,56 +45,99 @@ struct Shape {
     int main_chunks;     // blocks per sequence of the main pass
 };
 
+// Lanes that share a token in the vector form: 8 experts each.
+int lanes_for(int E) {
+    int lanes = 1;
+    while (lanes < 32 && lanes * 8 < E) lanes *= 2;
+    return lanes;
+}
+
 Shape shape(int64_t n, int k, int E, int64_t S) {
     Shape s;
     s.tokens = n / S;
     s.seqs = S;
     s.k = k;
     s.E = E;
-    const int64_t want = (s.tokens * k + 8191) / 8192, fit = kMaxBlocks / S > 0 ? kMaxBlocks / S : 1;
+    const int64_t want = (s.tokens * k + kChunkIds - 1) / kChunkIds, fit = kMaxBlocks / S > 0 ? kMaxBlocks / S : 1;
     int64_t c = want < 32 ? want : 32;
     if (c > fit) c = fit;
     if (c < 1) c = 1;
     s.count_chunks = (int)c;
     s.count_tokens = (s.tokens + c - 1) / c;
-    int64_t d = (s.tokens + kMainWarps - 1) / kMainWarps;
+    const int64_t at_once = kMainWarps * (E % 8 == 0 ? 32 / lanes_for(E) : 1);   // tokens a block has in hand
+    int64_t d = (s.tokens + at_once - 1) / at_once;
     if (d > fit) d = fit;
     s.main_chunks = d < 1 ? 1 : (int)d;
     return s;
 }
 
+// part[block][E + 1]: slots per expert, routed tokens.  ticket: zeroed for the main kernel.
 __global__ void __launch_bounds__(kCountThreads)
 balance_count_kernel(const int32_t *__restrict__ idx, int64_t tokens, int k, int E, int chunks, int64_t per_chunk,
-                     int32_t *__restrict__ part, uint32_t *status) {
-    extern __shared__ int32_t s_count[];   // [E + 1]: slots per expert, routed tokens
+                     int32_t *__restrict__ part, uint32_t *__restrict__ ticket, uint32_t *status) {
+    extern __shared__ int32_t s_count[];
     griddep_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
     for (int e = threadIdx.x; e <= E; e += kCountThreads) s_count[e] = 0;
     __syncthreads();
     const int64_t seq = blockIdx.x / chunks, c = blockIdx.x % chunks;
     const int64_t t0 = c * per_chunk, t1 = t0 + per_chunk < tokens ? t0 + per_chunk : tokens;
+    const bool vec = (k & 3) == 0 && (reinterpret_cast<uintptr_t>(idx) & 15) == 0;
     bool bad = false;
     for (int64_t t = t0 + threadIdx.x; t < t1; t += kCountThreads) {
         const int32_t *p = idx + (seq * tokens + t) * k;
         bool any = false;
-        for (int j = 0; j < k; ++j) {
-            const int32_t e = __ldg(p + j);
-            if (e >= 0 && e < E) {
-                atomicAdd(&s_count[e], 1);
-                any = true;
-            } else if (e != -1) {
-                bad = true;
+        for (int j = 0; j < k; j += 8) {   // the loads of 8 slots before the first of them is used
+            int32_t id[8];
+            if (vec) {
+                const int4 a = __ldg(reinterpret_cast<const int4 *>(p + j));
+                const int4 b = j + 4 < k ? __ldg(reinterpret_cast<const int4 *>(p + j) + 1) : make_int4(-1, -1, -1, -1);
+                id[0] = a.x, id[1] = a.y, id[2] = a.z, id[3] = a.w, id[4] = b.x, id[5] = b.y, id[6] = b.z, id[7] = b.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) id[i] = j + i < k ? __ldg(p + j + i) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (id[i] >= 0 && id[i] < E) {
+                    atomicAdd(&s_count[id[i]], 1);
+                    any = true;
+                } else if (id[i] != -1) {
+                    bad = true;
+                }
             }
         }
-        if (any) atomicAdd(&s_count[E], 1);
+        const uint32_t m = __ballot_sync(__activemask(), any);
+        if ((threadIdx.x & 31) == __ffs(__activemask()) - 1 && m) atomicAdd(&s_count[E], __popc(m));
     }
     __syncthreads();
     for (int e = threadIdx.x; e <= E; e += kCountThreads) part[(int64_t)blockIdx.x * (E + 1) + e] = s_count[e];
     if (bad) report(status, kErrRange);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// 2^x, subnormal results included.
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// 1 / x for x in [1, 2], within one step.
+__device__ __forceinline__ float rcp12(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+template <int LANES>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     return v;
 }
 
@@ -103,32 +155,90 @@ __device__ __forceinline__ void store1(void *p, int64_t i, float v) {
     else static_cast<__half *>(p)[i] = __float2half_rn(v);
 }
 
-// One warp per token, lane l holding experts l, l + 32, ...  part: the count
-// kernel's chunks (chunks > 0), or counts / routed as the forward gave them.
-template <int DT, int V>
+// A token's logits in one lane: N groups of eight neighbours (VEC), or N single experts 32 apart.
+template <int DT, int LANES, int N, bool VEC>
+struct Row {
+    static constexpr int V = VEC ? 8 * N : N;
+    Vec8<DT> raw[VEC ? N : 1];
+    float one[VEC ? 1 : N];
+
+    static __device__ __forceinline__ int expert(int lane, int i) {
+        return VEC ? ((i / 8) * LANES + lane) * 8 + i % 8 : lane + 32 * i;
+    }
+    __device__ __forceinline__ void load(const void *p, int64_t tok, int E, int lane) {
+        if (VEC) {
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+                if (expert(lane, 8 * c) < E) raw[c].load(p, (tok * E + expert(lane, 8 * c)) >> 3);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (expert(lane, i) < E) one[i] = load1<DT>(p, tok * E + expert(lane, i));
+        }
+    }
+    __device__ __forceinline__ void widen(float l[V], int E, int lane) const {
+        if (VEC) {
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                raw[c].widen(l + 8 * c);
+                if (expert(lane, 8 * c) >= E)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) l[8 * c + i] = -INFINITY;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) l[i] = expert(lane, i) < E ? one[i] : -INFINITY;
+        }
+    }
+    static __device__ __forceinline__ void store(void *p, int64_t tok, int E, int lane, const float v[V]) {
+        if (VEC) {
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+                if (expert(lane, 8 * c) < E) Vec8<DT>::store(p, (tok * E + expert(lane, 8 * c)) >> 3, v + 8 * c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (expert(lane, i) < E) store1<DT>(p, tok * E + expert(lane, i), v[i]);
+        }
+    }
+};
+
+// LANES lanes a token.  part: the count kernel's chunks (chunks > 0), or null
+// and counts / routed as the forward gave them (loss_part null then).
+template <int DT, int LANES, int N, bool VEC>
 __global__ void __launch_bounds__(kMainThreads)
 balance_main_kernel(const void *__restrict__ logits, const int32_t *__restrict__ idx, int64_t tokens, int k, int E,
-                    double scale, int sigmoid, const int32_t *__restrict__ part, int chunks,
-                    int32_t *__restrict__ counts, int32_t *__restrict__ routed, const float *__restrict__ grad_loss,
-                    void *__restrict__ grad, double *__restrict__ loss_part, int main_chunks) {
-    extern __shared__ float s_w[];   // [E] weights less their mean
-    __shared__ long long s_total;
+                    double scale, int sigmoid, const int32_t *__restrict__ part, int chunks, int32_t *counts,
+                    int32_t *routed, const float *__restrict__ grad_loss, void *__restrict__ grad, double *loss_part,
+                    uint32_t *ticket, float *loss, int main_chunks) {
+    using R = Row<DT, LANES, N, VEC>;
+    constexpr int V = R::V, kTokens = 32 / LANES;   // tokens a warp has in hand
+    extern __shared__ float s_w[];                  // [E] weights less their mean
+    __shared__ unsigned long long s_total;
     __shared__ int s_routed;
     __shared__ double s_loss[kMainWarps];
+    __shared__ bool s_last;
     griddep_wait();
     const int64_t seq = blockIdx.x / main_chunks;
     const int chunk = (int)(blockIdx.x % main_chunks);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x % LANES, warp = threadIdx.x >> 5;
+    const int64_t step = (int64_t)main_chunks * kMainWarps * kTokens;
+    int64_t r = ((int64_t)chunk * kMainWarps + warp) * kTokens + (threadIdx.x & 31) / LANES;
+    R row;
+    if (r < tokens) row.load(logits, seq * tokens + r, E, lane);   // in flight through the weights
     int32_t *s_c = reinterpret_cast<int32_t *>(s_w);
-    if (threadIdx.x == 0) { s_total = 0; s_routed = 0; }
+    if (threadIdx.x == 0) s_total = 0;
     __syncthreads();
-    long long mine = 0;
+    unsigned long long mine = 0;
     for (int e = threadIdx.x; e <= E; e += kMainThreads) {
         int32_t c = 0;
-        if (chunks > 0)
-            for (int i = 0; i < chunks; ++i) c += part[(seq * chunks + i) * (E + 1) + e];
-        else
+        if (chunks > 0) {
+            const int32_t *q = part + seq * chunks * (E + 1) + e;
+#pragma unroll 8
+            for (int i = 0; i < chunks; ++i) c += q[(int64_t)i * (E + 1)];
+        } else {
             c = e < E ? counts[seq * E + e] : routed[seq];
+        }
         if (e < E) {
             s_c[e] = c;
             mine += c;
@@ -138,148 +248,179 @@ balance_main_kernel(const void *__restrict__ logits, const int32_t *__restrict__
             if (chunks > 0 && chunk == 0) routed[seq] = c;
         }
     }
-    atomicAdd((unsigned long long *)&s_total, (unsigned long long)mine);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+    if ((threadIdx.x & 31) == 0) atomicAdd(&s_total, mine);
     __syncthreads();
-    const long long total = s_total;
+    const long long total = (long long)s_total;
     const double t = (double)s_routed, unit = t > 0 ? scale / (t * t) : 0.0;   // scale = alpha / (S k)
     const float mean = (float)(unit * (double)total);
-    for (int e = threadIdx.x; e < E; e += kMainThreads)
-        s_w[e] = (float)(unit * (double)((long long)E * s_c[e] - total));
-    __syncthreads();
-    const float g = grad != nullptr ? (grad_loss != nullptr ? __ldg(grad_loss) : 1.0f) : 0.0f;
+    float w[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = R::expert(lane, i);
+        w[i] = e < E ? (float)(unit * (double)((long long)E * s_c[e] - total)) : 0.0f;
+    }
+    const float g = grad != nullptr && grad_loss != nullptr ? __ldg(grad_loss) : 1.0f;
     double acc = 0.0;
-    for (int64_t r = chunk * kMainWarps + warp; r < tokens; r += (int64_t)main_chunks * kMainWarps) {
+    for (; __any_sync(0xFFFFFFFFu, r < tokens); r += step) {
+        const bool here = r < tokens;
         const int64_t tok = seq * tokens + r;
+        float l[V], p[V];
+        row.widen(l, here ? E : 0, lane);
+        if (r + step < tokens) row.load(logits, tok + step, E, lane);
         bool any = false;
-        if (lane < k) {
-            const int32_t e = __ldg(idx + tok * k + lane);
-            any = e >= 0 && e < E;
+        for (int j = lane; here && j < k; j += LANES) {
+            const int32_t e = __ldg(idx + tok * k + j);
+            any = any || (e >= 0 && e < E);
         }
-        any = __any_sync(0xFFFFFFFFu, any);
-        if (!any) {
-            if (grad != nullptr)
-                for (int e = lane; e < E; e += 32) store1<DT>(grad, tok * E + e, 0.0f);
-            continue;
-        }
-        float l[V], p[V], gate[V];
+        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, any);
+        any = ((votes >> ((threadIdx.x & 31) / LANES * LANES)) & (LANES == 32 ? 0xFFFFFFFFu : (1u << (LANES & 31)) - 1u)) != 0;
         float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            l[i] = e < E ? load1<DT>(logits, tok * E + e) : -INFINITY;
-            m = fmaxf(m, l[i]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        float sum = 0.0f, dot = 0.0f;
+        for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+        m = group_max<LANES>(m);
         if (m == -INFINITY) m = 0.0f;        // nothing left (or NaN): exp(-inf) below, not exp(nan)
-        if (sigmoid) m = fminf(m, 0.0f);     // common factor: keeps p where every sigmoid underflows
+        float sum = 0.0f, dot = 0.0f;
+        if (!sigmoid) {
+            const float shift = -m * kLog2e;   // its rounding is a factor that all p share
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (sigmoid) {
-                const float z = expf(-fabsf(l[i])), d = 1.0f / (1.0f + z);
-                p[i] = (l[i] > 0.0f ? 1.0f : expf(l[i] - m)) * d;
-                gate[i] = (l[i] > 0.0f ? z : 1.0f) * d;
-            } else {
-                p[i] = expf(l[i] - m);
-                gate[i] = 1.0f;
-            }
-            sum += p[i];
-            const int e = lane + 32 * i;
-            if (e < E) dot += p[i] * s_w[e];
-        }
-        sum = warp_sum(sum);
-        dot = warp_sum(dot);
-        const bool none = sum == 0.0f;       // every logit is -inf: p = 0
-        const float inv = none ? 0.0f : 1.0f / sum;
-        dot *= inv;
-        if (!none) acc += (double)(mean + dot);
-        if (grad != nullptr) {
+            for (int i = 0; i < V; ++i) p[i] = ex2(fmaf(l[i], kLog2e, shift));
+        } else {
+            // sigmoid(l) exp(-m) with m = min(max l, 0): the common factor keeps p
+            // where every sigmoid underflows.  l becomes the slope 1 - sigmoid(l).
+            m = fminf(m, 0.0f);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int e = lane + 32 * i;
-                if (e < E) store1<DT>(grad, tok * E + e, g * (p[i] * inv) * (s_w[e] - dot) * gate[i]);
+                const bool up = l[i] > 0.0f;
+                const float z = ex2(-fabsf(l[i]) * kLog2e), d = rcp12(1.0f + z);
+                p[i] = (up ? 1.0f : m < 0.0f ? ex2((l[i] - m) * kLog2e) : z) * d;
+                l[i] = (up ? z : 1.0f) * d;
             }
         }
-    }
-    if (loss_part != nullptr) {
-        if (lane == 0) s_loss[warp] = acc;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            double v = 0.0;
-            for (int i = 0; i < kMainWarps; ++i) v += s_loss[i];
-            loss_part[blockIdx.x] = v;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            sum += p[i];
+            dot = fmaf(p[i], w[i], dot);
+        }
+        sum = group_sum<LANES>(sum);
+        dot = group_sum<LANES>(dot);
+        const bool none = sum == 0.0f || !any;   // every logit -inf, or a token without a copy
+        const float inv = none ? 0.0f : __fdiv_rn(1.0f, sum);
+        dot = none ? 0.0f : dot * inv;
+        if (!none && lane == 0) acc += (double)(mean + dot);
+        if (grad != nullptr && here) {
+            const float scale_p = g * inv;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float q = (p[i] * scale_p) * (w[i] - dot);
+                l[i] = none ? 0.0f : sigmoid ? q * l[i] : q;
+            }
+            R::store(grad, tok, E, lane, l);
         }
     }
-}
-
-__global__ void __launch_bounds__(256) balance_sum_kernel(const double *__restrict__ part, int64_t n,
-                                                          float *__restrict__ loss) {
-    __shared__ double s[256];
-    griddep_wait();
-    double v = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += 256) v += part[i];
-    s[threadIdx.x] = v;
+    if (loss_part == nullptr) return;
+#pragma unroll
+    for (int o = 16; o >= LANES && o > 0; o >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
+    if ((threadIdx.x & 31) == 0) s_loss[warp] = acc;
     __syncthreads();
-    for (int o = 128; o > 0; o >>= 1) {
-        if (threadIdx.x < o) s[threadIdx.x] += s[threadIdx.x + o];
-        __syncthreads();
+    if (threadIdx.x == 0) {
+        double v = 0.0;
+        for (int i = 0; i < kMainWarps; ++i) v += s_loss[i];
+        loss_part[blockIdx.x] = v;
+        __threadfence();
+        s_last = atomicAdd(ticket, 1u) == gridDim.x - 1;
     }
-    if (threadIdx.x == 0) *loss = (float)s[0];
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    double v = 0.0;
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kMainThreads) v += *(volatile double *)(loss_part + i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if ((threadIdx.x & 31) == 0) s_loss[warp] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        v = 0.0;
+        for (int i = 0; i < kMainWarps; ++i) v += s_loss[i];
+        *loss = (float)v;
+    }
 }
 
 size_t round16(size_t v) { return (v + 15) / 16 * 16; }
 
-template <int DT, int V>
-cudaError_t launch_main(const Shape &s, const void *logits, const int32_t *idx, double scale, int sigmoid,
-                        const int32_t *part, int chunks, int32_t *counts, int32_t *routed, const float *grad_loss,
-                        void *grad, double *loss_part, cudaStream_t stream) {
-    return launch_pdl(balance_main_kernel<DT, V>, dim3((unsigned)(s.seqs * s.main_chunks)), dim3(kMainThreads),
-                      (size_t)s.E * 4, stream, logits, idx, s.tokens, s.k, s.E, scale, sigmoid, part, chunks, counts,
-                      routed, grad_loss, grad, loss_part, s.main_chunks);
+struct Args {
+    const void *logits;
+    const int32_t *idx;
+    double scale;
+    int sigmoid;
+    const int32_t *part;
+    int chunks;
+    int32_t *counts, *routed;
+    const float *grad_loss;
+    void *grad;
+    double *loss_part;
+    uint32_t *ticket;
+    float *loss;
+    cudaStream_t stream;
+};
+
+template <int DT, int LANES, int N, bool VEC>
+cudaError_t launch_main(const Shape &s, const Args &a) {
+    return launch_pdl(balance_main_kernel<DT, LANES, N, VEC>, dim3((unsigned)(s.seqs * s.main_chunks)), dim3(kMainThreads),
+                      (size_t)s.E * 4, a.stream, a.logits, a.idx, s.tokens, s.k, s.E, a.scale, a.sigmoid, a.part, a.chunks,
+                      a.counts, a.routed, a.grad_loss, a.grad, a.loss_part, a.ticket, a.loss, s.main_chunks);
 }
 
-template <int DT, typename... A>
-cudaError_t main_by_width(const Shape &s, A... a) {
-    if (s.E <= 32) return launch_main<DT, 1>(s, a...);
-    if (s.E <= 64) return launch_main<DT, 2>(s, a...);
-    if (s.E <= 128) return launch_main<DT, 4>(s, a...);
-    if (s.E <= 256) return launch_main<DT, 8>(s, a...);
-    if (s.E <= 512) return launch_main<DT, 16>(s, a...);
-    return launch_main<DT, 32>(s, a...);
+template <int DT>
+cudaError_t main_by_width(const Shape &s, const Args &a) {
+    if (s.E % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.grad)) & 15) == 0) {
+        switch (lanes_for(s.E)) {
+            case 1: return launch_main<DT, 1, 1, true>(s, a);
+            case 2: return launch_main<DT, 2, 1, true>(s, a);
+            case 4: return launch_main<DT, 4, 1, true>(s, a);
+            case 8: return launch_main<DT, 8, 1, true>(s, a);
+            case 16: return launch_main<DT, 16, 1, true>(s, a);
+            default:
+                return s.E <= 256 ? launch_main<DT, 32, 1, true>(s, a)
+                       : s.E <= 512 ? launch_main<DT, 32, 2, true>(s, a) : launch_main<DT, 32, 4, true>(s, a);
+        }
+    }
+    if (s.E <= 32) return launch_main<DT, 32, 1, false>(s, a);
+    if (s.E <= 128) return launch_main<DT, 32, 4, false>(s, a);
+    if (s.E <= 256) return launch_main<DT, 32, 8, false>(s, a);
+    return launch_main<DT, 32, 32, false>(s, a);
 }
 
-template <typename... A>
-cudaError_t main_by_type(int dtype, const Shape &s, A... a) {
+cudaError_t main_by_type(int dtype, const Shape &s, const Args &a) {
     switch (dtype) {
-        case CGL_BF16: return main_by_width<CGL_BF16>(s, a...);
-        case CGL_F16: return main_by_width<CGL_F16>(s, a...);
-        default: return main_by_width<CGL_F32>(s, a...);
+        case CGL_BF16: return main_by_width<CGL_BF16>(s, a);
+        case CGL_F16: return main_by_width<CGL_F16>(s, a);
+        default: return main_by_width<CGL_F32>(s, a);
     }
 }
 
 }  // namespace
 
+// The ticket (16 bytes), the blocks' loss sums, the chunks' counts.
 size_t balance_workspace_bytes(int64_t n, int k, int E, int64_t S) {
     const Shape s = shape(n, k, E, S);
-    return round16((size_t)S * s.count_chunks * (E + 1) * 4) + (size_t)S * s.main_chunks * 8;
+    return 16 + round16((size_t)S * s.main_chunks * 8) + (size_t)S * s.count_chunks * (E + 1) * 4;
 }
 
 cgl_status launch_balance_loss(const void *logits, int dtype, const int32_t *idx, int64_t n, int k, int E, int64_t S,
                                float alpha, int score, const float *grad_loss, float *loss, int32_t *counts,
                                int32_t *routed, void *grad, void *ws, uint32_t *status, cudaStream_t stream) {
     const Shape s = shape(n, k, E, S);
-    int32_t *part = static_cast<int32_t *>(ws);
-    double *loss_part =
-        reinterpret_cast<double *>(static_cast<uint8_t *>(ws) + round16((size_t)S * s.count_chunks * (E + 1) * 4));
+    uint32_t *ticket = static_cast<uint32_t *>(ws);
+    double *loss_part = reinterpret_cast<double *>(static_cast<uint8_t *>(ws) + 16);
+    int32_t *part = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + 16 + round16((size_t)S * s.main_chunks * 8));
     if (launch_pdl(balance_count_kernel, dim3((unsigned)(S * s.count_chunks)), dim3(kCountThreads), (size_t)(E + 1) * 4,
-                   stream, idx, s.tokens, k, E, s.count_chunks, s.count_tokens, part, status) != cudaSuccess)
+                   stream, idx, s.tokens, k, E, s.count_chunks, s.count_tokens, part, ticket, status) != cudaSuccess)
         return CGL_ECUDA;
-    if (main_by_type(dtype, s, logits, idx, (double)alpha / ((double)S * k), score, (const int32_t *)part,
-                     s.count_chunks, counts, routed, grad_loss, grad, loss_part, stream) != cudaSuccess)
-        return CGL_ECUDA;
-    return launch_pdl(balance_sum_kernel, dim3(1), dim3(256), 0, stream, loss_part, S * s.main_chunks, loss) ==
-                   cudaSuccess ? CGL_OK : CGL_ECUDA;
+    const Args a = {logits, idx, (double)alpha / ((double)S * k), score, part, s.count_chunks, counts, routed,
+                    grad_loss, grad, loss_part, ticket, loss, stream};
+    return main_by_type(dtype, s, a) == cudaSuccess ? CGL_OK : CGL_ECUDA;
 }
 
 cgl_status launch_balance_loss_backward(const float *grad_loss, const void *logits, int dtype, const int32_t *idx,
@@ -287,9 +428,9 @@ cgl_status launch_balance_loss_backward(const float *grad_loss, const void *logi
                                         const int32_t *counts, const int32_t *routed, void *grad, cudaStream_t stream) {
     if (n == 0) return CGL_OK;
     const Shape s = shape(n, k, E, S);
-    return main_by_type(dtype, s, logits, idx, (double)alpha / ((double)S * k), score, (const int32_t *)nullptr, 0,
-                        const_cast<int32_t *>(counts), const_cast<int32_t *>(routed), grad_loss, grad,
-                        (double *)nullptr, stream) == cudaSuccess ? CGL_OK : CGL_ECUDA;
+    const Args a = {logits, idx, (double)alpha / ((double)S * k), score, nullptr, 0, const_cast<int32_t *>(counts),
+                    const_cast<int32_t *>(routed), grad_loss, grad, nullptr, nullptr, nullptr, stream};
+    return main_by_type(dtype, s, a) == cudaSuccess ? CGL_OK : CGL_ECUDA;
 }
 
 }  // namespace cgl
