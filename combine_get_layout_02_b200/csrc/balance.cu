@@ -32,7 +32,7 @@ namespace {
 constexpr int kCountThreads = 512;
 constexpr int kMainThreads = 256;
 constexpr int kMainWarps = kMainThreads / 32;
-constexpr int64_t kMaxBlocks = 1184;   // 148 SMs x 8 blocks; a constant, so sums do not depend on the device
+constexpr int64_t kMaxBlocks = 592;    // 148 SMs x 4 blocks; a constant, so sums do not depend on the device
 constexpr int64_t kChunkIds = 4096;    // ids a histogram block
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -45,14 +45,23 @@ struct Shape {
     int main_chunks;     // blocks per sequence of the main pass
 };
 
-// Lanes that share a token in the vector form: 8 experts each.
-int lanes_for(int E) {
-    int lanes = 1;
-    while (lanes < 32 && lanes * 8 < E) lanes *= 2;
-    return lanes;
+// The vector form: lanes that share a token, and groups of 8 experts a lane.
+// 16-bit logits of many tokens take two groups a lane where there are over 8
+// (half the lanes, one shuffle round less for two tokens at once): 65536 x 256
+// BF16, loss and gradient as two calls, 52 -> 41 us; binary32 logits need the
+// registers for occupancy (36 -> 40 us), few tokens the warps (12.5 -> 12.6 us).
+constexpr int64_t kManyTokens = 12288;
+struct Width { int lanes, groups; };
+Width width_for(int64_t n, int E, int dtype) {
+    const int groups = (E + 7) / 8;
+    Width w = {1, 1};
+    if (dtype != CGL_F32 && n >= kManyTokens && groups > 8) w.groups = 2;
+    while (w.lanes < 32 && w.lanes * w.groups < groups) w.lanes *= 2;
+    while (w.lanes * w.groups < groups) w.groups *= 2;
+    return w;
 }
 
-Shape shape(int64_t n, int k, int E, int64_t S) {
+Shape shape(int64_t n, int k, int E, int64_t S, int dtype) {
     Shape s;
     s.tokens = n / S;
     s.seqs = S;
@@ -64,7 +73,7 @@ Shape shape(int64_t n, int k, int E, int64_t S) {
     if (c < 1) c = 1;
     s.count_chunks = (int)c;
     s.count_tokens = (s.tokens + c - 1) / c;
-    const int64_t at_once = kMainWarps * (E % 8 == 0 ? 32 / lanes_for(E) : 1);   // tokens a block has in hand
+    const int64_t at_once = kMainWarps * (E % 8 == 0 ? 32 / width_for(n, E, dtype).lanes : 1);   // tokens a block has in hand
     int64_t d = (s.tokens + at_once - 1) / at_once;
     if (d > fit) d = fit;
     s.main_chunks = d < 1 ? 1 : (int)d;
@@ -77,6 +86,9 @@ balance_count_kernel(const int32_t *__restrict__ idx, int64_t tokens, int k, int
                      int32_t *__restrict__ part, uint32_t *__restrict__ ticket, uint32_t *status) {
     extern __shared__ int32_t s_count[];
     griddep_wait();
+    // The main kernel's blocks may come now: what they read before their own
+    // wait is the logits and ids, and those are there, since this block's wait is over.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
     for (int e = threadIdx.x; e <= E; e += kCountThreads) s_count[e] = 0;
     __syncthreads();
@@ -115,10 +127,13 @@ balance_count_kernel(const int32_t *__restrict__ idx, int64_t tokens, int k, int
     if (bad) report(status, kErrRange);
 }
 
-// 2^x, subnormal results included.
+// 2^x; with FTZ results below 2^-126 are 0, without it they are subnormal (and
+// the compiler adds three instructions).
+template <bool FTZ>
 __device__ __forceinline__ float ex2(float x) {
     float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    if (FTZ) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    else asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 // 1 / x for x in [1, 2], within one step.
@@ -165,6 +180,23 @@ struct Row {
     static __device__ __forceinline__ int expert(int lane, int i) {
         return VEC ? ((i / 8) * LANES + lane) * 8 + i % 8 : lane + 32 * i;
     }
+    // Where expert e's weight stands in shared memory: four of a lane's eight
+    // side by side, the lanes' fours side by side, so that a 16-byte read of all
+    // lanes meets each bank once a phase.
+    static __device__ __forceinline__ int place(int e) {
+        if (!VEC) return e;
+        const int i = e & 7, g = e >> 3;
+        return ((g / LANES * 2 + (i >> 2)) * LANES + g % LANES) * 4 + (i & 3);
+    }
+    static __device__ __forceinline__ void weights(const float *s_w, int lane, int c, float w[8]) {
+        if (VEC) {
+            *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(s_w + ((c * 2) * LANES + lane) * 4);
+            *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(s_w + ((c * 2 + 1) * LANES + lane) * 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 8 * c + i < N ? s_w[lane + 32 * (8 * c + i)] : 0.0f;
+        }
+    }
     __device__ __forceinline__ void load(const void *p, int64_t tok, int E, int lane) {
         if (VEC) {
 #pragma unroll
@@ -205,28 +237,31 @@ struct Row {
 
 // LANES lanes a token.  part: the count kernel's chunks (chunks > 0), or null
 // and counts / routed as the forward gave them (loss_part null then).
-template <int DT, int LANES, int N, bool VEC>
-__global__ void __launch_bounds__(kMainThreads)
+template <int DT, int LANES, int N, bool VEC, bool SIG>
+__global__ void __launch_bounds__(kMainThreads, Row<DT, LANES, N, VEC>::V <= 16 ? 4 : 1)   // 4: the grid is one wave
 balance_main_kernel(const void *__restrict__ logits, const int32_t *__restrict__ idx, int64_t tokens, int k, int E,
-                    double scale, int sigmoid, const int32_t *__restrict__ part, int chunks, int32_t *counts,
+                    double scale, const int32_t *__restrict__ part, int chunks, int32_t *counts,
                     int32_t *routed, const float *__restrict__ grad_loss, void *__restrict__ grad, double *loss_part,
                     uint32_t *ticket, float *loss, int main_chunks) {
     using R = Row<DT, LANES, N, VEC>;
     constexpr int V = R::V, kTokens = 32 / LANES;   // tokens a warp has in hand
-    extern __shared__ float s_w[];                  // [E] weights less their mean
+    extern __shared__ __align__(16) float s_w[];    // [V * LANES] weights less their mean, then [E] counts
     __shared__ unsigned long long s_total;
     __shared__ int s_routed;
     __shared__ double s_loss[kMainWarps];
     __shared__ bool s_last;
-    griddep_wait();
+    if (chunks == 0) griddep_wait();
     const int64_t seq = blockIdx.x / main_chunks;
     const int chunk = (int)(blockIdx.x % main_chunks);
     const int lane = threadIdx.x % LANES, warp = threadIdx.x >> 5;
     const int64_t step = (int64_t)main_chunks * kMainWarps * kTokens;
     int64_t r = ((int64_t)chunk * kMainWarps + warp) * kTokens + (threadIdx.x & 31) / LANES;
     R row;
+    int32_t id = -1;   // the lane's first slot, with the row
+    if (r < tokens && lane < k) id = __ldg(idx + (seq * tokens + r) * k + lane);
     if (r < tokens) row.load(logits, seq * tokens + r, E, lane);   // in flight through the weights
-    int32_t *s_c = reinterpret_cast<int32_t *>(s_w);
+    if (chunks > 0) griddep_wait();   // the counts (see balance_count_kernel on the logits)
+    int32_t *s_c = reinterpret_cast<int32_t *>(s_w + V * LANES);
     if (threadIdx.x == 0) s_total = 0;
     __syncthreads();
     unsigned long long mine = 0;
@@ -234,7 +269,7 @@ balance_main_kernel(const void *__restrict__ logits, const int32_t *__restrict__
         int32_t c = 0;
         if (chunks > 0) {
             const int32_t *q = part + seq * chunks * (E + 1) + e;
-#pragma unroll 8
+#pragma unroll 16
             for (int i = 0; i < chunks; ++i) c += q[(int64_t)i * (E + 1)];
         } else {
             c = e < E ? counts[seq * E + e] : routed[seq];
@@ -255,12 +290,9 @@ balance_main_kernel(const void *__restrict__ logits, const int32_t *__restrict__
     const long long total = (long long)s_total;
     const double t = (double)s_routed, unit = t > 0 ? scale / (t * t) : 0.0;   // scale = alpha / (S k)
     const float mean = (float)(unit * (double)total);
-    float w[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = R::expert(lane, i);
-        w[i] = e < E ? (float)(unit * (double)((long long)E * s_c[e] - total)) : 0.0f;
-    }
+    for (int e = threadIdx.x; e < V * LANES; e += kMainThreads)
+        s_w[R::place(e)] = e < E ? (float)(unit * (double)((long long)E * s_c[e] - total)) : 0.0f;
+    __syncthreads();
     const float g = grad != nullptr && grad_loss != nullptr ? __ldg(grad_loss) : 1.0f;
     double acc = 0.0;
     for (; __any_sync(0xFFFFFFFFu, r < tokens); r += step) {
@@ -268,40 +300,68 @@ balance_main_kernel(const void *__restrict__ logits, const int32_t *__restrict__
         const int64_t tok = seq * tokens + r;
         float l[V], p[V];
         row.widen(l, here ? E : 0, lane);
-        if (r + step < tokens) row.load(logits, tok + step, E, lane);
-        bool any = false;
-        for (int j = lane; here && j < k; j += LANES) {
+        bool any = here && id >= 0 && id < E;
+        if (r + step < tokens) {
+            if (lane < k) id = __ldg(idx + (tok + step) * k + lane);
+            row.load(logits, tok + step, E, lane);
+        }
+        for (int j = lane + LANES; here && j < k; j += LANES) {
             const int32_t e = __ldg(idx + tok * k + j);
             any = any || (e >= 0 && e < E);
         }
         const uint32_t votes = __ballot_sync(0xFFFFFFFFu, any);
         any = ((votes >> ((threadIdx.x & 31) / LANES * LANES)) & (LANES == 32 ? 0xFFFFFFFFu : (1u << (LANES & 31)) - 1u)) != 0;
-        float m = -INFINITY;
+        float m = -INFINITY, low = INFINITY;
 #pragma unroll
-        for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+        for (int i = 0; i < V; ++i) {
+            m = fmaxf(m, l[i]);
+            low = fminf(low, SIG ? -fabsf(l[i]) : l[i]);
+        }
         m = group_max<LANES>(m);
         if (m == -INFINITY) m = 0.0f;        // nothing left (or NaN): exp(-inf) below, not exp(nan)
         float sum = 0.0f, dot = 0.0f;
-        if (!sigmoid) {
+        if (!SIG) {
             const float shift = -m * kLog2e;   // its rounding is a factor that all p share
+            if (__any_sync(0xFFFFFFFFu, fmaf(low, kLog2e, shift) < -125.0f)) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) p[i] = ex2(fmaf(l[i], kLog2e, shift));
+                for (int i = 0; i < V; ++i) p[i] = ex2<false>(fmaf(l[i], kLog2e, shift));
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) p[i] = ex2<true>(fmaf(l[i], kLog2e, shift));
+            }
         } else {
             // sigmoid(l) exp(-m) with m = min(max l, 0): the common factor keeps p
             // where every sigmoid underflows.  l becomes the slope 1 - sigmoid(l).
             m = fminf(m, 0.0f);
+            if (__any_sync(0xFFFFFFFFu, m < 0.0f || low < -86.0f)) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const bool up = l[i] > 0.0f;
-                const float z = ex2(-fabsf(l[i]) * kLog2e), d = rcp12(1.0f + z);
-                p[i] = (up ? 1.0f : m < 0.0f ? ex2((l[i] - m) * kLog2e) : z) * d;
-                l[i] = (up ? z : 1.0f) * d;
+                for (int i = 0; i < V; ++i) {
+                    const bool up = l[i] > 0.0f;
+                    const float z = ex2<false>(-fabsf(l[i]) * kLog2e), d = rcp12(1.0f + z);
+                    p[i] = (up ? 1.0f : ex2<false>((l[i] - m) * kLog2e)) * d;
+                    l[i] = (up ? z : 1.0f) * d;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const bool up = l[i] > 0.0f;
+                    const float z = ex2<true>(-fabsf(l[i]) * kLog2e), d = rcp12(1.0f + z);
+                    p[i] = (up ? 1.0f : z) * d;
+                    l[i] = (up ? z : 1.0f) * d;
+                }
             }
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            sum += p[i];
-            dot = fmaf(p[i], w[i], dot);
+        for (int c = 0; c < (V + 7) / 8; ++c) {
+            float w[8];
+            R::weights(s_w, lane, c, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (8 * c + i < V) {
+                    sum += p[8 * c + i];
+                    dot = fmaf(p[8 * c + i], w[i], dot);
+                }
+            }
         }
         sum = group_sum<LANES>(sum);
         dot = group_sum<LANES>(dot);
@@ -310,13 +370,20 @@ balance_main_kernel(const void *__restrict__ logits, const int32_t *__restrict__
         dot = none ? 0.0f : dot * inv;
         if (!none && lane == 0) acc += (double)(mean + dot);
         if (grad != nullptr && here) {
-            const float scale_p = g * inv;
+            const float gi = g * inv, gd = -gi * dot;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float q = (p[i] * scale_p) * (w[i] - dot);
-                l[i] = none ? 0.0f : sigmoid ? q * l[i] : q;
+            for (int c = 0; c < (V + 7) / 8; ++c) {
+                float w[8];
+                R::weights(s_w, lane, c, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (8 * c + i < V) {
+                        const float q = p[8 * c + i] * fmaf(w[i], gi, gd);
+                        p[8 * c + i] = none ? 0.0f : SIG ? q * l[8 * c + i] : q;   // 0 for NaN too where the token takes no part
+                    }
+                }
             }
-            R::store(grad, tok, E, lane, l);
+            R::store(grad, tok, E, lane, p);
         }
     }
     if (loss_part == nullptr) return;
@@ -353,7 +420,7 @@ struct Args {
     const void *logits;
     const int32_t *idx;
     double scale;
-    int sigmoid;
+    int score;
     const int32_t *part;
     int chunks;
     int32_t *counts, *routed;
@@ -367,23 +434,29 @@ struct Args {
 
 template <int DT, int LANES, int N, bool VEC>
 cudaError_t launch_main(const Shape &s, const Args &a) {
-    return launch_pdl(balance_main_kernel<DT, LANES, N, VEC>, dim3((unsigned)(s.seqs * s.main_chunks)), dim3(kMainThreads),
-                      (size_t)s.E * 4, a.stream, a.logits, a.idx, s.tokens, s.k, s.E, a.scale, a.sigmoid, a.part, a.chunks,
-                      a.counts, a.routed, a.grad_loss, a.grad, a.loss_part, a.ticket, a.loss, s.main_chunks);
+    const size_t smem = (size_t)(LANES * N * (VEC ? 8 : 1) + s.E) * 4;
+    const auto kernel = a.score == CGL_SCORE_SIGMOID ? balance_main_kernel<DT, LANES, N, VEC, true>
+                                                     : balance_main_kernel<DT, LANES, N, VEC, false>;
+    return launch_pdl(kernel, dim3((unsigned)(s.seqs * s.main_chunks)), dim3(kMainThreads), smem, a.stream, a.logits, a.idx,
+                      s.tokens, s.k, s.E, a.scale, a.part, a.chunks, a.counts, a.routed, a.grad_loss, a.grad, a.loss_part,
+                      a.ticket, a.loss, s.main_chunks);
 }
 
 template <int DT>
 cudaError_t main_by_width(const Shape &s, const Args &a) {
     if (s.E % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.grad)) & 15) == 0) {
-        switch (lanes_for(s.E)) {
-            case 1: return launch_main<DT, 1, 1, true>(s, a);
-            case 2: return launch_main<DT, 2, 1, true>(s, a);
-            case 4: return launch_main<DT, 4, 1, true>(s, a);
-            case 8: return launch_main<DT, 8, 1, true>(s, a);
-            case 16: return launch_main<DT, 16, 1, true>(s, a);
-            default:
-                return s.E <= 256 ? launch_main<DT, 32, 1, true>(s, a)
-                       : s.E <= 512 ? launch_main<DT, 32, 2, true>(s, a) : launch_main<DT, 32, 4, true>(s, a);
+        const Width w = width_for(s.tokens * s.seqs, s.E, DT);
+        switch (w.lanes * 8 + w.groups) {
+            case 1 * 8 + 1: return launch_main<DT, 1, 1, true>(s, a);
+            case 2 * 8 + 1: return launch_main<DT, 2, 1, true>(s, a);
+            case 4 * 8 + 1: return launch_main<DT, 4, 1, true>(s, a);
+            case 8 * 8 + 1: return launch_main<DT, 8, 1, true>(s, a);
+            case 8 * 8 + 2: return launch_main<DT, 8, 2, true>(s, a);
+            case 16 * 8 + 1: return launch_main<DT, 16, 1, true>(s, a);
+            case 16 * 8 + 2: return launch_main<DT, 16, 2, true>(s, a);
+            case 32 * 8 + 1: return launch_main<DT, 32, 1, true>(s, a);
+            case 32 * 8 + 2: return launch_main<DT, 32, 2, true>(s, a);
+            default: return launch_main<DT, 32, 4, true>(s, a);
         }
     }
     if (s.E <= 32) return launch_main<DT, 32, 1, false>(s, a);
@@ -404,14 +477,15 @@ cudaError_t main_by_type(int dtype, const Shape &s, const Args &a) {
 
 // The ticket (16 bytes), the blocks' loss sums, the chunks' counts.
 size_t balance_workspace_bytes(int64_t n, int k, int E, int64_t S) {
-    const Shape s = shape(n, k, E, S);
-    return 16 + round16((size_t)S * s.main_chunks * 8) + (size_t)S * s.count_chunks * (E + 1) * 4;
+    const Shape s = shape(n, k, E, S, CGL_F32), h = shape(n, k, E, S, CGL_BF16);   // types may differ in their blocks
+    const int blocks = s.main_chunks > h.main_chunks ? s.main_chunks : h.main_chunks;
+    return 16 + round16((size_t)S * blocks * 8) + (size_t)S * s.count_chunks * (E + 1) * 4;
 }
 
 cgl_status launch_balance_loss(const void *logits, int dtype, const int32_t *idx, int64_t n, int k, int E, int64_t S,
                                float alpha, int score, const float *grad_loss, float *loss, int32_t *counts,
                                int32_t *routed, void *grad, void *ws, uint32_t *status, cudaStream_t stream) {
-    const Shape s = shape(n, k, E, S);
+    const Shape s = shape(n, k, E, S, dtype);
     uint32_t *ticket = static_cast<uint32_t *>(ws);
     double *loss_part = reinterpret_cast<double *>(static_cast<uint8_t *>(ws) + 16);
     int32_t *part = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + 16 + round16((size_t)S * s.main_chunks * 8));
@@ -427,7 +501,7 @@ cgl_status launch_balance_loss_backward(const float *grad_loss, const void *logi
                                         int64_t n, int k, int E, int64_t S, float alpha, int score,
                                         const int32_t *counts, const int32_t *routed, void *grad, cudaStream_t stream) {
     if (n == 0) return CGL_OK;
-    const Shape s = shape(n, k, E, S);
+    const Shape s = shape(n, k, E, S, dtype);
     const Args a = {logits, idx, (double)alpha / ((double)S * k), score, nullptr, 0, const_cast<int32_t *>(counts),
                     const_cast<int32_t *>(routed), grad_loss, grad, nullptr, nullptr, nullptr, stream};
     return main_by_type(dtype, s, a) == cudaSuccess ? CGL_OK : CGL_ECUDA;
