@@ -159,6 +159,8 @@ def _dev(t: torch.Tensor, name: str, dtype=None, ndim=None):
 
 
 def _opts(num_sms: int = 0, capacity: int = 0, pow2_scales: bool = False, scratch: Optional[torch.Tensor] = None):
+    if scratch is None and num_sms == 0 and capacity == 0 and not pow2_scales:
+        return None   # NULL: all fields zero
     sp = None
     if scratch is not None:
         if not scratch.is_cuda or scratch.numel() * scratch.element_size() < 16 or not scratch.is_contiguous():
@@ -466,11 +468,13 @@ _SCORES = {"softmax": 0, "sigmoid": 1}                              # cgl_score
 
 def _launch(where: str, fn, device, stream, *args):
     """fn(*args, stream) with `device` current (its own current stream unless one is given)."""
-    if device.index != torch.cuda.current_device():
+    # the raw stream: torch.cuda.current_stream() makes a Stream object, 4 us of a small call's 15
+    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
+    if device.index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
-            code = fn(*args, _stream(stream))
+            code = fn(*args, raw)
     else:
-        code = fn(*args, _stream(stream))
+        code = fn(*args, raw)
     if code != OK:
         raise CglError(code, where)
 

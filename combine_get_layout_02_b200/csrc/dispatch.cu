@@ -20,12 +20,14 @@
 // read it (bulk wait_group.read).  One lane of each 128-value block stores its
 // fp32 scale.
 //
+// MXFP4 (format in mxfp4.cuh), hidden <= 16384: the same staging with a row of
+// codes and a row of scale bytes, two lanes a block of 32.
 // BF16, hidden <= 8192 and a multiple of 16: the same staging with BF16 rows.
 // FP8 above 16384 and BF16 otherwise: one thread per 16 or 8 values of the
 // flattened (token, chunk) grid, 16-byte loads and one 16-byte store per copy.  Every
 // kernel launches with programmatic dependent launch: blocks start while the
 // layout drains and wait (griddepcontrol) before their first global read.
-#include "common.cuh"
+#include "mxfp4.cuh"
 #include "launch.h"
 
 namespace cgl {
@@ -35,6 +37,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxBulkHidden = 16384;    // one thread per 16 values: at most 1024 threads
 constexpr int kBulkThreadsPerSM = 1024;  // CTAs per SM of the bulk kernels = this / block size
+constexpr int kMxThreadsPerSM = 2048;    // of the MXFP4 one, whose rows are half as long
 constexpr int kMaxBulkHiddenBf16 = 8192; // two staged BF16 rows stay within 32 KiB of shared memory
 
 // Dynamic token order: thread 0 of each CTA claims tokens from a 64-bit word,
@@ -220,6 +223,129 @@ dispatch_fp8_kernel(const uint16_t *__restrict__ x, int64_t n, int h, int k,
     if (bad) report(status, kErrRange);
 }
 
+// MXFP4 rows through the same staging: one thread per 16 values, two lanes a
+// block, k bulk copies of h / 2 bytes of codes and, where h / 32 and recv_scale
+// allow 16-byte copies (bulk_scales), k of the scale bytes; else the even lanes
+// store the scale bytes themselves.
+__global__ void __launch_bounds__(1024)
+dispatch_mxfp4_bulk_kernel(const uint16_t *__restrict__ x, int64_t n, int h, int k, const int32_t *__restrict__ dst_pos,
+                           uint8_t *__restrict__ recv_x, uint8_t *__restrict__ recv_scale, int64_t recv_rows,
+                           int bulk_scales, int pitch, unsigned long long *claim, uint32_t *status) {
+    extern __shared__ __align__(128) uint8_t rows_smem[];   // [2][pitch]: codes, then scale bytes
+    __shared__ int64_t s_next[2];      // claimed tokens (dynamic order, as in the FP8 kernel)
+    griddep_wait();
+    const int chunks = h >> 4, nblk = h >> 5;
+    const int c = threadIdx.x;
+    const bool active = c < chunks;
+    bool bad = false;
+    int buf = 0;
+    int64_t t = blockIdx.x, tn = t + gridDim.x;
+    unsigned long long pend = (unsigned long long)n;   // thread 0: the claim in flight (raw)
+    if (claim != nullptr) {
+        if (threadIdx.x == 0) {
+            s_next[0] = take_claim(atomicAdd(claim, 1ull), n, bad);
+            s_next[1] = take_claim(atomicAdd(claim, 1ull), n, bad);
+        }
+        __syncthreads();
+        t = s_next[0];
+        tn = t < n ? s_next[1] : n;
+        if (threadIdx.x == 0 && tn < n) pend = atomicAdd(claim, 1ull);
+    }
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (t < n && active) {
+        a = ld_nc_v4(x + t * h + (int64_t)c * 16);
+        b = ld_nc_v4(x + t * h + (int64_t)c * 16 + 8);
+    }
+    for (int it = 0; t < n; buf ^= 1, ++it) {
+        uint4 an = make_uint4(0, 0, 0, 0), bn = an;   // the next token's chunk, in flight
+        if (tn < n && active) {
+            an = ld_nc_v4(x + tn * h + (int64_t)c * 16);
+            bn = ld_nc_v4(x + tn * h + (int64_t)c * 16 + 8);
+        }
+        uint32_t byte;
+        const uint2 q = mx_quantize16(a, b, byte);
+        uint8_t *row = rows_smem + buf * pitch;
+        if (threadIdx.x == 0) {
+            bulk_wait_read<1>();   // copies from two tokens ago have read `row`
+            if (claim != nullptr) s_next[it & 1] = take_claim(pend, n, bad);
+        }
+        __syncthreads();
+        if (active) {
+            *reinterpret_cast<uint2 *>(row + c * 8) = q;
+            if ((c & 1) == 0) row[(h >> 1) + (c >> 1)] = (uint8_t)byte;
+        }
+        fence_proxy_async();
+        __syncthreads();
+        int64_t tnn = tn + gridDim.x;   // the token after the next one
+        if (claim != nullptr) {
+            tnn = tn < n ? s_next[it & 1] : n;
+            if (threadIdx.x == 0) pend = tnn < n ? atomicAdd(claim, 1ull) : (unsigned long long)n;
+        }
+        const int32_t *dp = dst_pos + t * k;
+        if (threadIdx.x == 0) {
+            for (int j = 0; j < k; ++j) {
+                const int32_t r = __ldg(dp + j);
+                if (r < 0) continue;
+                if (r >= recv_rows) { bad = true; continue; }
+                bulk_store(recv_x + (int64_t)r * (h >> 1), row, (uint32_t)(h >> 1));
+                if (bulk_scales) bulk_store(recv_scale + (int64_t)r * nblk, row + (h >> 1), (uint32_t)nblk);
+            }
+            bulk_commit();
+        }
+        if (!bulk_scales && active && (c & 1) == 0) {
+            for (int j = 0; j < k; ++j) {
+                const int32_t r = __ldg(dp + j);
+                if (r >= 0 && r < recv_rows) recv_scale[(int64_t)r * nblk + (c >> 1)] = (uint8_t)byte;
+            }
+        }
+        a = an;
+        b = bn;
+        t = tn;
+        tn = tnn;
+    }
+    if (threadIdx.x == 0) {
+        if (claim != nullptr) claims_done(claim);   // before the wait, which hides the atomic
+        bulk_wait_all();
+    }
+    if (bad) report(status, kErrRange);
+}
+
+// Past 16384 values: one thread per 8 values of the flattened (token, chunk) grid.
+__global__ void __launch_bounds__(kThreads)
+dispatch_mxfp4_kernel(const uint16_t *__restrict__ x, int64_t n, int h, int k, const int32_t *__restrict__ dst_pos,
+                      uint8_t *__restrict__ recv_x, uint8_t *__restrict__ recv_scale, int64_t recv_rows,
+                      uint32_t *status) {
+    griddep_wait();
+    const int per_row = h >> 3, nblk = h >> 5;
+    const int64_t total = n * per_row;
+    const int64_t stride = (int64_t)gridDim.x * kThreads;
+    bool bad = false;
+    for (int64_t base = (int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31); base < total; base += stride) {
+        const int64_t g = base + (threadIdx.x & 31);
+        const bool active = g < total;
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (active) {
+            Vec8<CGL_BF16> in;
+            in.load(x, g);
+            in.widen(v);
+        }
+        uint32_t byte;
+        const uint32_t q = mx_quantize8(v, byte);
+        if (!active) continue;
+        const int64_t t = g / per_row;
+        const int c = (int)(g - t * per_row);
+        const int32_t *dp = dst_pos + t * k;
+        for (int j = 0; j < k; ++j) {
+            const int32_t row = __ldg(dp + j);
+            if (row < 0) continue;
+            if (row >= recv_rows) { bad = true; continue; }
+            reinterpret_cast<uint32_t *>(recv_x)[(int64_t)row * per_row + c] = q;
+            if ((c & 3) == 0) recv_scale[(int64_t)row * nblk + (c >> 2)] = (uint8_t)byte;
+        }
+    }
+    if (bad) report(status, kErrRange);
+}
+
 // BF16 rows through the same staging: one thread per 16 values, k bulk copies per token.
 __global__ void __launch_bounds__(1024)
 dispatch_bf16_bulk_kernel(const uint16_t *__restrict__ x, int64_t n, int h, int k,
@@ -368,6 +494,33 @@ cgl_status launch_dispatch_bf16(const uint16_t *x, int64_t n, int h, int k, cons
     if (grid <= 0) return CGL_ECUDA;
     const cudaError_t err = launch_pdl(dispatch_bf16_kernel, dim3(grid), dim3(kThreads), 0, stream, x, n,
                                        h, k, dst_pos, recv_x, recv_rows, status);
+    return err == cudaSuccess ? CGL_OK : CGL_ECUDA;
+}
+
+cgl_status launch_dispatch_mxfp4(const uint16_t *x, int64_t n, int h, int k, const int32_t *dst_pos, uint8_t *recv_x,
+                                 uint8_t *recv_scale, int64_t recv_rows, int num_sms, uint32_t *status,
+                                 cudaStream_t stream, unsigned long long *claim) {
+    if (n == 0) return CGL_OK;
+    if (h <= kMaxBulkHidden) {
+        const int threads = (h / 16 + 31) / 32 * 32;
+        const int pitch = (h / 2 + h / 32 + 15) / 16 * 16;
+        const int bulk_scales = h % 512 == 0 && (reinterpret_cast<uintptr_t>(recv_scale) & 15) == 0;
+        const int grid = persistent_grid((const void *)dispatch_mxfp4_bulk_kernel, threads, (size_t)2 * pitch,
+                                         kMxThreadsPerSM / threads, num_sms, n);
+        if (grid <= 0) return CGL_ECUDA;
+        // few tokens a CTA: the claims cost more than the even load gives (1024
+        // tokens of 7168, top-8: 9.5 against 7.5 us; 4096: 32.3 against 34.5)
+        if (n <= 4 * (int64_t)grid) claim = nullptr;
+        const cudaError_t err = launch_pdl(dispatch_mxfp4_bulk_kernel, dim3(grid), dim3(threads), (size_t)2 * pitch, stream,
+                                           x, n, h, k, dst_pos, recv_x, recv_scale, recv_rows, bulk_scales, pitch, claim,
+                                           status);
+        return err == cudaSuccess ? CGL_OK : CGL_ECUDA;
+    }
+    const int64_t work = n * (h / 8);
+    const int grid = copy_grid((const void *)dispatch_mxfp4_kernel, kThreads, (work + kThreads - 1) / kThreads, num_sms);
+    if (grid <= 0) return CGL_ECUDA;
+    const cudaError_t err = launch_pdl(dispatch_mxfp4_kernel, dim3(grid), dim3(kThreads), 0, stream, x, n, h, k, dst_pos,
+                                       recv_x, recv_scale, recv_rows, status);
     return err == cudaSuccess ? CGL_OK : CGL_ECUDA;
 }
 

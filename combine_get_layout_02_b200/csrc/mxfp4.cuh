@@ -75,6 +75,24 @@ __device__ __forceinline__ void cvt_f32x8_e2m1(uint32_t codes, float v[8]) {
             : "r"(h[i]));
 }
 
+// Four E2M1 codes -> four floats (exact).
+__device__ __forceinline__ void cvt_f32x4_e2m1(uint16_t codes, float v[4]) {
+    uint32_t h[2];
+    asm("{\n"
+        ".reg .b8 b0, b1;\n"
+        "mov.b16 {b0, b1}, %2;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        "}"
+        : "=r"(h[0]), "=r"(h[1])
+        : "h"(codes));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v[2 * i] = __half2float(__ushort_as_half((unsigned short)(h[i] & 0xFFFFu)));
+        v[2 * i + 1] = __half2float(__ushort_as_half((unsigned short)(h[i] >> 16)));
+    }
+}
+
 // Eight values of a row by type: loaded as 16-byte words, widened exactly.
 template <int DT>
 struct Vec8;
@@ -157,6 +175,26 @@ __device__ __forceinline__ uint32_t mx_quantize8(float v[8], uint32_t &byte) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) q[j] = __fmul_rn(v[j], inv);
     return cvt_e2m1x8(q);
+}
+
+// Quantise this lane's sixteen BF16 values (a, b); each aligned pair of lanes holds one block.
+__device__ __forceinline__ uint2 mx_quantize16(const uint4 a, const uint4 b, uint32_t &byte) {
+    // The largest |value| by its bits, NaN above everything: pairs compared as 16-bit integers.
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    uint32_t m = __vmaxu2(__vmaxu2(__vmaxu2(a.x & kAbs, a.y & kAbs), __vmaxu2(a.z & kAbs, a.w & kAbs)),
+                          __vmaxu2(__vmaxu2(b.x & kAbs, b.y & kAbs), __vmaxu2(b.z & kAbs, b.w & kAbs)));
+    m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    byte = mx_scale_byte(max(m << 16, m & 0xFFFF0000u));
+    if (byte == 255u) return make_uint2(0u, 0u);
+    const float inv = mx_inverse(byte);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[2 * i] = __fmul_rn(bf16_lo(w[i]), inv);
+        v[2 * i + 1] = __fmul_rn(bf16_hi(w[i]), inv);
+    }
+    return make_uint2(cvt_e2m1x8(v), cvt_e2m1x8(v + 8));
 }
 
 }  // namespace cgl
