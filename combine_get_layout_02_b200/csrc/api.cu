@@ -382,7 +382,7 @@ cgl_status cgl_matmul_mxfp4(const uint8_t *a, const uint8_t *a_scale, int64_t nu
                             const uint8_t *w_scale, int E, int F, int K, const int32_t *expert_offset, uint16_t *y,
                             const cgl_opts *opts, uint32_t *status_dev, void *stream) {
     if (E < 1 || E > kMaxExperts || F < 1 || F > (1 << 20) || K < 32 || K % 32 != 0 || K > (1 << 20) || num_rows < 0 ||
-        num_rows >= ((int64_t)1 << 31))
+        num_rows > ((int64_t)1 << 31) - 4096)
         return CGL_EINVAL;
     const int cap = opt_cap(opts);
     if (cap < 0 || opt_sms(opts) < 0 || !flags_ok(opts)) return CGL_EINVAL;

@@ -43,7 +43,7 @@ constexpr int kStageK = 256;              // values a stage
 constexpr int kChunk = 4;                 // stages a chunk of scales (1024 values, 32 bytes a row)
 constexpr int kM = 128;                   // features a tile
 constexpr int kMaxStages = 12;
-constexpr int kMaxNt = 192;               // 2 accumulators of 192 columns + 5 stages' scales: 504 of 512 columns
+constexpr int kMaxNt = 208;               // 2 accumulators of 208 columns + 4 stages' scales = 512 columns
 constexpr int kOutBytes = 4 * 2048;       // the epilogue's 32 x 32 BF16 blocks, one a warp
 constexpr size_t kSmemLimit = 226 * 1024; // dynamic part: 227 KiB less the static part
 constexpr uint32_t kABytes = kM * kStageK / 2;
@@ -250,8 +250,8 @@ struct Tiles {
     const int32_t *first, *row0s, *counts;   // shared: tiles' prefix sums over experts, rows
     int ftiles, rank, last;                  // last: tiles of rows in all
     int q, ft, dq, dft;                      // the tile of rows and of features, and the step from one tile to the next
-    int e, end, per, at0;                    // expert; first tile of rows behind it, rows a tile, row0 of a tile q: at0 + q * per
-    int f0, row0, n, stop;
+    int e, begin, end, per, rows0, stop;     // expert: its tiles of rows, rows a tile, its rows
+    int f0, row0, n;
 
     __device__ __forceinline__ void start(const Params &p, const int32_t *tables) {
         first = tables;
@@ -263,7 +263,7 @@ struct Tiles {
         const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
         q = pair / ftiles, ft = pair % ftiles;
         dq = pairs / ftiles, dft = pairs % ftiles;
-        e = -1, end = 0;
+        e = -1, begin = end = 0;
         place();
     }
     __device__ __forceinline__ bool valid() const { return q < last; }
@@ -277,18 +277,17 @@ struct Tiles {
     __device__ __forceinline__ void place() {
         if (q >= last) return;
         if (q >= end) {
-            int begin = end;
             do {
                 begin = end;
                 end = first[++e + 1];
             } while (end <= q);
-            const int m = counts[e];
-            per = ((m + end - begin - 1) / (end - begin) + 15) & ~15;
-            at0 = row0s[e] - begin * per;
-            stop = row0s[e] + m;
+            const uint32_t m = counts[e], parts = end - begin;
+            per = (int)(((m + parts - 1) / parts + 15) & ~15u);
+            rows0 = row0s[e];
+            stop = rows0 + (int)m;
         }
         f0 = (2 * ft + rank) * kM;
-        row0 = at0 + q * per;
+        row0 = rows0 + (q - begin) * per;
         n = stop - row0 < per ? stop - row0 : per;
     }
     __device__ __forceinline__ int columns() const { return (n + 15) & ~15; }
@@ -378,7 +377,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     if (warp == 0) {
         const int per = (p.E + 31) / 32, e0 = lane * per, e1 = e0 + per < p.E ? e0 + per : p.E;
         int sum = 0;
-        for (int e = e0; e < e1; ++e) sum += (tables[2 * p.E + 1 + e] + p.nt - 1) / p.nt;
+        for (int e = e0; e < e1; ++e) sum += ((uint32_t)tables[2 * p.E + 1 + e] + p.nt - 1) / p.nt;
         int before = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -388,7 +387,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         before -= sum;
         for (int e = e0; e < e1; ++e) {
             tables[e] = before;
-            before += (tables[2 * p.E + 1 + e] + p.nt - 1) / p.nt;
+            before += ((uint32_t)tables[2 * p.E + 1 + e] + p.nt - 1) / p.nt;
         }
         if (e0 < p.E && e1 == p.E) tables[p.E] = before;
     }

@@ -487,9 +487,13 @@ cgl_status cgl_dispatch_mxfp4(const uint16_t *x, int64_t num_tokens, int hidden,
  *   no expert may hold anything); w uint8 [E, out, in/2], w_scale uint8
  *   [E, out, in/32]; expert_offset int32 [E + 1].
  * Out (device): y BF16 [num_rows, out]; rows of no expert are NOT written.
- * Requires in % 32 == 0; in, out <= 2^20; num_rows < 2^31, and >= E * capacity
- * when padded; a and w 16-byte aligned, y 2-byte.  opts: capacity, num_sms.
- * Device errors: CGL_ERANGE when offsets run backwards or past num_rows (clamped).
+ * Requires in % 32 == 0; in, out <= 2^20; num_rows <= 2^31 - 4096, and >= E *
+ * capacity when padded; a and w 16-byte aligned, y 2-byte (16-byte aligned rows
+ * are stored faster).  opts: capacity, num_sms (blocks work in pairs: at least
+ * two SMs).
+ * Device errors: CGL_ERANGE when offsets run backwards or past num_rows
+ * (clamped); CGL_ETIMEOUT if a bounded wait (about a second) inside a block pair
+ * gives up, y then undefined.
  */
 cgl_status cgl_matmul_mxfp4(const uint8_t *a, const uint8_t *a_scale, int64_t num_rows, const uint8_t *w,
                             const uint8_t *w_scale, int num_experts, int out_features, int in_features,
