@@ -61,6 +61,7 @@ struct Params {
     int box;         // token rows a TMA box
     int stages;
     int chunks;      // chunks of scales in shared memory
+    int split;       // pairs that share a tile, each a part of K (one cluster)
     int wide;        // y's rows allow 16-byte stores
     uint32_t stage_bytes, chunk_bytes;
 };
@@ -87,10 +88,10 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// The same barrier in the pair's first block.
-__device__ __forceinline__ uint32_t in_first(uint32_t bar) {
+// The same shared-memory address in another block of the cluster.
+__device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
 // Arrive there.  What the arrival announces is read by the tensor core of the
@@ -181,9 +182,9 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 // Arrive, once this thread's MMAs and copies so far have ended, at a barrier of both blocks or of this one.
-__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+__device__ __forceinline__ void mma_commit_both(uint32_t bar, uint32_t lead) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"((uint16_t)3)
+                 "h"((uint16_t)(3u << lead))
                  : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -260,7 +261,7 @@ struct Tiles {
         ftiles = (p.F + 2 * kM - 1) / (2 * kM);
         rank = (int)(blockIdx.x & 1);
         last = first[p.E];
-        const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+        const int per_cluster = 2 * p.split, pair = blockIdx.x / per_cluster, pairs = gridDim.x / per_cluster;
         q = pair / ftiles, ft = pair % ftiles;
         dq = pairs / ftiles, dft = pairs % ftiles;
         e = -1, begin = end = 0;
@@ -320,9 +321,84 @@ __device__ __forceinline__ void load_scales(const uint8_t *row, int at, int byte
     }
 }
 
+// ---- results ---------------------------------------------------------------------------------
+
+// Another pair's sums of a tile: for each 32 columns and each epilogue warp its
+// 32 registers, 128 bytes (a lane each) a register.
+__host__ __device__ __forceinline__ uint32_t part_bytes(int nt) { return (uint32_t)((nt + 31) / 32) * (4 * 32 * 32 * 4); }
+__device__ __forceinline__ int part_index(int column, int quarter, int lane) { return ((column / 32) * 4 + quarter) * 1024 + lane; }
+
+__device__ __forceinline__ void dump_tile(const Tiles &tile, uint32_t d, int quarter, int lane, uint32_t part) {
+    d += (uint32_t)(quarter * 32) << 16;
+    const int columns = tile.columns();
+    for (int c = 0; c < columns; c += 32) {
+        uint32_t r[2][16];
+        __syncwarp();
+        tmem_ld_16x32(d + c, r[0]);
+        tmem_ld_16x32(d + c + (16u << 16), r[1]);
+        tmem_ld_wait();
+        const uint32_t to = part + 4 * part_index(c, quarter, lane);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 128 * j), "r"(r[j / 16][j % 16]) : "memory");
+    }
+}
+
+// A warp's 32 features of the tile, `parts` other pairs' sums added to this one's, as BF16 rows of y.
+__device__ __forceinline__ void store_tile(const Params &p, const Tiles &tile, uint32_t d, int quarter, int lane, uint32_t out,
+                                           uint8_t *out_ptr, const float *part, int parts) {
+    const int f = tile.f0 + quarter * 32;
+    const uint32_t mine = out + quarter * 2048;
+    const uint8_t *mine_ptr = out_ptr + quarter * 2048;
+    d += (uint32_t)(quarter * 32) << 16;
+    const int columns = tile.columns();
+    for (int c = 0; c < columns; c += 32) {
+        // 32 features x 32 tokens -> [token][feature], 64 bytes a token, its
+        // 16-byte pieces exchanged by the token's number so that neither side
+        // meets a bank twice
+        uint32_t r[2][16];
+        tmem_ld_16x32(d + c, r[0]);
+        tmem_ld_16x32(d + c + (16u << 16), r[1]);
+        tmem_ld_wait();
+        for (int i = 0; i < parts; ++i) {
+            const float *q = part + (size_t)i * (part_bytes(p.nt) / 4) + part_index(c, quarter, lane);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j / 16][j % 16] = __float_as_uint(__uint_as_float(r[j / 16][j % 16]) + q[32 * j]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int u = 0; u < 4; u += 2) {
+                const int token = 8 * (u + (lane >> 4)) + (lane & 7), piece = 2 * h + ((lane >> 3) & 1);
+                uint32_t b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    b[i] = cvt_bf16x2(__uint_as_float(r[h][4 * u + 2 * i]), __uint_as_float(r[h][4 * u + 2 * i + 1]));
+                stmatrix_trans(mine + token * 64 + ((piece ^ ((token >> 1) & 3)) << 4), b[0], b[1], b[2], b[3]);
+            }
+        __syncwarp();
+        const int there = tile.n - c < 32 ? tile.n - c : 32;
+        uint16_t *y = p.y + ((int64_t)tile.row0 + c) * p.F + f;
+        if (p.wide) {
+            const int piece = lane & 3;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int token = 8 * i + (lane >> 2);
+                const uint4 v = *reinterpret_cast<const uint4 *>(mine_ptr + token * 64 + ((piece ^ ((token >> 1) & 3)) << 4));
+                if (token < there && f + 8 * piece < p.F) *reinterpret_cast<uint4 *>(y + (int64_t)token * p.F + 8 * piece) = v;
+            }
+        } else if (f + lane < p.F) {
+            for (int token = 0; token < there; ++token)
+                y[(int64_t)token * p.F + lane] = *reinterpret_cast<const uint16_t *>(
+                    mine_ptr + token * 64 + (((lane >> 3) ^ ((token >> 1) & 3)) << 4) + 2 * (lane & 7));
+        }
+        __syncwarp();
+    }
+}
+
 // ---- the kernel ------------------------------------------------------------------------------
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     // full, sffull and accfree count for the pair, in its first block; empty, sffree and accfull are told to both
@@ -332,7 +408,8 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     volatile int *abort = &s_abort_word;
 
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const bool first = cluster_rank() == 0;
+    const uint32_t rank = cluster_rank(), lead = rank & ~1u;   // lead: the pair's first block
+    const bool first = rank == lead;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
     const uint32_t sf_ring = ring + p.stages * p.stage_bytes, out = sf_ring + p.chunks * p.chunk_bytes;
@@ -396,9 +473,13 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const int ksteps = (p.K + kStageK - 1) / kStageK;
+    // this pair's stages [k0, k1), whole chunks of scales
+    const int ksteps = (p.K + kStageK - 1) / kStageK, kchunks = (ksteps + kChunk - 1) / kChunk;
+    const int c0 = kchunks * (int)(rank >> 1) / p.split, c1 = kchunks * (int)((rank >> 1) + 1) / p.split;
+    const int k0 = c0 * kChunk, k1 = c1 * kChunk < ksteps ? c1 * kChunk : ksteps;
 
     Tiles tile;
+    bool done = false;
     if (warp == 0 || warp == 9) {
         int s = 0;
         uint32_t phase = 0;
@@ -407,10 +488,10 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             const int half = tile.columns() / 2, boxes = (half + p.box - 1) / p.box;
             const uint32_t box_bytes = p.box * (kStageK / 2);
             const int row0 = tile.row0 + tile.rank * half;
-            for (int k = 0; k < ksteps; ++k) {
+            for (int k = k0; k < k1; ++k) {
                 ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_empty[s]), phase ^ 1, abort, p.status));
                 if (!ok) break;
-                const uint32_t base = ring + s * p.stage_bytes, bar = in_first(smem_u32(&s_full[s]));
+                const uint32_t base = ring + s * p.stage_bytes, bar = in_block(smem_u32(&s_full[s]), lead);
                 if (warp == 0) {
                     if (elect_one()) {
                         if (first) bar_expect(smem_u32(&s_full[s]), 2 * (kABytes + boxes * box_bytes));
@@ -447,7 +528,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 const uint32_t i0 = instr_desc(tile.columns(), 0), i2 = instr_desc(tile.columns(), 2);
                 ok = bar_wait(smem_u32(&s_accfree[acc]), accphase ^ 1, abort, p.status);
                 const uint32_t d = tmem + acc * p.nt;
-                for (int k = 0; k < ksteps; ++k) {
+                for (int k = k0; k < k1; ++k) {
                     if (!ready) ok = ok && bar_wait(full0 + 8 * s, phase, abort, p.status);
                     tc_fence_after();
                     const uint32_t empty = empty0 + 8 * s, ta = tsf, tb = tsf + 8;
@@ -459,11 +540,11 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
 #pragma unroll
                         for (int i = 0; i < 4; ++i)     // 64 values: 32 bytes (two units) of each row
                             mma_mxf4(d, da + 2 * i, db + 2 * i, (i & 1) ? i2 : i0, ta + 4 * (i >> 1), tb + 4 * (i >> 1) * nb,
-                                     i > 0 || k > 0);
-                        mma_commit_both(empty);
+                                     i > 0 || k > k0);
+                        mma_commit_both(empty, lead);
                     }
                 }
-                if (elect_one() && ok) mma_commit_both(smem_u32(&s_accfull[acc]));
+                if (elect_one() && ok) mma_commit_both(smem_u32(&s_accfull[acc]), lead);
                 any = true;
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 acc ^= 1;
@@ -473,13 +554,13 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             uint32_t ch = 0, chphase = 0;
             for (; ok && tile.valid(); tile.next()) {
                 const bool two = tile.columns() > 128;
-                for (int k = 0; k < ksteps; k += kChunk) {
+                for (int k = k0; k < k1; k += kChunk) {
                     ok = ok && bar_wait(smem_u32(&s_sffull[ch]), chphase, abort, p.status);
                     const uint32_t sf = sf_ring + ch * p.chunk_bytes;
                     const uint64_t sa = desc_scales(sf), sb = desc_scales(sf + kChunkA);
 #pragma unroll
                     for (int j = 0; j < kChunk; ++j) {
-                        if (k + j >= ksteps) break;
+                        if (k + j >= k1) break;
                         ok = ok && bar_wait(empty0 + 8 * s, phase ^ 1, abort, p.status);
                         tc_fence_after();
                         if (elect_one() && ok) {
@@ -494,7 +575,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                         ++s, tsf += sf_cols;
                         if (s == stages) s = 0, tsf = sf0, phase ^= 1;
                     }
-                    if (elect_one() && ok) mma_commit_both(smem_u32(&s_sffree[ch]));
+                    if (elect_one() && ok) mma_commit_both(smem_u32(&s_sffree[ch]), lead);
                     any = true;
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
@@ -514,8 +595,8 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         const bool weights = warp == 2;
         const int block = warp == 8 ? 1 : 0;   // 128-row block of the token side
         if (weights || block < p.nb) {
-            const int row_bytes = p.K / 32, chunks = (ksteps + kChunk - 1) / kChunk;
-            int ch = 0, chunk = 0;
+            const int row_bytes = p.K / 32;
+            int ch = 0, chunk = c0;
             uint32_t phase = 0;
             uint32_t v[4][8], nv[4][8];
             const auto load = [&](const Tiles &t, int c, uint32_t (&to)[4][8]) {
@@ -552,13 +633,13 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 Tiles second = tile;
                 second.next();
                 to_l2(second);
-                load(tile, 0, v);
+                load(tile, c0, v);
             }
             while (ok && tile.valid()) {
                 Tiles ahead = tile;
                 int ahead_chunk = chunk + 1;
-                if (ahead_chunk == chunks) {
-                    ahead_chunk = 0;
+                if (ahead_chunk == c1) {
+                    ahead_chunk = c0;
                     ahead.next();
                     Tiles after = ahead;
                     after.next();
@@ -574,7 +655,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                         *reinterpret_cast<uint4 *>(to + j * step) = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
                     fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0) bar_arrive_remote(in_first(smem_u32(&s_sffull[ch])));
+                    if (lane == 0) bar_arrive_remote(in_block(smem_u32(&s_sffull[ch]), lead));
                     if (++ch == p.chunks) ch = 0, phase ^= 1;
                 }
 #pragma unroll
@@ -586,59 +667,37 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             }
         }
     } else if (warp >= 4 && warp < 8) {
-        const int quarter = warp & 3;
-        const uint32_t mine = out + quarter * 2048;
-        const uint8_t *mine_ptr = out_ptr + quarter * 2048;
         int acc = 0;
         uint32_t accphase = 0;
         for (tile.start(p, tables); tile.valid(); tile.next()) {
-            if (!__all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_accfull[acc]), accphase, abort, p.status))) break;
+            done = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_accfull[acc]), accphase, abort, p.status));
+            if (!done || p.split > 1) break;
             tc_fence_after();
-            const int f = tile.f0 + quarter * 32;
-            const uint32_t d = tmem + acc * p.nt + ((uint32_t)(quarter * 32) << 16);
-            const int columns = tile.columns();
-            for (int c = 0; c < columns; c += 32) {
-                // 32 features x 32 tokens -> [token][feature], 64 bytes a token, its
-                // 16-byte pieces exchanged by the token's number so that neither side
-                // meets a bank twice
-                uint32_t r[2][16];
-                tmem_ld_16x32(d + c, r[0]);
-                tmem_ld_16x32(d + c + (16u << 16), r[1]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int u = 0; u < 4; u += 2) {
-                        const int token = 8 * (u + (lane >> 4)) + (lane & 7), piece = 2 * h + ((lane >> 3) & 1);
-                        uint32_t b[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            b[i] = cvt_bf16x2(__uint_as_float(r[h][4 * u + 2 * i]), __uint_as_float(r[h][4 * u + 2 * i + 1]));
-                        stmatrix_trans(mine + token * 64 + ((piece ^ ((token >> 1) & 3)) << 4), b[0], b[1], b[2], b[3]);
-                    }
-                __syncwarp();
-                const int there = tile.n - c < 32 ? tile.n - c : 32;
-                uint16_t *y = p.y + ((int64_t)tile.row0 + c) * p.F + f;
-                if (p.wide) {
-                    const int piece = lane & 3;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int token = 8 * i + (lane >> 2);
-                        const uint4 v = *reinterpret_cast<const uint4 *>(mine_ptr + token * 64 + ((piece ^ ((token >> 1) & 3)) << 4));
-                        if (token < there && f + 8 * piece < p.F) *reinterpret_cast<uint4 *>(y + (int64_t)token * p.F + 8 * piece) = v;
-                    }
-                } else if (f + lane < p.F) {
-                    for (int token = 0; token < there; ++token)
-                        y[(int64_t)token * p.F + lane] = *reinterpret_cast<const uint16_t *>(
-                            mine_ptr + token * 64 + (((lane >> 3) ^ ((token >> 1) & 3)) << 4) + 2 * (lane & 7));
-                }
-                __syncwarp();
-            }
+            store_tile(p, tile, tmem + acc * p.nt, warp & 3, lane, out, out_ptr, nullptr, 0);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive_remote(in_first(smem_u32(&s_accfree[acc])));
+            if (lane == 0) bar_arrive_remote(in_block(smem_u32(&s_accfree[acc]), lead));
             acc ^= 1;
             if (acc == 0) accphase ^= 1;
+        }
+    }
+    if (p.split > 1) {
+        // One tile a cluster.  Once every pair's MMAs have ended the rings are free:
+        // the others lay their sums into the first pair's, register by register, and
+        // it adds them to its own in the pairs' order.
+        __syncwarp();
+        cluster_sync();
+        const bool epilogue = warp >= 4 && warp < 8 && done;   // done: this pair's part of a tile is in TMEM
+        if (epilogue && rank >= 2) {
+            tc_fence_after();
+            const uint32_t part = in_block(ring + (rank / 2 - 1) * part_bytes(p.nt), rank & 1);
+            dump_tile(tile, tmem, warp & 3, lane, part);
+        }
+        __syncwarp();
+        cluster_sync();
+        if (epilogue && rank < 2) {
+            tc_fence_after();
+            store_tile(p, tile, tmem, warp & 3, lane, out, out_ptr, reinterpret_cast<const float *>(ring_ptr), p.split - 1);
         }
     }
     __syncwarp();
@@ -714,9 +773,30 @@ cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows
     const int64_t most = ((rows + p.nt - 1) / p.nt + (rows < E ? rows : E)) * ftiles;   // tiles there can be
     int64_t pairs = (num_sms > 0 && num_sms < sms ? num_sms : sms) / 2;
     if (pairs < 1) pairs = 1;
+    // Where the tiles leave three quarters or half of the pairs without work, four
+    // or two pairs share one, a part of K each (at least one chunk of scales), as
+    // long as their sums fit into the first pair's ring.
+    p.split = 1;
+    for (int split = 4; split > 1 && p.split == 1; split /= 2)
+        if (most * split <= pairs && (K + kStageK * kChunk - 1) / (kStageK * kChunk) >= split &&
+            (split - 1) * part_bytes(p.nt) <= (uint32_t)stages * p.stage_bytes)
+            p.split = split;
     if (pairs > most) pairs = most;
-    return launch_pdl(matmul_mxfp4_kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), smem, stream, map_a, map_w, p) == cudaSuccess
-               ? CGL_OK : CGL_ECUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs * p.split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2 * p.split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, matmul_mxfp4_kernel, map_a, map_w, p) == cudaSuccess ? CGL_OK : CGL_ECUDA;
 }
 
 }  // namespace cgl
