@@ -416,24 +416,26 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     uint8_t *sf_ptr = ring_ptr + (size_t)p.stages * p.stage_bytes, *out_ptr = sf_ptr + (size_t)p.chunks * p.chunk_bytes;
     int32_t *tables = reinterpret_cast<int32_t *>(out_ptr + kOutBytes);
 
-    if (threadIdx.x == 0) {
-        s_abort_word = 0;
-        for (int i = 0; i < p.stages; ++i) {
-            bar_init(smem_u32(&s_full[i]), 2);   // the copies' bytes, the scales in TMEM
-            bar_init(smem_u32(&s_empty[i]), 1);
+    if (warp == 0) {   // a lane each: one thread alone took 1000 cycles
+        if (lane < p.stages) {
+            bar_init(smem_u32(&s_full[lane]), 2);   // the copies' bytes, the scales in TMEM
+            bar_init(smem_u32(&s_empty[lane]), 1);
         }
-        for (int i = 0; i < p.chunks; ++i) {
-            bar_init(smem_u32(&s_sffull[i]), 2 * (1 + p.nb));   // the scale warps of both blocks
-            bar_init(smem_u32(&s_sffree[i]), 1);
+        if (lane < p.chunks) {
+            bar_init(smem_u32(&s_sffull[lane]), 2 * (1 + p.nb));   // the scale warps of both blocks
+            bar_init(smem_u32(&s_sffree[lane]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            bar_init(smem_u32(&s_accfull[i]), 1);
-            bar_init(smem_u32(&s_accfree[i]), 8);   // the epilogue warps of both blocks
+        if (lane < 2) {
+            bar_init(smem_u32(&s_accfull[lane]), 1);
+            bar_init(smem_u32(&s_accfree[lane]), 8);   // the epilogue warps of both blocks
+            bar_init(smem_u32(&s_drain[lane]), 1);
         }
-        for (int i = 0; i < 2; ++i) bar_init(smem_u32(&s_drain[i]), 1);
+        if (lane == 0) {
+            s_abort_word = 0;
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
@@ -702,12 +704,11 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync();   // the pair's memory and barriers stay until both are done
+    cluster_sync();   // the pair's memory, barriers and TMEM stay until both are done
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
-    cluster_sync();   // neither block leaves while the other frees its half
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
