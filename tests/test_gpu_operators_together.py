@@ -110,6 +110,29 @@ def test_other_streams_and_two_calls_at_once():
     assert all(torch.equal(b.loss, lw.loss) and torch.equal(b.grad_logits, lw.grad_logits) for b in loss)
 
 
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_a_given_stream_owns_what_the_call_allocates(as_handle):
+    """The given stream is behind; the caller's stream meanwhile reuses whatever memory it may."""
+    x, logits, idx, wt, wq, ws = _layer(n=600)
+    lay = cgl.get_layout(idx, 16, 4)
+    one = torch.ones(1, device="cuda")
+    want = cgl.balance_loss(logits, idx, grad_loss=one)
+    rx, rs = cgl.dispatch_mxfp4(x, lay.dst_pos, lay.num_recv_rows)
+    y = cgl.matmul_mxfp4(rx, rs, wq, ws, lay.expert_offset)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)                # about 10 ms
+    arg = s.cuda_stream if as_handle else s
+    b = cgl.balance_loss(logits, idx, grad_loss=one, stream=arg)
+    px, ps = cgl.dispatch_mxfp4(x, lay.dst_pos, lay.num_recv_rows, stream=arg)
+    py = cgl.matmul_mxfp4(px, ps, wq, ws, lay.expert_offset, stream=arg)
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (512, 4096, 70_000, 300_000, 1 << 20) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(b.loss, want.loss) and torch.equal(b.counts, want.counts) and torch.equal(b.grad_logits, want.grad_logits)
+    assert torch.equal(px, rx) and torch.equal(ps, rs) and torch.equal(py, y) and len(junk) == 40
+
+
 def test_unaligned_buffers():
     """y and the scales at any address they may have; dispatch's scale rows too."""
     x, _, idx, wt, wq, ws = _layer(n=100, h=512, f=264)
