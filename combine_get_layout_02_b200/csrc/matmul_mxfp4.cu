@@ -20,10 +20,24 @@
 //               while the next tile's MMAs run
 // Why pairs: one block alone (128 x 208) moves 45 KB a stage into shared memory and
 // reads them out again in 700 cycles of its 128 bytes a cycle, where the MMAs need
-// 416; a pair holds half the tokens' rows each.
+// 416; a pair holds half the tokens' rows each (131072 x 2048 -> 7168 over 256
+// experts: 2.37 ms with single blocks, 1.26 ms with pairs at that step).
 // Scales stay in their rows in memory, [rows, in / 32], because a tile starts at
 // any row of the receive buffer; a warp reads 32 bytes of each row, four stages'
 // worth, one such chunk ahead.
+// Tiles fewer than half of the pairs: two or four pairs share one, a part of K
+// each, and join their sums in order through distributed shared memory.
+//
+// What bounds it (one B200; floors at the measured 6.53 TB/s copy and four times
+// the measured bf16 rate): few rows an expert, the weights' bytes: 4 rows, 7168 ->
+// 4096, 256 experts 612 us, 6.5 TB/s; 128 rows 727 us against 672, and 780 to 880
+// when run for seconds, where the 1000 W cap takes the clock to 1.0 GHz.  Many
+// rows: the bytes that the SMs take from L2, at 64 a cycle and SM: 512 rows a
+// expert on average, 2048 -> 7168: 1.03 ms (1.16 to 1.24 in a long run) against
+// 615; without the loads 0.82, with all weights in L2 1.05.  More columns a tile
+// would take fewer bytes (160, 192, 208: 1.35, 1.23, 1.16 ms in a long run), but
+// two accumulators and the scales fill TMEM at 208.  One row, 7168 -> 4096: 14.7
+// us, of which the launch, the tables and the first loads are 8.
 //
 // Every wait is bounded (about a second, then CGL_ETIMEOUT): the block's roles
 // leave their loops, copies and MMAs in flight are waited for, TMEM is freed.
@@ -63,6 +77,7 @@ struct Params {
     int chunks;      // chunks of scales in shared memory
     int split;       // pairs that share a tile, each a part of K (one cluster)
     int wide;        // y's rows allow 16-byte stores
+    int aligned;     // every scale row starts at a 16-byte boundary
     uint32_t stage_bytes, chunk_bytes;
 };
 
@@ -296,28 +311,46 @@ struct Tiles {
 
 // ---- scales ----------------------------------------------------------------------------------
 
-// 32 scale bytes of a row from byte `at` (those behind the row's end zero).
-__device__ __forceinline__ void load_scales(const uint8_t *row, int at, int bytes, bool there, uint32_t v[8]) {
+// Sixteen bytes at `q`, those outside the array [begin, end) zero.
+__device__ __noinline__ uint4 edge16(const uint8_t *q, const uint8_t *begin, const uint8_t *end) {
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0;
-    if (!there) return;
-    if ((bytes & 15) == 0 && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
-        if (at < bytes) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(row + at));
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    for (int i = 0; i < 16; ++i)
+        if (q + i >= begin && q + i < end) w[i / 4] |= (uint32_t)__ldg(q + i) << (8 * (i % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The 16-byte pieces around a chunk of a scale row (32 bytes from p, `valid` of
+// them in the row), which may start anywhere.  A lane loads a row: each load
+// touches 32 lines whatever its width, so it is as wide as it can be (64 experts
+// of 128 rows, 7200 -> 2048: 115 us, with 4-byte words 175; 7168 takes 99).
+__device__ __forceinline__ void load_scales(const uint8_t *p, int valid, const uint8_t *begin, const uint8_t *end, uint32_t w[12]) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        uint4 a = make_uint4(0, 0, 0, 0);
+        if (16 * i < off + valid) {
+            const uint8_t *q = p - off + 16 * i;
+            a = q >= begin && q + 16 <= end ? __ldg(reinterpret_cast<const uint4 *>(q)) : edge16(q, begin, end);
         }
-        if (at + 16 < bytes) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(row + at + 16));
-            v[4] = a.x, v[5] = a.y, v[6] = a.z, v[7] = a.w;
-        }
-    } else if ((bytes & 3) == 0 && (reinterpret_cast<uintptr_t>(row) & 3) == 0) {
+        w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+    }
+}
+
+// The chunk's bytes out of those pieces; what is behind `valid` becomes zero.
+__device__ __forceinline__ void shift_scales(const uint32_t w[12], const uint8_t *p, int valid, uint32_t v[8]) {
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+    uint32_t t[10];
+#pragma unroll
+    for (int i = 0; i < 10; ++i) t[i] = (off & 8) ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 9; ++i) t[i] = (off & 4) ? t[i + 1] : t[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __funnelshift_r(t[i], t[i + 1], 8 * (off & 3));
+    if (valid < 32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (at + 4 * i < bytes) v[i] = __ldg(reinterpret_cast<const uint32_t *>(row + at) + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (at + i < bytes) v[i / 4] |= (uint32_t)__ldg(row + at + i) << (8 * (i % 4));
+            if (valid - 4 * i < 4) v[i] &= valid > 4 * i ? (1u << (8 * (valid - 4 * i))) - 1u : 0u;
     }
 }
 
@@ -600,22 +633,22 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             const int row_bytes = p.K / 32;
             int ch = 0, chunk = c0;
             uint32_t phase = 0;
-            uint32_t v[4][8], nv[4][8];
-            const auto load = [&](const Tiles &t, int c, uint32_t (&to)[4][8]) {
+            uint32_t raw[4][12], v[4][8];   // the chunk ahead, in flight, and the present one
+            const uint8_t *const begin = weights ? p.sw : p.sa;
+            const uint8_t *const end = begin + (weights ? (int64_t)p.E * p.F : p.rows) * row_bytes;
+            // this lane's first row of a tile's chunk; rows 32 apart, `rows` of 128 there
+            const auto chunk_at = [&](const Tiles &t, int c, int &rows, int &valid) {
+                rows = (weights ? p.F - t.f0 : t.n - block * 128) - lane;
+                valid = row_bytes - c * 32 < 32 ? row_bytes - c * 32 : 32;
+                return begin + (weights ? (int64_t)t.e * p.F + t.f0 : (int64_t)t.row0 + block * 128) * row_bytes +
+                       (int64_t)lane * row_bytes + c * 32;
+            };
+            const auto load = [&](const Tiles &t, int c) {
+                int rows, valid;
+                const uint8_t *at = chunk_at(t, c, rows, valid);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = (weights ? 0 : block * 128) + i * 32 + lane;
-                    const uint8_t *row;
-                    bool there;
-                    if (weights) {
-                        there = t.f0 + r < p.F;
-                        row = p.sw + ((int64_t)t.e * p.F + t.f0 + r) * row_bytes;
-                    } else {
-                        there = r < t.n;
-                        row = p.sa + ((int64_t)t.row0 + r) * row_bytes;
-                    }
-                    load_scales(row, c * 32, row_bytes, there, to[i]);
-                }
+                for (int i = 0; i < 4; ++i)
+                    load_scales(at + (int64_t)(32 * i) * row_bytes, 32 * i < rows ? valid : -16, begin, end, raw[i]);
             };
             // the weights' scales of a tile lie in one piece: asked into L2 a tile
             // ahead, since a load that has to queue behind the ring's own copies
@@ -635,7 +668,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 Tiles second = tile;
                 second.next();
                 to_l2(second);
-                load(tile, c0, v);
+                load(tile, c0);
             }
             while (ok && tile.valid()) {
                 Tiles ahead = tile;
@@ -647,7 +680,19 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                     after.next();
                     to_l2(after);
                 }
-                if (ahead.valid()) load(ahead, ahead_chunk, nv);
+                if (p.aligned) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[i][j] = raw[i][j];
+                } else {
+                    int rows, valid;
+                    const uint8_t *at = chunk_at(tile, chunk, rows, valid);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        shift_scales(raw[i], at + (int64_t)(32 * i) * row_bytes, 32 * i < rows ? valid : 0, v[i]);
+                }
+                if (ahead.valid()) load(ahead, ahead_chunk);
                 ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_sffree[ch]), phase ^ 1, abort, p.status));
                 if (ok) {
                     uint8_t *to = sf_ptr + (size_t)ch * p.chunk_bytes + (weights ? 0 : kChunkA + 512 * block) + lane * 16;
@@ -660,10 +705,6 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                     if (lane == 0) bar_arrive_remote(in_block(smem_u32(&s_sffull[ch]), lead));
                     if (++ch == p.chunks) ch = 0, phase ^= 1;
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] = nv[i][j];
                 tile = ahead;
                 chunk = ahead_chunk;
             }
@@ -762,6 +803,7 @@ cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows
     if (stages > kMaxStages) stages = kMaxStages;
     p.chunks = room - (size_t)stages * p.stage_bytes >= 3 * p.chunk_bytes ? 3 : 2;
     p.stages = stages;
+    p.aligned = K % 512 == 0 && ((reinterpret_cast<uintptr_t>(sa) | reinterpret_cast<uintptr_t>(sw)) & 15) == 0;
     p.wide = F % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
     const size_t smem = 1024 + (size_t)stages * p.stage_bytes + (size_t)p.chunks * p.chunk_bytes + kOutBytes + tables;
 

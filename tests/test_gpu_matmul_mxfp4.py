@@ -68,6 +68,21 @@ def test_padded(counts, cap):
     _check(*_case(counts, 320, 192, cap, cap=cap))
 
 
+@pytest.mark.parametrize("k", [1056, 1088, 1120, 1152, 1184, 7200])
+@pytest.mark.parametrize("shift", [0, 1, 2, 3])
+def test_scale_rows_of_every_alignment(k, shift):
+    """Rows of k / 32 scale bytes start at any byte; the arrays lie between NaN scales, which must not be read into them."""
+    a, sa, w, sw, off, _ = _case([3, 0, 70], k, 130, k + shift, lo=127, hi=127)
+
+    def place(s):
+        buf = torch.full((s.numel() + 16,), 255, dtype=torch.uint8, device="cuda")
+        t = buf[4 + shift:4 + shift + s.numel()].view(s.shape)
+        t.copy_(s)
+        return t
+
+    _check(a, place(sa), w, place(sw), off, 0, tail=0)
+
+
 def test_one_expert_without_offsets():
     a, sa, w, sw, _, _ = _case([77], 512, 200, 1)
     _check(a, sa, w, sw, None, 0)
