@@ -61,7 +61,8 @@ typedef enum cgl_status {
     CGL_EALIGN = 2,     /* a pointer is not aligned as the call requires */
     CGL_ERANGE = 3,     /* (device) an expert id < -1 or >= E, or a receive row outside the buffer */
     CGL_ECAPACITY = 4,  /* (device) a padded expert received more copies than its capacity */
-    CGL_ETIMEOUT = 5,   /* (device) a bounded wait between the layout's blocks gave up (~1 s) */
+    CGL_ETIMEOUT = 5,   /* (device) a bounded wait between the layout's blocks, or inside the MXFP4
+                           product, gave up (~1 s) */
     CGL_ECUDA = 6,      /* the CUDA runtime refused a launch or an attribute call */
     CGL_ENOTIMPL = 7    /* not implemented */
 } cgl_status;
@@ -412,8 +413,9 @@ cgl_status cgl_combine_backward(const uint16_t *grad_out, const uint16_t *y, int
 
 /*
  * cgl_selftest_bounded_wait -- diagnostic for failure detection.  Runs the
- * layout's inter-block wait (the only software wait in any kernel of this
- * library) in one block, exit path included, on a layout workspace header:
+ * layout's inter-block wait (the only software wait between blocks that are
+ * launched apart; cgl_matmul_mxfp4's waits are inside a block pair, bounded the
+ * same way) in one block, exit path included, on a layout workspace header:
  * workspace[0] is the generation word and workspace[1 .. nflags] are the flags.
  * It waits for a tag that no layout launch writes, so on zeroed memory, or on
  * a header that layout calls have used, it must give up after ~1 s (2^31 SM
@@ -529,6 +531,8 @@ size_t cgl_balance_loss_workspace_bytes(int64_t num_tokens, int num_topk, int nu
  *   num_routed int32 [S] (T_s); grad_logits [num_tokens, E] in the logits' type =
  *   grad_loss * dloss/dlogits (0 for tokens not routed), or NULL for none.
  * The counts carry no gradient.  Sums are binary32 or wider, in a fixed order.
+ * grad_logits must not overlap the logits.  16-byte aligned rows (E % 8 == 0 and
+ * aligned pointers) are read and written faster.
  * workspace: device, 16-byte aligned, any contents, scratch for the call.
  * Limits: num_tokens % num_sequences == 0, num_sequences <= 2^24, and the
  * library's own.  Device errors: CGL_ERANGE for ids < -1 or >= E (not counted).

@@ -93,16 +93,33 @@ def _check(logits, idx, S=1, alpha=0.02, score="softmax", g=1.0, status=None):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("n,E,k,S,pad", [(1, 1, 1, 1, 0), (1, 16, 4, 1, 0), (128, 16, 4, 1, 0), (7, 5, 2, 7, 0.3), (96, 33, 3, 4, 0.2),
                                          (300, 64, 6, 3, 0.5), (1000, 256, 8, 1, 0.1), (515, 100, 32, 5, 0.1),
-                                         (64, 1024, 8, 2, 0), (40, 1000, 1, 1, 0.2), (3000, 128, 2, 10, 0)])
+                                         (64, 1024, 8, 2, 0), (40, 1000, 1, 1, 0.2), (3000, 128, 2, 10, 0),
+                                         (30, 130, 4, 1, 0.1), (50, 701, 5, 2, 0.1), (33, 512, 8, 1, 0.1)])
 def test_against_definition(n, E, k, S, pad, score, dtype):
     logits, idx = _inputs(n, E, k, dtype, n + E, pad)
     _check(logits, idx, S, 0.02, score, g=256.0 if dtype == torch.float16 else 0.75)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-def test_large_batch(score):
-    logits, idx = _inputs(20000, 256, 8, torch.float32, 5, 0.05)
-    _check(logits, idx, 4, 1e-3, score)
+@pytest.mark.parametrize("E,k", [(256, 8), (128, 3), (72, 2)])
+def test_large_batch(E, k, score, dtype):
+    """Past the size at which 16-bit logits take two groups of experts a lane."""
+    logits, idx = _inputs(20000, E, k, dtype, 5, 0.05)
+    _check(logits, idx, 4, 1e-3, score, g=0.75 * 2 ** 10)
+
+
+def test_repeated_ids_and_unaligned_rows():
+    """A token may name an expert twice; rows off the 16-byte grid take the other loads, with equal values."""
+    g = torch.Generator().manual_seed(3)
+    idx = torch.randint(0, 64, (200, 6), generator=g, dtype=torch.int32).cuda()
+    idx[:, 1] = idx[:, 0]
+    logits = _inputs(200, 64, 6, torch.float32, 4)[0]
+    b = _check(logits, idx, 2)
+    off = torch.empty(200 * 64 + 1, device="cuda")[1:].view(200, 64)
+    off.copy_(logits)
+    u = _check(off, idx, 2)
+    assert torch.equal(u.counts, b.counts)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
