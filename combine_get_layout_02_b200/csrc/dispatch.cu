@@ -253,14 +253,14 @@ dispatch_mxfp4_bulk_kernel(const uint16_t *__restrict__ x, int64_t n, int h, int
     }
     uint4 a = make_uint4(0, 0, 0, 0), b = a;
     if (t < n && active) {
-        a = ld_nc_v4(x + t * h + (int64_t)c * 16);
-        b = ld_nc_v4(x + t * h + (int64_t)c * 16 + 8);
+        a = ld_nc_l1_v4(x + t * h + (int64_t)c * 16);
+        b = ld_nc_l1_v4(x + t * h + (int64_t)c * 16 + 8);
     }
     for (int it = 0; t < n; buf ^= 1, ++it) {
         uint4 an = make_uint4(0, 0, 0, 0), bn = an;   // the next token's chunk, in flight
         if (tn < n && active) {
-            an = ld_nc_v4(x + tn * h + (int64_t)c * 16);
-            bn = ld_nc_v4(x + tn * h + (int64_t)c * 16 + 8);
+            an = ld_nc_l1_v4(x + tn * h + (int64_t)c * 16);
+            bn = ld_nc_l1_v4(x + tn * h + (int64_t)c * 16 + 8);
         }
         uint32_t byte;
         const uint2 q = mx_quantize16(a, b, byte);
@@ -508,9 +508,10 @@ cgl_status launch_dispatch_mxfp4(const uint16_t *x, int64_t n, int h, int k, con
         const int grid = persistent_grid((const void *)dispatch_mxfp4_bulk_kernel, threads, (size_t)2 * pitch,
                                          kMxThreadsPerSM / threads, num_sms, n);
         if (grid <= 0) return CGL_ECUDA;
-        // few tokens a CTA: the claims cost more than the even load gives (1024
-        // tokens of 7168, top-8: 9.5 against 7.5 us; 4096: 32.3 against 34.5)
-        if (n <= 4 * (int64_t)grid) claim = nullptr;
+        // few tokens a CTA: the claims cost more than the even load gives (tokens of
+        // 7168, top-8, on 592 CTAs: 2500 tokens 16.1 against 14.1 us; 4096: 32.0
+        // against 32.6; 16384: 122 against 132)
+        if (n <= 6 * (int64_t)grid) claim = nullptr;
         const cudaError_t err = launch_pdl(dispatch_mxfp4_bulk_kernel, dim3(grid), dim3(threads), (size_t)2 * pitch, stream,
                                            x, n, h, k, dst_pos, recv_x, recv_scale, recv_rows, bulk_scales, pitch, claim,
                                            status);

@@ -145,8 +145,8 @@ struct Vec8<CGL_F32> {
     uint4 a, b;
     __device__ __forceinline__ void load(const void *x, int64_t i) {
         const float *p = static_cast<const float *>(x) + i * 8;
-        a = ld_nc_v4(p);
-        b = ld_nc_v4(p + 4);
+        a = ld_nc_l1_v4(p);   // L1 keeps the sector for its other half
+        b = ld_nc_l1_v4(p + 4);
     }
     __device__ __forceinline__ void widen(float v[8]) const {
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
