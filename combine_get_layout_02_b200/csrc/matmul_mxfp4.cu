@@ -30,7 +30,7 @@
 //
 // What bounds it (one B200; floors at the measured 6.53 TB/s copy and four times
 // the measured bf16 rate): few rows an expert, the weights' bytes: 4 rows, 7168 ->
-// 4096, 256 experts 612 us, 6.5 TB/s; 128 rows 727 us against 672, and 780 to 880
+// 4096, 256 experts 612 us, 6.4 TB/s; 128 rows 727 us against 672, and 780 to 880
 // when run for seconds, where the 1000 W cap takes the clock to 1.0 GHz.  Many
 // rows: the bytes that the SMs take from L2, at 64 a cycle and SM: 512 rows a
 // expert on average, 2048 -> 7168: 1.03 ms (1.16 to 1.24 in a long run) against
