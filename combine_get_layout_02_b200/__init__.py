@@ -28,7 +28,6 @@ power-of-two scale per 32), and for training the loss that keeps the routing eve
 from __future__ import annotations
 
 import ctypes as C
-import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -467,16 +466,9 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # cgl_dtype
 _SCORES = {"softmax": 0, "sigmoid": 1}                              # cgl_score
 
 
-def _streamed(fn):
-    """A call with stream=s runs with s current, so that what it allocates belongs to s as well."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
-        if stream is None:
-            return fn(*args, **kwargs)
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-        with torch.cuda.stream(s):
-            return fn(*args, **kwargs)
-    return call
+def _on(stream):
+    """Makes `stream` (a torch stream or a handle) current, so that what a call allocates belongs to it as well."""
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
 def _launch(where: str, fn, device, *args):
@@ -498,8 +490,8 @@ def _buf(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor)
         return like.new_empty(shape, dtype=dtype)   # 0.5 us less than torch.empty
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != like.device:
         raise TypeError(f"{name} must be {dtype} on {like.device}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
     return t
 
 
@@ -515,18 +507,20 @@ def _float_type(t: torch.Tensor, name: str) -> int:
     return _DTYPES[t.dtype]
 
 
-@_streamed
 def quantize_mxfp4(x: torch.Tensor, *, codes: Optional[torch.Tensor] = None,
                    scales: Optional[torch.Tensor] = None, num_sms: int = 0, stream=None):
     """MXFP4 codes and scales of x [..., C], C % 32 == 0 (cgl_quantize_mxfp4).
 
     Returns (codes uint8 [..., C/2], two codes a byte with the lower index in the low half;
     scales uint8 [..., C/32], 2^(byte - 127)).  Blocks with an infinity or NaN get scale byte 255 (NaN)."""
+    if stream is not None:
+        with _on(stream):
+            return quantize_mxfp4(x, codes=codes, scales=scales, num_sms=num_sms)
     x = _dev(x, "x")
     dt = _float_type(x, "x")
-    if x.dim() < 1 or x.shape[-1] % 32 or x.shape[-1] == 0:
+    *lead, c = x.shape or (0,)
+    if c == 0 or c % 32:
         raise ValueError(f"x must have a last dimension that is a multiple of 32, got {tuple(x.shape)}")
-    c, lead = x.shape[-1], x.shape[:-1]
     codes = _buf(codes, "codes", (*lead, c // 2), torch.uint8, x)
     scales = _buf(scales, "scales", (*lead, c // 32), torch.uint8, x)
     _launch("cgl_quantize_mxfp4", lib().cgl_quantize_mxfp4, x.device, _ptr(x), dt, x.numel() // c, c,
@@ -534,25 +528,27 @@ def quantize_mxfp4(x: torch.Tensor, *, codes: Optional[torch.Tensor] = None,
     return codes, scales
 
 
-@_streamed
 def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16, *,
                      out: Optional[torch.Tensor] = None, num_sms: int = 0, stream=None) -> torch.Tensor:
     """The values MXFP4 codes [..., C/2] and scales [..., C/32] stand for, [..., C] (cgl_dequantize_mxfp4)."""
+    if stream is not None:
+        with _on(stream):
+            return dequantize_mxfp4(codes, scales, dtype, out=out, num_sms=num_sms)
     codes = _dev(codes, "codes", torch.uint8)
     scales = _dev(scales, "scales", torch.uint8)
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
     _same(codes.device, scales=scales)
-    c = 2 * codes.shape[-1] if codes.dim() else 0
-    if c == 0 or c % 32 or tuple(scales.shape) != (*codes.shape[:-1], c // 32):
+    *lead, half = codes.shape or (0,)
+    c = 2 * half
+    if c == 0 or c % 32 or scales.shape != (*lead, c // 32):
         raise ValueError(f"codes [..., C/2] and scales [..., C/32] expected, got {tuple(codes.shape)}, {tuple(scales.shape)}")
-    out = _buf(out, "out", (*codes.shape[:-1], c), dtype, codes)
+    out = _buf(out, "out", (*lead, c), dtype, codes)
     _launch("cgl_dequantize_mxfp4", lib().cgl_dequantize_mxfp4, codes.device, _ptr(codes), _ptr(scales),
             out.numel() // c, c, _ptr(out), _DTYPES[dtype], _opts(num_sms))
     return out
 
 
-@_streamed
 def dispatch_mxfp4(x: torch.Tensor, dst_pos: torch.Tensor, num_recv_rows: int, *,
                    recv_x: Optional[torch.Tensor] = None, recv_scale: Optional[torch.Tensor] = None,
                    status: Optional[torch.Tensor] = None, num_sms: int = 0,
@@ -562,6 +558,10 @@ def dispatch_mxfp4(x: torch.Tensor, dst_pos: torch.Tensor, num_recv_rows: int, *
     scratch: new_scratch() (cgl_opts.scratch): tokens handed out dynamically, same results.
     Returns (recv_x uint8 [rows, H/2], recv_scale uint8 [rows, H/32]); rows that receive no copy
     are left as they were (uninitialised when allocated here)."""
+    if stream is not None:
+        with _on(stream):
+            return dispatch_mxfp4(x, dst_pos, num_recv_rows, recv_x=recv_x, recv_scale=recv_scale, status=status,
+                                  num_sms=num_sms, scratch=scratch)
     x = _dev(x, "x", torch.bfloat16, 2)
     dst = _dev(dst_pos, "dst_pos", torch.int32, 2)
     n, h = x.shape
@@ -577,7 +577,6 @@ def dispatch_mxfp4(x: torch.Tensor, dst_pos: torch.Tensor, num_recv_rows: int, *
     return recv_x, recv_scale
 
 
-@_streamed
 def matmul_mxfp4(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
                  expert_offset: Optional[torch.Tensor] = None, capacity: int = 0, *,
                  y: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
@@ -588,6 +587,9 @@ def matmul_mxfp4(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scal
     w uint8 [E, out, in/2], w_scale uint8 [E, out, in/32].  expert_offset int32 [E + 1] and
     capacity as get_layout gives them; without expert_offset w has one expert (or is [out, in/2])
     and takes every row.  Rows of no expert are left as they were."""
+    if stream is not None:
+        with _on(stream):
+            return matmul_mxfp4(a, a_scale, w, w_scale, expert_offset, capacity, y=y, status=status, num_sms=num_sms)
     a = _dev(a, "a", torch.uint8, 2)
     a_scale = _dev(a_scale, "a_scale", torch.uint8, 2)
     w = _dev(w, "w", torch.uint8)
@@ -596,10 +598,9 @@ def matmul_mxfp4(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scal
         w, w_scale = w.unsqueeze(0), w_scale.unsqueeze(0)
     if w.dim() != 3:
         raise ValueError(f"w must have 3 dims, got {w.dim()}")
-    (rows, kb), (E, F) = a.shape, w.shape[:2]
+    (rows, kb), (E, F, wb) = a.shape, w.shape
     K = 2 * kb
-    if (w.shape[2] != kb or K == 0 or K % 32 or tuple(a_scale.shape) != (rows, K // 32)
-            or tuple(w_scale.shape) != (E, F, K // 32)):
+    if wb != kb or K == 0 or K % 32 or a_scale.shape != (rows, K // 32) or w_scale.shape != (E, F, K // 32):
         raise ValueError(f"a [rows, in/2], a_scale [rows, in/32], w [E, out, in/2], w_scale [E, out, in/32] expected, got "
                          f"{tuple(a.shape)}, {tuple(a_scale.shape)}, {tuple(w.shape)}, {tuple(w_scale.shape)}")
     if expert_offset is not None:
@@ -633,14 +634,13 @@ def _balance_args(logits, topk_idx, score, num_sequences, where):
     if idx.shape[0] != logits.shape[0]:
         raise ValueError(f"topk_idx must have {logits.shape[0]} rows, got {idx.shape[0]}")
     _same(logits.device, topk_idx=idx)
-    n, E = logits.shape
-    ws_bytes = balance_loss_workspace_bytes(n, idx.shape[1], E, num_sequences)
+    (n, E), k = logits.shape, idx.shape[1]
+    ws_bytes = int(lib().cgl_balance_loss_workspace_bytes(n, k, E, num_sequences))
     if ws_bytes == 0:
         raise CglError(EINVAL, where, "invalid sizes")
-    return logits, idx, dt, n, idx.shape[1], E, ws_bytes
+    return logits, idx, dt, n, k, E, ws_bytes
 
 
-@_streamed
 def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, *, num_sequences: int = 1, alpha: float = 1.0,
                  score: str = "softmax", grad_loss: Optional[torch.Tensor] = None,
                  loss: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
@@ -652,6 +652,11 @@ def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, *, num_sequences:
     logits [N, E] (bfloat16, float16 or float32), topk_idx int32 [N, k] (-1 = no copy; a token with no copy
     takes no part).  score: "softmax", or "sigmoid" (normalised over the experts).  grad_loss: fp32 [1] on the
     device, the gradient that arrives at the loss; without it, balance_loss_backward gives grad_logits later."""
+    if stream is not None:
+        with _on(stream):
+            return balance_loss(logits, topk_idx, num_sequences=num_sequences, alpha=alpha, score=score,
+                                grad_loss=grad_loss, loss=loss, counts=counts, num_routed=num_routed,
+                                grad_logits=grad_logits, workspace=workspace, status=status)
     logits, idx, dt, n, k, E, ws_bytes = _balance_args(logits, topk_idx, score, num_sequences, "balance_loss")
     dev = logits.device
     if grad_loss is not None:
@@ -659,28 +664,40 @@ def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, *, num_sequences:
     elif grad_logits is not None:
         raise ValueError("grad_logits needs grad_loss")
     _same(dev, status=status)
+    S = num_sequences
     loss = _buf(loss, "loss", (1,), torch.float32, logits)
-    counts = _buf(counts, "counts", (num_sequences, E), torch.int32, logits)
-    num_routed = _buf(num_routed, "num_routed", (num_sequences,), torch.int32, logits)
     if grad_loss is not None:
         grad_logits = torch.empty_like(logits) if grad_logits is None else \
             _buf(grad_logits, "grad_logits", (n, E), logits.dtype, logits)
-    if workspace is None:
-        workspace = logits.new_empty(ws_bytes, dtype=torch.uint8)
+    if counts is None and num_routed is None and workspace is None:   # one allocation for the three, workspace first
+        ints = ws_bytes // 4
+        small = logits.new_empty(ints + S * (E + 1), dtype=torch.int32)
+        counts, num_routed = small.as_strided((S, E), (E, 1), ints), small.as_strided((S,), (1,), ints + S * E)
+        ws = small.data_ptr()
     else:
-        _same(dev, workspace=_dev(workspace, "workspace"))
-    _launch("cgl_balance_loss", lib().cgl_balance_loss, dev, _ptr(logits), dt, _ptr(idx), n, k, E,
-            num_sequences, float(alpha), _SCORES[score], _ptr(grad_loss), _ptr(loss), _ptr(counts), _ptr(num_routed),
-            _ptr(grad_logits), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status))
+        counts = _buf(counts, "counts", (S, E), torch.int32, logits)
+        num_routed = _buf(num_routed, "num_routed", (S,), torch.int32, logits)
+        if workspace is None:
+            workspace = logits.new_empty(ws_bytes, dtype=torch.uint8)
+        else:
+            _same(dev, workspace=_dev(workspace, "workspace"))
+            ws_bytes = workspace.numel() * workspace.element_size()
+        ws = workspace.data_ptr()
+    _launch("cgl_balance_loss", lib().cgl_balance_loss, dev, _ptr(logits), dt, _ptr(idx), n, k, E, S, float(alpha),
+            _SCORES[score], _ptr(grad_loss), _ptr(loss), _ptr(counts), _ptr(num_routed), _ptr(grad_logits), ws, ws_bytes,
+            _ptr(status))
     return BalanceLoss(loss, counts, num_routed, grad_logits)
 
 
-@_streamed
 def balance_loss_backward(grad_loss: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor,
                           counts: torch.Tensor, num_routed: torch.Tensor, *, num_sequences: int = 1,
                           alpha: float = 1.0, score: str = "softmax", grad_logits: Optional[torch.Tensor] = None,
                           stream=None) -> torch.Tensor:
     """Gradient of balance_loss for the logits, from the forward's counts and num_routed (cgl_balance_loss_backward)."""
+    if stream is not None:
+        with _on(stream):
+            return balance_loss_backward(grad_loss, logits, topk_idx, counts, num_routed, num_sequences=num_sequences,
+                                         alpha=alpha, score=score, grad_logits=grad_logits)
     logits, idx, dt, n, k, E, _ = _balance_args(logits, topk_idx, score, num_sequences, "balance_loss_backward")
     dev = logits.device
     _buf(_dev(grad_loss, "grad_loss", torch.float32), "grad_loss", (1,), torch.float32, logits)
