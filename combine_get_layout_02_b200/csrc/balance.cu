@@ -11,8 +11,9 @@
 // an exact integer, so near-equal counts lose nothing to cancellation.
 //
 // Two kernels: histograms of id chunks (shared-memory integer atomics, whose
-// order has no effect), then the pass over the logits, where every block first
-// sums the chunks' counts for itself and the last block to finish adds up the
+// order has no effect; clusters of eight blocks add theirs up through distributed
+// shared memory), then the pass over the logits, where every block first
+// sums the clusters' counts for itself and the last block to finish adds up the
 // blocks' loss sums in their order.  The grid goes by the sizes alone, so equal
 // inputs give equal bits.
 //
@@ -34,13 +35,16 @@ constexpr int kMainThreads = 256;
 constexpr int kMainWarps = kMainThreads / 32;
 constexpr int64_t kMaxBlocks = 592;    // 148 SMs x 4 blocks; a constant, so sums do not depend on the device
 constexpr int64_t kChunkIds = 4096;    // ids a histogram block
+constexpr int kCluster = 8;            // histogram blocks a cluster, where a sequence has more than one
+constexpr int kMaxParts = 16;          // clusters a sequence
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Shape {
     int64_t tokens;      // per sequence
     int64_t seqs;
     int k, E;
-    int count_chunks;    // histogram blocks per sequence
+    int count_chunks;    // histogram blocks per sequence: 1, or a multiple of kCluster
+    int parts;           // sums per sequence that they leave
     int64_t count_tokens;
     int main_chunks;     // blocks per sequence of the main pass
 };
@@ -68,9 +72,16 @@ Shape shape(int64_t n, int k, int E, int64_t S, int dtype) {
     s.k = k;
     s.E = E;
     const int64_t want = (s.tokens * k + kChunkIds - 1) / kChunkIds, fit = kMaxBlocks / S > 0 ? kMaxBlocks / S : 1;
-    int64_t c = want < 32 ? want : 32;
-    if (c > fit) c = fit;
-    if (c < 1) c = 1;
+    int64_t c = 1;
+    if (want > 1 && S * kCluster <= 2 * kMaxBlocks) {   // 2: a block has little to do
+        const int64_t most = 2 * fit / kCluster > 1 ? 2 * fit / kCluster : 1;
+        c = (want + kCluster - 1) / kCluster;
+        c = (c < most ? c : most) < kMaxParts ? (c < most ? c : most) : kMaxParts;
+        s.parts = (int)c;
+        c *= kCluster;
+    } else {
+        s.parts = 1;
+    }
     s.count_chunks = (int)c;
     s.count_tokens = (s.tokens + c - 1) / c;
     const int64_t at_once = kMainWarps * (E % 8 == 0 ? 32 / width_for(n, E, dtype).lanes : 1);   // tokens a block has in hand
@@ -80,7 +91,7 @@ Shape shape(int64_t n, int k, int E, int64_t S, int dtype) {
     return s;
 }
 
-// part[block][E + 1]: slots per expert, routed tokens.  ticket: zeroed for the main kernel.
+// part[cluster][E + 1]: slots per expert, routed tokens.  ticket: zeroed for the main kernel.
 __global__ void __launch_bounds__(kCountThreads)
 balance_count_kernel(const int32_t *__restrict__ idx, int64_t tokens, int k, int E, int chunks, int64_t per_chunk,
                      int32_t *__restrict__ part, uint32_t *__restrict__ ticket, uint32_t *status) {
@@ -122,8 +133,31 @@ balance_count_kernel(const int32_t *__restrict__ idx, int64_t tokens, int k, int
         const uint32_t m = __ballot_sync(__activemask(), any);
         if ((threadIdx.x & 31) == __ffs(__activemask()) - 1 && m) atomicAdd(&s_count[E], __popc(m));
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e <= E; e += kCountThreads) part[(int64_t)blockIdx.x * (E + 1) + e] = s_count[e];
+    if (chunks == 1) {
+        __syncthreads();
+        for (int e = threadIdx.x; e <= E; e += kCountThreads) part[(int64_t)blockIdx.x * (E + 1) + e] = s_count[e];
+    } else {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        for (int e = blockIdx.x % kCluster + threadIdx.x * kCluster; e <= E; e += kCountThreads * kCluster) {
+            int32_t sum = 0;
+#pragma unroll
+            for (int r = 0; r < kCluster; ++r) {
+                int32_t v;
+                asm volatile(
+                    "{\n.reg .b32 a;\n"
+                    "mapa.shared::cluster.u32 a, %1, %2;\n"
+                    "ld.shared::cluster.s32 %0, [a];\n}"
+                    : "=r"(v)
+                    : "r"((uint32_t)__cvta_generic_to_shared(s_count + e)), "r"(r)
+                    : "memory");
+                sum += v;
+            }
+            part[(int64_t)(blockIdx.x / kCluster) * (E + 1) + e] = sum;
+        }
+        __syncwarp();   // no block leaves while another reads its counts
+        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
     if (bad) report(status, kErrRange);
 }
 
@@ -235,8 +269,8 @@ struct Row {
     }
 };
 
-// LANES lanes a token.  part: the count kernel's chunks (chunks > 0), or null
-// and counts / routed as the forward gave them (loss_part null then).
+// LANES lanes a token.  part: the count kernel's sums (chunks a sequence), or null,
+// chunks 0, and counts / routed as the forward gave them (loss_part null then).
 template <int DT, int LANES, int N, bool VEC, bool SIG>
 __global__ void __launch_bounds__(kMainThreads, Row<DT, LANES, N, VEC>::V <= 16 ? 4 : 1)   // 4: the grid is one wave
 balance_main_kernel(const void *__restrict__ logits, const int32_t *__restrict__ idx, int64_t tokens, int k, int E,
@@ -479,7 +513,7 @@ cudaError_t main_by_type(int dtype, const Shape &s, const Args &a) {
 size_t balance_workspace_bytes(int64_t n, int k, int E, int64_t S) {
     const Shape s = shape(n, k, E, S, CGL_F32), h = shape(n, k, E, S, CGL_BF16);   // types may differ in their blocks
     const int blocks = s.main_chunks > h.main_chunks ? s.main_chunks : h.main_chunks;
-    return 16 + round16((size_t)S * blocks * 8) + (size_t)S * s.count_chunks * (E + 1) * 4;
+    return 16 + round16((size_t)S * blocks * 8) + (size_t)S * s.parts * (E + 1) * 4;
 }
 
 cgl_status launch_balance_loss(const void *logits, int dtype, const int32_t *idx, int64_t n, int k, int E, int64_t S,
@@ -489,10 +523,24 @@ cgl_status launch_balance_loss(const void *logits, int dtype, const int32_t *idx
     uint32_t *ticket = static_cast<uint32_t *>(ws);
     double *loss_part = reinterpret_cast<double *>(static_cast<uint8_t *>(ws) + 16);
     int32_t *part = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + 16 + round16((size_t)S * s.main_chunks * 8));
-    if (launch_pdl(balance_count_kernel, dim3((unsigned)(S * s.count_chunks)), dim3(kCountThreads), (size_t)(E + 1) * 4,
-                   stream, idx, s.tokens, k, E, s.count_chunks, s.count_tokens, part, ticket, status) != cudaSuccess)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(S * s.count_chunks));
+    cfg.blockDim = dim3(kCountThreads);
+    cfg.dynamicSmemBytes = (size_t)(E + 1) * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = s.count_chunks > 1 ? kCluster : 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, balance_count_kernel, idx, s.tokens, k, E, s.count_chunks, s.count_tokens, part, ticket,
+                           status) != cudaSuccess)
         return CGL_ECUDA;
-    const Args a = {logits, idx, (double)alpha / ((double)S * k), score, part, s.count_chunks, counts, routed,
+    const Args a = {logits, idx, (double)alpha / ((double)S * k), score, part, s.parts, counts, routed,
                     grad_loss, grad, loss_part, ticket, loss, stream};
     return main_by_type(dtype, s, a) == cudaSuccess ? CGL_OK : CGL_ECUDA;
 }
