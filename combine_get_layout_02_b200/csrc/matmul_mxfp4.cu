@@ -14,8 +14,9 @@
 //               swizzle; 0 the weights, 9 the tokens
 //   warp 1, 10  in the pair's first block, for both: 1 issues the MMAs, 4 a stage,
 //               10 the copies of the scales from shared memory to TMEM (tcgen05.cp)
-//   warp 2      the weights' scales, 3 and 8 the tokens': global rows -> the 512-byte
-//               blocks that tcgen05.cp wants (row r's word at (r % 32) * 16 + (r / 32) * 4)
+//   warps 2, 11 the weights' scales (11: see the launcher), 3 and 8 the tokens':
+//               global rows -> the 512-byte blocks that tcgen05.cp wants (row r's word
+//               at (r % 32) * 16 + (r / 32) * 4)
 //   warps 4-7   TMEM -> registers -> transposed through shared memory -> BF16 rows,
 //               while the next tile's MMAs run
 // Why pairs: one block alone (128 x 208) moves 45 KB a stage into shared memory and
@@ -30,7 +31,7 @@
 //
 // What bounds it (one B200; floors at the measured 6.53 TB/s copy and four times
 // the measured bf16 rate): few rows an expert, the weights' bytes: 4 rows, 7168 ->
-// 4096, 256 experts 612 us, 6.4 TB/s; 128 rows 727 us against 672, and 780 to 880
+// 4096, 256 experts 612 us, 6.4 TB/s; 128 rows 683 us against 672, and 770 to 850
 // when run for seconds, where the 1000 W cap takes the clock to 1.0 GHz.  Many
 // rows: the bytes that the SMs take from L2, at 64 a cycle and SM: 512 rows a
 // expert on average, 2048 -> 7168: 1.03 ms (1.16 to 1.24 in a long run) against
@@ -52,7 +53,7 @@ namespace {
 
 constexpr uint32_t kErrTimeout = 1u << CGL_ETIMEOUT;
 constexpr long long kWaitCycles = 1ll << 31;
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr int kStageK = 256;              // values a stage
 constexpr int kChunk = 4;                 // stages a chunk of scales (1024 values, 32 bytes a row)
 constexpr int kM = 128;                   // features a tile
@@ -75,6 +76,7 @@ struct Params {
     int box;         // token rows a TMA box
     int stages;
     int chunks;      // chunks of scales in shared memory
+    int sfwarps;     // warps for the weights' scales (1 or 2)
     int split;       // pairs that share a tile, each a part of K (one cluster)
     int wide;        // y's rows allow 16-byte stores
     int aligned;     // every scale row starts at a 16-byte boundary
@@ -478,7 +480,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
 
     // tables: first[E + 1] (tiles of nt rows before each expert), row0[E], rows[E]
     bool bad = false;
-    for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
         int r0, m;
         expert_rows(p, e, r0, m, bad);
         tables[p.E + 1 + e] = r0;
@@ -626,12 +628,13 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             const long long start = clock64();
             while (!bar_try(drain, 0) && clock64() - start < kWaitCycles) {}
         }
-    } else if (warp == 2 || warp == 3 || warp == 8) {
-        const bool weights = warp == 2;
+    } else if (warp == 2 || warp == 3 || warp == 8 || warp == 11) {
+        const bool weights = warp == 2 || warp == 11;
         const int block = warp == 8 ? 1 : 0;   // 128-row block of the token side
-        if (weights || block < p.nb) {
+        const int odd = warp == 11 ? 1 : 0, stride = weights ? p.sfwarps : 1;   // which of the chunks
+        if (weights ? odd < p.sfwarps : block < p.nb) {
             const int row_bytes = p.K / 32;
-            int ch = 0, chunk = c0;
+            int ch = odd, chunk = c0;
             uint32_t phase = 0;
             uint32_t raw[4][12], v[4][8];   // the chunk ahead, in flight, and the present one
             const uint8_t *const begin = weights ? p.sw : p.sa;
@@ -654,57 +657,64 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             // ahead, since a load that has to queue behind the ring's own copies
             // comes too late (one chunk in flight a warp)
             const auto to_l2 = [&](const Tiles &t) {
-                if (!weights || lane != 0 || !t.valid()) return;
+                if (!weights || odd || lane != 0 || !t.valid()) return;
                 const int there = p.F - t.f0 < kM ? p.F - t.f0 : kM;
                 if (there <= 0) return;
                 const uintptr_t a = reinterpret_cast<uintptr_t>(p.sw + ((int64_t)t.e * p.F + t.f0) * row_bytes);
                 const uintptr_t a0 = (a + 15) & ~(uintptr_t)15, a1 = (a + (int64_t)there * row_bytes) & ~(uintptr_t)15;
                 if (a1 > a0) prefetch_l2_bulk(reinterpret_cast<const void *>(a0), (uint32_t)(a1 - a0));
             };
-            bool ok = true;
+            const auto step = [&](Tiles &t, int &c) {
+                if (++c < c1) return;
+                c = c0;
+                t.next();
+                Tiles after = t;
+                after.next();
+                to_l2(after);
+            };
             tile.start(p, tables);
             to_l2(tile);
             if (tile.valid()) {
                 Tiles second = tile;
                 second.next();
                 to_l2(second);
-                load(tile, c0);
             }
-            while (ok && tile.valid()) {
-                Tiles ahead = tile;
-                int ahead_chunk = chunk + 1;
-                if (ahead_chunk == c1) {
-                    ahead_chunk = c0;
-                    ahead.next();
-                    Tiles after = ahead;
-                    after.next();
-                    to_l2(after);
-                }
-                if (p.aligned) {
+            // one copy of each part of the loop: its instructions are what the
+            // block's other warps wait for in the instruction cache
+            Tiles ahead = tile;
+            int ahead_chunk = c0, steps = odd;
+            for (bool have = false;; have = true, steps = stride) {
+#pragma unroll 1
+                for (int i = 0; i < steps && ahead.valid(); ++i) step(ahead, ahead_chunk);
+                if (have) {
+                    if (p.aligned) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[i][j] = raw[i][j];
-                } else {
-                    int rows, valid;
-                    const uint8_t *at = chunk_at(tile, chunk, rows, valid);
+                            for (int j = 0; j < 8; ++j) v[i][j] = raw[i][j];
+                    } else {
+                        int rows, valid;
+                        const uint8_t *at = chunk_at(tile, chunk, rows, valid);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        shift_scales(raw[i], at + (int64_t)(32 * i) * row_bytes, 32 * i < rows ? valid : 0, v[i]);
+                        for (int i = 0; i < 4; ++i)
+                            shift_scales(raw[i], at + (int64_t)(32 * i) * row_bytes, 32 * i < rows ? valid : 0, v[i]);
+                    }
                 }
                 if (ahead.valid()) load(ahead, ahead_chunk);
-                ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_sffree[ch]), phase ^ 1, abort, p.status));
-                if (ok) {
+                if (have) {
+                    if (!__all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_sffree[ch]), phase ^ 1, abort, p.status))) break;
                     uint8_t *to = sf_ptr + (size_t)ch * p.chunk_bytes + (weights ? 0 : kChunkA + 512 * block) + lane * 16;
-                    const int step = 512 * (weights ? 1 : p.nb);
+                    const int pitch = 512 * (weights ? 1 : p.nb);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)   // 128 values each; past the row's end zeros that nothing reads
-                        *reinterpret_cast<uint4 *>(to + j * step) = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
+                        *reinterpret_cast<uint4 *>(to + j * pitch) = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) bar_arrive_remote(in_block(smem_u32(&s_sffull[ch]), lead));
-                    if (++ch == p.chunks) ch = 0, phase ^= 1;
+                    ch += stride;
+                    if (ch >= p.chunks) ch -= p.chunks, phase ^= 1;
                 }
+                if (!ahead.valid()) break;
                 tile = ahead;
                 chunk = ahead_chunk;
             }
@@ -804,6 +814,11 @@ cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows
     p.chunks = room - (size_t)stages * p.stage_bytes >= 3 * p.chunk_bytes ? 3 : 2;
     p.stages = stages;
     p.aligned = K % 512 == 0 && ((reinterpret_cast<uintptr_t>(sa) | reinterpret_cast<uintptr_t>(sw)) & 15) == 0;
+    // Few rows an expert: the weights come fast, and one warp for their scales is
+    // what the ring waits for (64 experts, 7168 -> 2048: 16 rows 91 us with one warp,
+    // 82 with two, 128 rows 103 and 99).  Many rows: the second only takes issue
+    // slots (2048 -> 7168: 256 rows 177 and 195 us, 512 rows 293 and 310).
+    p.sfwarps = p.nt <= 176 ? 2 : 1;
     p.wide = F % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
     const size_t smem = 1024 + (size_t)stages * p.stage_bytes + (size_t)p.chunks * p.chunk_bytes + kOutBytes + tables;
 
@@ -827,7 +842,7 @@ cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows
     if (pairs > most) pairs = most;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs * p.split));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(p.sfwarps == 2 ? kThreads : kThreads - 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
