@@ -239,27 +239,18 @@ __device__ __forceinline__ void cluster_sync() {
 
 // ---- the list of tiles -----------------------------------------------------------------------
 
-// Rows [r0, r0 + m) of expert e.  Offsets that run backwards or out of the
-// buffer are clamped and reported.
+// Rows [r0, r0 + m) of expert e.  `bad`: offsets that run backwards or out of the
+// buffer.  Where no expert's are, the experts' rows are apart and in the buffer.
 __device__ __forceinline__ void expert_rows(const Params &p, int e, int &r0, int &m, bool &bad) {
     if (p.off == nullptr) {
         r0 = 0;
         m = (int)p.rows;
         return;
     }
-    const int64_t a = __ldg(p.off + e), b = __ldg(p.off + e + 1);
-    if (a < 0 || b < a) bad = true;
-    if (p.cap > 0) {
-        const int64_t c = b - a;
-        r0 = (int)(e * p.cap);
-        m = (int)(c < 0 ? 0 : c > p.cap ? p.cap : c);
-    } else {
-        if (b > p.rows) bad = true;
-        const int64_t x = a < 0 ? 0 : a > p.rows ? p.rows : a;
-        const int64_t z = b < x ? x : b > p.rows ? p.rows : b;
-        r0 = (int)x;
-        m = (int)(z - x);
-    }
+    const int64_t a = __ldg(p.off + e), b = __ldg(p.off + e + 1), n = b - a;
+    if (a < 0 || n < 0 || (p.cap == 0 && b > p.rows)) bad = true;
+    r0 = (int)(p.cap > 0 ? e * p.cap : a);
+    m = (int)(p.cap > 0 && n > p.cap ? p.cap : n);
 }
 
 // One tile: features [f0, f0 + 128) of expert e in this block (the pair's 256
@@ -486,9 +477,12 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         tables[p.E + 1 + e] = r0;
         tables[2 * p.E + 1 + e] = m;
     }
+    // bad offsets: no tiles at all, for the sums below hold only where rows do not overlap
+    const bool refused = __syncthreads_or(bad) != 0;
     if (bad && blockIdx.x == 0) report(p.status, kErrRange);
-    __syncthreads();
-    if (warp == 0) {
+    if (refused) {
+        for (int e = threadIdx.x; e <= p.E; e += blockDim.x) tables[e] = 0;
+    } else if (warp == 0) {
         const int per = (p.E + 31) / 32, e0 = lane * per, e1 = e0 + per < p.E ? e0 + per : p.E;
         int sum = 0;
         for (int e = e0; e < e1; ++e) sum += ((uint32_t)tables[2 * p.E + 1 + e] + p.nt - 1) / p.nt;
@@ -798,7 +792,8 @@ cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows
     Params p = {};
     p.sa = sa, p.sw = sw, p.off = off, p.y = y, p.status = status;
     p.rows = rows, p.cap = cap, p.E = E, p.F = F, p.K = K;
-    // Columns a tile: twice the mean rows of an expert (a padded one's capacity), so that few experts need two tiles.
+    // Columns a tile: a quarter over the mean rows of an expert (a padded one's
+    // capacity), so that few experts need two tiles.
     const int64_t mean = (rows + E - 1) / E, want = cap > 0 ? cap : mean + mean / 4 + 8;
     p.nt = want >= kMaxNt ? kMaxNt : want <= 32 ? 32 : (int)((want + 15) / 16 * 16);
     p.nb = p.nt > 128 ? 2 : 1;

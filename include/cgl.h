@@ -494,7 +494,7 @@ cgl_status cgl_dispatch_mxfp4(const uint16_t *x, int64_t num_tokens, int hidden,
  * are stored faster).  opts: capacity, num_sms (blocks work in pairs: at least
  * two SMs).
  * Device errors: CGL_ERANGE when offsets run backwards or past num_rows
- * (clamped); CGL_ETIMEOUT if a bounded wait (about a second) inside a block pair
+ * (nothing is computed then); CGL_ETIMEOUT if a bounded wait (about a second) inside a block pair
  * gives up, y then undefined.
  */
 cgl_status cgl_matmul_mxfp4(const uint8_t *a, const uint8_t *a_scale, int64_t num_rows, const uint8_t *w,

@@ -143,14 +143,23 @@ def test_extreme_scales():
     assert torch.isinf(y[8:, 64:]).all()           # 64 * 2^254
 
 
-def test_bad_offsets_are_reported_and_stay_in_the_buffer():
-    a, sa, w, sw, off, _ = _case([8, 8], 64, 32, 5)
-    for bad in ([0, 9, 4], [0, 8, 17], [-3, 8, 16]):
+@pytest.mark.parametrize("k", [64, 4096])       # 4096: pairs share a tile
+def test_bad_offsets_are_reported_and_nothing_is_computed(k):
+    a, sa, w, sw, off, _ = _case([8, 8, 0], k, 32, 5)
+    for bad in ([0, 9, 4, 16], [0, 8, 17, 17], [-3, 8, 16, 16], [0, 16, 0, 16], [16, 0, 16, 0], [0, 8, 2 ** 31 - 1, 16]):
         st = cgl.new_status()
         y = torch.full((18, 32), -7.0, dtype=torch.bfloat16, device="cuda")
         cgl.matmul_mxfp4(a, sa, w, sw, torch.tensor(bad, dtype=torch.int32, device="cuda"), y=y[:16], status=st)
         assert cgl.status_bits(st) == ["CGL_ERANGE"]
-        assert (y[16:] == -7.0).all()
+        assert (y == -7.0).all()
+    # padded rows: only offsets that run backwards are wrong, more copies than rows are the layout's overflow
+    st = cgl.new_status()
+    y = torch.full((15, 32), -7.0, dtype=torch.bfloat16, device="cuda")
+    for offs, bits in (([0, 9, 4, 16], ["CGL_ERANGE"]), ([0, 900, 900, 2000], [])):
+        st = cgl.new_status()
+        cgl.matmul_mxfp4(a[:15], sa[:15], w, sw, torch.tensor(offs, dtype=torch.int32, device="cuda"), 5, y=y, status=st)
+        assert cgl.status_bits(st) == bits
+        assert ((y == -7.0).all() if bits else (y[5:10] == -7.0).all() and (y[:5] != -7.0).any())
 
 
 def test_same_answer_every_time_and_on_one_sm():
