@@ -643,6 +643,20 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             const auto load = [&](const Tiles &t, int c) {
                 int rows, valid;
                 const uint8_t *at = chunk_at(t, c, rows, valid);
+                if (p.aligned) {   // the plain form, for its fewer instructions
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 *q = reinterpret_cast<const uint4 *>(at + (int64_t)(32 * i) * row_bytes);
+                        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                        if (32 * i < rows) {
+                            a = __ldg(q);
+                            if (valid > 16) b = __ldg(q + 1);
+                        }
+                        raw[i][0] = a.x, raw[i][1] = a.y, raw[i][2] = a.z, raw[i][3] = a.w;
+                        raw[i][4] = b.x, raw[i][5] = b.y, raw[i][6] = b.z, raw[i][7] = b.w;
+                    }
+                    return;
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     load_scales(at + (int64_t)(32 * i) * row_bytes, 32 * i < rows ? valid : -16, begin, end, raw[i]);
