@@ -256,7 +256,7 @@ __device__ __forceinline__ void expert_rows(const Params &p, int e, int &r0, int
 // One tile: features [f0, f0 + 128) of expert e in this block (the pair's 256
 // side by side; f0 may be past the last one), token rows [row0, row0 + n).
 struct Tiles {
-    const int32_t *first, *row0s, *counts;   // shared: tiles' prefix sums over experts, rows
+    const int32_t *first, *row0s, *counts, *pers;   // shared: tiles' prefix sums over experts, rows, rows a tile
     int ftiles, rank, last;                  // last: tiles of rows in all
     int q, ft, dq, dft;                      // the tile of rows and of features, and the step from one tile to the next
     int e, begin, end, per, rows0, stop;     // expert: its tiles of rows, rows a tile, its rows
@@ -266,6 +266,7 @@ struct Tiles {
         first = tables;
         row0s = tables + p.E + 1;
         counts = row0s + p.E;
+        pers = counts + p.E;
         ftiles = (p.F + 2 * kM - 1) / (2 * kM);
         rank = (int)(blockIdx.x & 1);
         last = first[p.E];
@@ -282,7 +283,6 @@ struct Tiles {
         if (ft >= ftiles) ft -= ftiles, ++q;
         place();
     }
-    // Rows of a tile: the expert's, in equal parts of at most nt, rounded up to 16.
     __device__ __forceinline__ void place() {
         if (q >= last) return;
         if (q >= end) {
@@ -290,10 +290,9 @@ struct Tiles {
                 begin = end;
                 end = first[++e + 1];
             } while (end <= q);
-            const uint32_t m = counts[e], parts = end - begin;
-            per = (int)(((m + parts - 1) / parts + 15) & ~15u);
+            per = pers[e];
             rows0 = row0s[e];
-            stop = rows0 + (int)m;
+            stop = rows0 + counts[e];
         }
         f0 = (2 * ft + rank) * kM;
         row0 = rows0 + (q - begin) * per;
@@ -469,13 +468,16 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     }
     griddep_wait();
 
-    // tables: first[E + 1] (tiles of nt rows before each expert), row0[E], rows[E]
+    // tables: first[E + 1] (tiles of nt rows before each expert), row0[E], rows[E], rows a tile[E]
     bool bad = false;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
         int r0, m;
         expert_rows(p, e, r0, m, bad);
         tables[p.E + 1 + e] = r0;
         tables[2 * p.E + 1 + e] = m;
+        // rows of a tile: the expert's, in equal parts of at most nt, rounded up to 16
+        const uint32_t parts = ((uint32_t)m + p.nt - 1) / p.nt;
+        tables[3 * p.E + 1 + e] = parts > 0 ? (int)((((uint32_t)m + parts - 1) / parts + 15) & ~15u) : 0;
     }
     // bad offsets: no tiles at all, for the sums below hold only where rows do not overlap
     const bool refused = __syncthreads_or(bad) != 0;
@@ -814,7 +816,7 @@ cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows
     p.box = p.nt > 64 ? 32 : 16;
     p.stage_bytes = kABytes + (p.nt / 2 + p.box - 1) / p.box * p.box * (kStageK / 2);
     p.chunk_bytes = kChunkA * (1 + p.nb);
-    const size_t tables = (size_t)(3 * E + 1) * 4;
+    const size_t tables = (size_t)(4 * E + 1) * 4;
     const size_t room = kSmemLimit - 1024 - kOutBytes - tables;
     int stages = (int)((room - 2 * p.chunk_bytes) / p.stage_bytes);
     const int by_tmem = (512 - 2 * p.nt) / (8 + 8 * p.nb);
