@@ -31,13 +31,13 @@
 //
 // What bounds it (one B200; floors at the measured 6.53 TB/s copy and four times
 // the measured bf16 rate): few rows an expert, the weights' bytes: 4 rows, 7168 ->
-// 4096, 256 experts 612 us, 6.4 TB/s; 128 rows 683 us against 672, and 770 to 850
-// when run for seconds, where the 1000 W cap takes the clock to 1.0 GHz.  Many
+// 4096, 256 experts 603 us, 6.5 TB/s; 128 rows 680 to 710 us against 672, and 770
+// to 860 when run for seconds, where the 1000 W cap takes the clock to 1.0 GHz.  Many
 // rows: the bytes that the SMs take from L2, at 64 a cycle and SM: 512 rows a
-// expert on average, 2048 -> 7168: 1.03 ms (1.16 to 1.24 in a long run) against
+// expert on average, 2048 -> 7168: 1.04 ms (1.15 to 1.20 in a long run) against
 // 615; without the loads 0.82, with all weights in L2 1.05.  More columns a tile
 // would take fewer bytes (160, 192, 208: 1.35, 1.23, 1.16 ms in a long run), but
-// two accumulators and the scales fill TMEM at 208.  One row, 7168 -> 4096: 14.7
+// two accumulators and the scales fill TMEM at 208.  One row, 7168 -> 4096: 12.7
 // us, of which the launch, the tables and the first loads are 8.
 //
 // Every wait is bounded (about a second, then CGL_ETIMEOUT): the block's roles
