@@ -38,6 +38,7 @@ constexpr int64_t kChunkIds = 4096;    // ids a histogram block
 constexpr int kCluster = 8;            // histogram blocks a cluster, where a sequence has more than one
 constexpr int kMaxParts = 16;          // clusters a sequence
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFar = 1048576.0f;     // 2^20, see the softmax
 
 struct Shape {
     int64_t tokens;      // per sequence
@@ -355,10 +356,14 @@ balance_main_kernel(const void *__restrict__ logits, const int32_t *__restrict__
         if (m == -INFINITY) m = 0.0f;        // nothing left (or NaN): exp(-inf) below, not exp(nan)
         float sum = 0.0f, dot = 0.0f;
         if (!SIG) {
-            const float shift = -m * kLog2e;   // its rounding is a factor that all p share
-            if (__any_sync(0xFFFFFFFFu, fmaf(low, kLog2e, shift) < -125.0f)) {
+            // The shift's rounding is a factor that all p share: at most 2^(2^-4) up
+            // to |m| = kFar.  Past it that factor would leave binary32's range, so
+            // there the difference is taken first.
+            const bool far = fabsf(m) > kFar;
+            const float base = far ? m : 0.0f, shift = far ? 0.0f : -m * kLog2e;
+            if (__any_sync(0xFFFFFFFFu, far || fmaf(low, kLog2e, shift) < -125.0f)) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) p[i] = ex2<false>(fmaf(l[i], kLog2e, shift));
+                for (int i = 0; i < V; ++i) p[i] = ex2<false>(fmaf(l[i] - base, kLog2e, shift));
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i) p[i] = ex2<true>(fmaf(l[i], kLog2e, shift));
@@ -399,7 +404,8 @@ balance_main_kernel(const void *__restrict__ logits, const int32_t *__restrict__
         }
         sum = group_sum<LANES>(sum);
         dot = group_sum<LANES>(dot);
-        const bool none = sum == 0.0f || !any;   // every logit -inf, or a token without a copy
+        // Every logit -inf (else the largest one's term is 0.4 or more), or a token without a copy.
+        const bool none = sum == 0.0f || !any;
         const float inv = none ? 0.0f : __fdiv_rn(1.0f, sum);
         dot = none ? 0.0f : dot * inv;
         if (!none && lane == 0) acc += (double)(mean + dot);
