@@ -466,9 +466,14 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # cgl_dtype
 _SCORES = {"softmax": 0, "sigmoid": 1}                              # cgl_score
 
 
-def _on(stream):
-    """Makes `stream` (a torch stream or a handle) current, so that what a call allocates belongs to it as well."""
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+def _on(stream, t: torch.Tensor, name: str):
+    """Makes `stream` (a torch stream or a handle) current on t's device, so that what a call allocates belongs to it as well."""
+    device = _dev(t, name).device
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)   # without a device: the current one's
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, {name} on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _launch(where: str, fn, device, *args):
@@ -514,7 +519,7 @@ def quantize_mxfp4(x: torch.Tensor, *, codes: Optional[torch.Tensor] = None,
     Returns (codes uint8 [..., C/2], two codes a byte with the lower index in the low half;
     scales uint8 [..., C/32], 2^(byte - 127)).  Blocks with an infinity or NaN get scale byte 255 (NaN)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x, "x"):
             return quantize_mxfp4(x, codes=codes, scales=scales, num_sms=num_sms)
     x = _dev(x, "x")
     dt = _float_type(x, "x")
@@ -532,7 +537,7 @@ def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dty
                      out: Optional[torch.Tensor] = None, num_sms: int = 0, stream=None) -> torch.Tensor:
     """The values MXFP4 codes [..., C/2] and scales [..., C/32] stand for, [..., C] (cgl_dequantize_mxfp4)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, codes, "codes"):
             return dequantize_mxfp4(codes, scales, dtype, out=out, num_sms=num_sms)
     codes = _dev(codes, "codes", torch.uint8)
     scales = _dev(scales, "scales", torch.uint8)
@@ -559,7 +564,7 @@ def dispatch_mxfp4(x: torch.Tensor, dst_pos: torch.Tensor, num_recv_rows: int, *
     Returns (recv_x uint8 [rows, H/2], recv_scale uint8 [rows, H/32]); rows that receive no copy
     are left as they were (uninitialised when allocated here)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x, "x"):
             return dispatch_mxfp4(x, dst_pos, num_recv_rows, recv_x=recv_x, recv_scale=recv_scale, status=status,
                                   num_sms=num_sms, scratch=scratch)
     x = _dev(x, "x", torch.bfloat16, 2)
@@ -588,7 +593,7 @@ def matmul_mxfp4(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scal
     capacity as get_layout gives them; without expert_offset w has one expert (or is [out, in/2])
     and takes every row.  Rows of no expert are left as they were."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, a, "a"):
             return matmul_mxfp4(a, a_scale, w, w_scale, expert_offset, capacity, y=y, status=status, num_sms=num_sms)
     a = _dev(a, "a", torch.uint8, 2)
     a_scale = _dev(a_scale, "a_scale", torch.uint8, 2)
@@ -653,7 +658,7 @@ def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, *, num_sequences:
     takes no part).  score: "softmax", or "sigmoid" (normalised over the experts).  grad_loss: fp32 [1] on the
     device, the gradient that arrives at the loss; without it, balance_loss_backward gives grad_logits later."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, logits, "logits"):
             return balance_loss(logits, topk_idx, num_sequences=num_sequences, alpha=alpha, score=score,
                                 grad_loss=grad_loss, loss=loss, counts=counts, num_routed=num_routed,
                                 grad_logits=grad_logits, workspace=workspace, status=status)
@@ -695,7 +700,7 @@ def balance_loss_backward(grad_loss: torch.Tensor, logits: torch.Tensor, topk_id
                           stream=None) -> torch.Tensor:
     """Gradient of balance_loss for the logits, from the forward's counts and num_routed (cgl_balance_loss_backward)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, logits, "logits"):
             return balance_loss_backward(grad_loss, logits, topk_idx, counts, num_routed, num_sequences=num_sequences,
                                          alpha=alpha, score=score, grad_logits=grad_logits)
     logits, idx, dt, n, k, E, _ = _balance_args(logits, topk_idx, score, num_sequences, "balance_loss_backward")
