@@ -108,6 +108,7 @@ balance_count_kernel(const int32_t *__restrict__ idx, int64_t tokens, int k, int
     const int64_t t0 = c * per_chunk, t1 = t0 + per_chunk < tokens ? t0 + per_chunk : tokens;
     const bool vec = (k & 3) == 0 && (reinterpret_cast<uintptr_t>(idx) & 15) == 0;
     bool bad = false;
+    int routed = 0;
     for (int64_t t = t0 + threadIdx.x; t < t1; t += kCountThreads) {
         const int32_t *p = idx + (seq * tokens + t) * k;
         bool any = false;
@@ -131,9 +132,10 @@ balance_count_kernel(const int32_t *__restrict__ idx, int64_t tokens, int k, int
                 }
             }
         }
-        const uint32_t m = __ballot_sync(__activemask(), any);
-        if ((threadIdx.x & 31) == __ffs(__activemask()) - 1 && m) atomicAdd(&s_count[E], __popc(m));
+        routed += any;
     }
+    routed = __reduce_add_sync(0xFFFFFFFFu, routed);   // behind the loop, which lanes leave apart: all 32 are here
+    if ((threadIdx.x & 31) == 0 && routed > 0) atomicAdd(&s_count[E], routed);
     if (chunks == 1) {
         __syncthreads();
         for (int e = threadIdx.x; e <= E; e += kCountThreads) part[(int64_t)blockIdx.x * (E + 1) + e] = s_count[e];
