@@ -97,12 +97,22 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n.reg .pred p;\n"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n"
         "selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
+}
+// Half of what a barrier counts is done by the pair's other block (arrivals,
+// copies' bytes, commits), so every wait has cluster scope; this fence after it
+// makes what the others wrote to shared memory before they arrived theirs to read.
+// It is restricted to shared memory, as is its counterpart in bar_arrive_smem: an
+// acquire or release of all memory at that scope holds a warp until its loads in
+// flight are there (4 rows an expert, 7168 -> 4096: 910 us with those, 620 with
+// these; 128 rows 909 and 689; 512 rows, 2048 -> 7168: 1256 and 1037).
+__device__ __forceinline__ void fence_acquire_smem() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 
 // The same shared-memory address in another block of the cluster.
@@ -111,20 +121,25 @@ __device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// Arrive there.  What the arrival announces is read by the tensor core of the
-// arriving block's own SM (its shared memory, after a proxy fence) or was read
-// from its own TMEM, so the release need not reach past the block: at cluster
-// scope each arrival took 1000 cycles of its warp.
-__device__ __forceinline__ void bar_arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrive at a barrier of the pair's first block, from either block.  _tmem hands
+// back TMEM that tcgen05.ld has read: execution order is all that needs, with
+// tcgen05's fences on both sides.  _smem announces what this warp wrote to its
+// own shared memory (after a proxy fence), which the tensor core reads on behalf
+// of a thread of the first block.
+__device__ __forceinline__ void bar_arrive_tmem(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_smem(uint32_t bar) {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Whether a phase has ended, without waiting.
+// Whether a phase has ended, without waiting (where it has, fence_acquire_smem is still to come).
 __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n.reg .pred p;\n"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n"
         "selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -134,17 +149,19 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
 
 // Bounded wait for a phase; false once this wait or another of the block has given up.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *status) {
-    if (bar_try(bar, parity)) return true;
-    const long long start = clock64();
-    for (;;) {
-        if (bar_try(bar, parity)) return true;
-        if (*abort) return false;
-        if (clock64() - start > kWaitCycles) {
-            *abort = 1;
-            report(status, kErrTimeout);
-            return false;
+    if (!bar_try(bar, parity)) {
+        const long long start = clock64();
+        while (!bar_try(bar, parity)) {
+            if (*abort) return false;
+            if (clock64() - start > kWaitCycles) {
+                *abort = 1;
+                report(status, kErrTimeout);
+                return false;
+            }
         }
     }
+    fence_acquire_smem();
+    return true;
 }
 
 // One lane of a converged warp, always the same.  What the elected lane issues
@@ -569,6 +586,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                     ++s, base += stage_bytes, tsf += sf_cols;
                     if (s == stages) s = 0, base = ring, tsf = sf0, phase ^= 1;
                     ready = bar_test(full0 + 8 * s, phase);
+                    fence_acquire_smem();
                     if (elect_one() && ok) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)     // 64 values: 32 bytes (two units) of each row
@@ -720,7 +738,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                         *reinterpret_cast<uint4 *>(to + j * pitch) = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
                     fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0) bar_arrive_remote(in_block(smem_u32(&s_sffull[ch]), lead));
+                    if (lane == 0) bar_arrive_smem(in_block(smem_u32(&s_sffull[ch]), lead));
                     ch += stride;
                     if (ch >= p.chunks) ch -= p.chunks, phase ^= 1;
                 }
@@ -739,7 +757,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             store_tile(p, tile, tmem + acc * p.nt, warp & 3, lane, out, out_ptr, nullptr, 0);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive_remote(in_block(smem_u32(&s_accfree[acc]), lead));
+            if (lane == 0) bar_arrive_tmem(in_block(smem_u32(&s_accfree[acc]), lead));
             acc ^= 1;
             if (acc == 0) accphase ^= 1;
         }
