@@ -555,6 +555,9 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 if (++s == p.stages) s = 0, phase ^= 1;
             }
         }
+        // Once more round the ring, a lane a place: the last releases are arrivals from
+        // the first block, and a block must not leave before they have reached its barriers.
+        if (ok && warp == 0 && lane < p.stages) ok = bar_wait(smem_u32(&s_empty[lane]), lane < s ? phase : phase ^ 1, abort, p.status);
         // Without an error the MMA warp has waited for every copy.  With one, those
         // in flight (issued at most a stage ring ago) get 2^28 cycles to land.
         if (!ok)
@@ -711,6 +714,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             // block's other warps wait for in the instruction cache
             Tiles ahead = tile;
             int ahead_chunk = c0, steps = odd;
+            bool ok = true;
             for (bool have = false;; have = true, steps = stride) {
 #pragma unroll 1
                 for (int i = 0; i < steps && ahead.valid(); ++i) step(ahead, ahead_chunk);
@@ -730,7 +734,8 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 }
                 if (ahead.valid()) load(ahead, ahead_chunk);
                 if (have) {
-                    if (!__all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_sffree[ch]), phase ^ 1, abort, p.status))) break;
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_sffree[ch]), phase ^ 1, abort, p.status));
+                    if (!ok) break;
                     uint8_t *to = sf_ptr + (size_t)ch * p.chunk_bytes + (weights ? 0 : kChunkA + 512 * block) + lane * 16;
                     const int pitch = 512 * (weights ? 1 : p.nb);
 #pragma unroll
@@ -746,6 +751,8 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 tile = ahead;
                 chunk = ahead_chunk;
             }
+            // the last releases of this ring, as those of the stages' (warp 3 has filled every place of it)
+            if (ok && warp == 3 && lane < p.chunks) bar_wait(smem_u32(&s_sffree[lane]), lane < ch ? phase : phase ^ 1, abort, p.status);
         }
     } else if (warp >= 4 && warp < 8) {
         int acc = 0;

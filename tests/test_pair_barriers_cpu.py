@@ -33,3 +33,25 @@ def test_relaxed_operations_stand_with_their_fences():
     assert "fence.acquire.sync_restrict::shared::cluster.cluster" in SOURCE
     assert re.search(r"= bar_test\([^;]*;\s*fence_acquire_smem\(\);", SOURCE)
     assert re.search(r"fence_proxy_async\(\);\s*__syncwarp\(\);\s*if \(lane == 0\) bar_arrive_smem\(", SOURCE)
+
+
+def _arrivals_left(fills, slots, tail):
+    """Arrivals at one block's ring that nothing in it has waited for when the role that fills it leaves: fill n waits for
+    the release of fill n - slots, the tail for those of `slots` fills more.  Each release is an arrival from the pair's
+    first block, which may still be under way."""
+    seen = {n - slots for n in range(fills + (slots if tail else 0)) if n >= slots}
+    return set(range(fills)) - seen
+
+
+def test_a_ring_without_a_tail_leaves_arrivals_under_way():
+    for fills in range(0, 30):
+        for slots in (2, 3, 4, 12):
+            assert len(_arrivals_left(fills, slots, False)) == min(fills, slots)
+            assert not _arrivals_left(fills, slots, True)
+
+
+def test_no_block_leaves_before_the_last_arrivals_of_its_rings():
+    """The roles that fill a ring wait as if to go round it once more: the stages' ring (s_empty) and the scales' (s_sffree)."""
+    for ring, slots, place in (("s_empty", "p.stages", "s"), ("s_sffree", "p.chunks", "ch")):
+        tail = rf"if \(ok && warp == \d && lane < {re.escape(slots)}\) (?:ok = )?bar_wait\(smem_u32\(&{ring}\[lane\]\), lane < {place} \? phase : phase \^ 1,"
+        assert re.search(tail, SOURCE), ring
