@@ -396,6 +396,18 @@ cgl_status cgl_matmul_mxfp4(const uint8_t *a, const uint8_t *a_scale, int64_t nu
                                status_dev, static_cast<cudaStream_t>(stream));
 }
 
+cgl_status cgl_selftest_matmul_timeout(const uint8_t *a, const uint8_t *a_scale, int64_t num_rows, const uint8_t *w,
+                                       const uint8_t *w_scale, int F, int K, uint16_t *y, int64_t wait_cycles,
+                                       uint32_t *status_dev, void *stream) {
+    if (F < 1 || F > (1 << 20) || K < 32 || K % 32 != 0 || K > (1 << 20) || num_rows < 1 || num_rows > (1 << 20) ||
+        wait_cycles < 0)
+        return CGL_EINVAL;
+    if (!a || !a_scale || !w || !w_scale || !y || !status_dev) return CGL_EINVAL;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(y, 2) || !aligned(status_dev, 4)) return CGL_EALIGN;
+    return launch_matmul_mxfp4(a, a_scale, num_rows, w, w_scale, 1, F, K, nullptr, 0, y, 0, status_dev,
+                               static_cast<cudaStream_t>(stream), wait_cycles);
+}
+
 static bool balance_sizes_ok(int64_t n, int k, int E, int64_t S) {
     return n >= 0 && k >= 1 && k <= kMaxTopk && E >= 1 && E <= kMaxExperts && S >= 1 && S <= ((int64_t)1 << 24) &&
            n % S == 0 && n * (int64_t)k < ((int64_t)1 << 31);

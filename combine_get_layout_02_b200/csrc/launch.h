@@ -119,10 +119,10 @@ cgl_status launch_dispatch_mxfp4(const uint16_t *x, int64_t n, int h, int k, con
                                  uint8_t *recv_scale, int64_t recv_rows, int num_sms, uint32_t *status,
                                  cudaStream_t stream, unsigned long long *claim);
 
-// The experts' product on MXFP4 rows (off null: one expert, all rows).
+// The experts' product on MXFP4 rows (off null: one expert, all rows; wait_cycles: a wait's limit, < 0: about a second).
 cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows, const uint8_t *w, const uint8_t *sw,
                                int E, int F, int K, const int32_t *off, int64_t cap, uint16_t *y, int num_sms,
-                               uint32_t *status, cudaStream_t stream);
+                               uint32_t *status, cudaStream_t stream, int64_t wait_cycles = -1);
 
 // Balance loss (score: 0 softmax, 1 normalised sigmoid; grad null: loss and counts only).
 size_t balance_workspace_bytes(int64_t n, int k, int E, int64_t S);

@@ -40,8 +40,9 @@
 // two accumulators and the scales fill TMEM at 208.  One row, 7168 -> 4096: 12.7
 // us, of which the launch, the tables and the first loads are 8.
 //
-// Every wait is bounded (about a second, then CGL_ETIMEOUT): the block's roles
-// leave their loops, copies and MMAs in flight are waited for, TMEM is freed.
+// Every wait is bounded (about a second, then CGL_ETIMEOUT): the pair's roles leave
+// their loops, MMAs in flight are waited for, copies and arrivals under way get
+// 0.15 s to land before either block leaves, TMEM is freed.
 #include <cuda.h>
 
 #include "mxfp4.cuh"
@@ -53,6 +54,7 @@ namespace {
 
 constexpr uint32_t kErrTimeout = 1u << CGL_ETIMEOUT;
 constexpr long long kWaitCycles = 1ll << 31;
+constexpr long long kLandCycles = 1ll << 28;
 constexpr int kThreads = 384;
 constexpr int kStageK = 256;              // values a stage
 constexpr int kChunk = 4;                 // stages a chunk of scales (1024 values, 32 bytes a row)
@@ -81,6 +83,7 @@ struct Params {
     int wide;        // y's rows allow 16-byte stores
     int aligned;     // every scale row starts at a 16-byte boundary
     uint32_t stage_bytes, chunk_bytes;
+    long long wait_cycles;   // a wait's limit: kWaitCycles, less in the self-test
 };
 
 // ---- barriers, TMA, tcgen05 ----------------------------------------------------------------
@@ -115,6 +118,11 @@ __device__ __forceinline__ void fence_acquire_smem() {
     asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
 // The same shared-memory address in another block of the cluster.
 __device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -147,15 +155,22 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Bounded wait for a phase; false once this wait or another of the block has given up.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *status) {
+// Tells both blocks of the pair that a wait has run out: a word in each one's shared memory.
+__device__ __forceinline__ void give_up(volatile int *abort, uint32_t *status) {
+    const uint32_t word = smem_u32(const_cast<const int *>(abort));
+    *abort = 1;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_block(word, cluster_rank() ^ 1)), "r"(1) : "memory");
+    report(status, kErrTimeout);
+}
+
+// Bounded wait for a phase; false once this wait or another of the pair has given up.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *abort, const Params &p) {
     if (!bar_try(bar, parity)) {
         const long long start = clock64();
         while (!bar_try(bar, parity)) {
             if (*abort) return false;
-            if (clock64() - start > kWaitCycles) {
-                *abort = 1;
-                report(status, kErrTimeout);
+            if (clock64() - start > p.wait_cycles) {
+                give_up(abort, p.status);
                 return false;
             }
         }
@@ -245,11 +260,6 @@ __device__ __forceinline__ void stmatrix_trans(uint32_t addr, uint32_t a, uint32
                  : "memory");
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -539,7 +549,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             const uint32_t box_bytes = p.box * (kStageK / 2);
             const int row0 = tile.row0 + tile.rank * half;
             for (int k = k0; k < k1; ++k) {
-                ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_empty[s]), phase ^ 1, abort, p.status));
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_empty[s]), phase ^ 1, abort, p));
                 if (!ok) break;
                 const uint32_t base = ring + s * p.stage_bytes, bar = in_block(smem_u32(&s_full[s]), lead);
                 if (warp == 0) {
@@ -557,11 +567,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         }
         // Once more round the ring, a lane a place: the last releases are arrivals from
         // the first block, and a block must not leave before they have reached its barriers.
-        if (ok && warp == 0 && lane < p.stages) ok = bar_wait(smem_u32(&s_empty[lane]), lane < s ? phase : phase ^ 1, abort, p.status);
-        // Without an error the MMA warp has waited for every copy.  With one, those
-        // in flight (issued at most a stage ring ago) get 2^28 cycles to land.
-        if (!ok)
-            for (const long long start = clock64(); clock64() - start < (1ll << 28);) {}
+        if (ok && warp == 0 && lane < p.stages) bar_wait(smem_u32(&s_empty[lane]), lane < s ? phase : phase ^ 1, abort, p);
     } else if ((warp == 1 || warp == 10) && first) {
         // What bounds this loop is its instructions: 20 to 30 cycles for each that it
         // issues, as much for each branch.  Hence two warps, a wait that is asked for
@@ -579,10 +585,10 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             bool ready = false;
             for (; ok && tile.valid(); tile.next()) {
                 const uint32_t i0 = instr_desc(tile.columns(), 0), i2 = instr_desc(tile.columns(), 2);
-                ok = bar_wait(smem_u32(&s_accfree[acc]), accphase ^ 1, abort, p.status);
+                ok = bar_wait(smem_u32(&s_accfree[acc]), accphase ^ 1, abort, p);
                 const uint32_t d = tmem + acc * p.nt;
                 for (int k = k0; k < k1; ++k) {
-                    if (!ready) ok = ok && bar_wait(full0 + 8 * s, phase, abort, p.status);
+                    if (!ready) ok = ok && bar_wait(full0 + 8 * s, phase, abort, p);
                     tc_fence_after();
                     const uint32_t empty = empty0 + 8 * s, ta = tsf, tb = tsf + 8;
                     const uint64_t da = desc_rows(base), db = desc_rows(base + kABytes);
@@ -609,13 +615,13 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             for (; ok && tile.valid(); tile.next()) {
                 const bool two = tile.columns() > 128;
                 for (int k = k0; k < k1; k += kChunk) {
-                    ok = ok && bar_wait(smem_u32(&s_sffull[ch]), chphase, abort, p.status);
+                    ok = ok && bar_wait(smem_u32(&s_sffull[ch]), chphase, abort, p);
                     const uint32_t sf = sf_ring + ch * p.chunk_bytes;
                     const uint64_t sa = desc_scales(sf), sb = desc_scales(sf + kChunkA);
 #pragma unroll
                     for (int j = 0; j < kChunk; ++j) {
                         if (k + j >= k1) break;
-                        ok = ok && bar_wait(empty0 + 8 * s, phase ^ 1, abort, p.status);
+                        ok = ok && bar_wait(empty0 + 8 * s, phase ^ 1, abort, p);
                         tc_fence_after();
                         if (elect_one() && ok) {
 #pragma unroll
@@ -734,7 +740,7 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 }
                 if (ahead.valid()) load(ahead, ahead_chunk);
                 if (have) {
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_sffree[ch]), phase ^ 1, abort, p.status));
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_sffree[ch]), phase ^ 1, abort, p));
                     if (!ok) break;
                     uint8_t *to = sf_ptr + (size_t)ch * p.chunk_bytes + (weights ? 0 : kChunkA + 512 * block) + lane * 16;
                     const int pitch = 512 * (weights ? 1 : p.nb);
@@ -752,13 +758,13 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 chunk = ahead_chunk;
             }
             // the last releases of this ring, as those of the stages' (warp 3 has filled every place of it)
-            if (ok && warp == 3 && lane < p.chunks) bar_wait(smem_u32(&s_sffree[lane]), lane < ch ? phase : phase ^ 1, abort, p.status);
+            if (ok && warp == 3 && lane < p.chunks) bar_wait(smem_u32(&s_sffree[lane]), lane < ch ? phase : phase ^ 1, abort, p);
         }
     } else if (warp >= 4 && warp < 8) {
         int acc = 0;
         uint32_t accphase = 0;
         for (tile.start(p, tables); tile.valid(); tile.next()) {
-            done = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_accfull[acc]), accphase, abort, p.status));
+            done = __all_sync(0xFFFFFFFFu, bar_wait(smem_u32(&s_accfull[acc]), accphase, abort, p));
             if (!done || p.split > 1) break;
             tc_fence_after();
             store_tile(p, tile, tmem + acc * p.nt, warp & 3, lane, out, out_ptr, nullptr, 0);
@@ -791,6 +797,12 @@ matmul_mxfp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     __syncwarp();
     tc_fence_before();
     cluster_sync();   // the pair's memory, barriers and TMEM stay until both are done
+    // Without an error the MMA warp has waited for every copy of both blocks.  With
+    // one, whichever role it was that gave up, copies and commits may still be under
+    // way; none was issued after the barrier above, and they get 2^28 cycles to land.
+    if (*abort)
+        for (const long long start = clock64(); clock64() - start < kLandCycles;) {}
+    __syncwarp();
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -828,11 +840,12 @@ bool make_map(CUtensorMap *map, const void *p, int64_t row_bytes, int64_t rows, 
 
 cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows, const uint8_t *w, const uint8_t *sw,
                                int E, int F, int K, const int32_t *off, int64_t cap, uint16_t *y, int num_sms,
-                               uint32_t *status, cudaStream_t stream) {
+                               uint32_t *status, cudaStream_t stream, int64_t wait_cycles) {
     if (rows == 0) return CGL_OK;
     Params p = {};
     p.sa = sa, p.sw = sw, p.off = off, p.y = y, p.status = status;
     p.rows = rows, p.cap = cap, p.E = E, p.F = F, p.K = K;
+    p.wait_cycles = wait_cycles < 0 || wait_cycles > kWaitCycles ? kWaitCycles : wait_cycles;
     // Columns a tile: a quarter over the mean rows of an expert (a padded one's
     // capacity), so that few experts need two tiles.
     const int64_t mean = (rows + E - 1) / E, want = cap > 0 ? cap : mean + mean / 4 + 8;

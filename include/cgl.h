@@ -502,6 +502,18 @@ cgl_status cgl_matmul_mxfp4(const uint8_t *a, const uint8_t *a_scale, int64_t nu
                             const int32_t *expert_offset, uint16_t *y, const cgl_opts *opts,
                             uint32_t *status_dev, void *stream);
 
+/*
+ * cgl_selftest_matmul_timeout -- diagnostic for failure detection.  cgl_matmul_mxfp4
+ * for one expert that has every row, with a limit of wait_cycles SM cycles (at most
+ * the usual 2^31) on each wait between the roles of a block pair.  With a limit
+ * shorter than the work, waits run out while copies and MMAs are under way: the
+ * call must then set CGL_ETIMEOUT in *status_dev, return within about half a second
+ * and leave the context usable, with y undefined.
+ */
+cgl_status cgl_selftest_matmul_timeout(const uint8_t *a, const uint8_t *a_scale, int64_t num_rows, const uint8_t *w,
+                                       const uint8_t *w_scale, int out_features, int in_features, uint16_t *y,
+                                       int64_t wait_cycles, uint32_t *status_dev, void *stream);
+
 /* How logits become the probabilities that the balance loss weighs. */
 typedef enum cgl_score {
     CGL_SCORE_SOFTMAX = 0,   /* p = softmax(logits) */

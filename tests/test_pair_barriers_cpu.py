@@ -55,3 +55,16 @@ def test_no_block_leaves_before_the_last_arrivals_of_its_rings():
     for ring, slots, place in (("s_empty", "p.stages", "s"), ("s_sffree", "p.chunks", "ch")):
         tail = rf"if \(ok && warp == \d && lane < {re.escape(slots)}\) (?:ok = )?bar_wait\(smem_u32\(&{ring}\[lane\]\), lane < {place} \? phase : phase \^ 1,"
         assert re.search(tail, SOURCE), ring
+
+
+def test_whichever_role_gives_up_both_blocks_wait_for_what_is_under_way():
+    """A wait that runs out is told to both blocks; behind the barrier that all roles of both have reached, before TMEM is
+    freed and any of them leaves, copies and arrivals get time to land."""
+    kernel = SOURCE[SOURCE.index("matmul_mxfp4_kernel(const __grid_constant__"):]
+    end = kernel[kernel.rindex("cluster_sync();"):kernel.index("tcgen05.dealloc")]
+    assert re.search(r"if \(\*abort\)\s*for \(const long long start = clock64\(\); clock64\(\) - start < kLandCycles;\)", end)
+    assert not re.search(r"\breturn\b", kernel[kernel.index("Tiles tile;"):kernel.index("tcgen05.dealloc")].split("const auto chunk_at")[0])
+    gives_up = re.search(r"void give_up\(.*?\n}", SOURCE, re.S).group()
+    assert "*abort = 1;" in gives_up and "st.shared::cluster" in gives_up and "cluster_rank() ^ 1" in gives_up
+    wait = re.search(r"bool bar_wait\(.*?\n}", SOURCE, re.S).group()
+    assert "give_up(abort" in wait and "*abort = 1" not in wait
