@@ -340,7 +340,7 @@ cgl_status cgl_selftest_bounded_wait(uint64_t *workspace, int nflags, uint32_t *
 
 static bool dtype_ok(int dtype) { return dtype == CGL_BF16 || dtype == CGL_F16 || dtype == CGL_F32; }
 
-// Rows of MXFP4: codes (cols / 2 bytes a row) at most 2^62 values in all.
+// Rows of MXFP4: codes (cols / 2 bytes a row), at most 2^48 values in all.
 static bool mx_sizes_ok(int64_t rows, int64_t cols) {
     return rows >= 0 && cols > 0 && cols % 32 == 0 && cols <= ((int64_t)1 << 30) && rows <= ((int64_t)1 << 32) &&
            rows <= ((int64_t)1 << 48) / cols;

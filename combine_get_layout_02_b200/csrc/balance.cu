@@ -52,9 +52,12 @@ struct Shape {
 
 // The vector form: lanes that share a token, and groups of 8 experts a lane.
 // 16-bit logits of many tokens take two groups a lane where there are over 8
-// (half the lanes, one shuffle round less for two tokens at once): 65536 x 256
-// BF16, loss and gradient as two calls, 52 -> 41 us; binary32 logits need the
-// registers for occupancy (36 -> 40 us), few tokens the warps (12.5 -> 12.6 us).
+// (half the lanes, one shuffle round less for two tokens at once).  BF16, 256
+// experts, loss and gradient as two calls, one group and two: 4096 tokens 13.4 and
+// 12.3 us, 8192 15.6 and 15.1, 12288 19.3 and 17.7, 65536 49.5 and 40.2; with 128
+// experts 11.3 and 10.8, 13.5 and 12.3, 15.3 and 14.5, 29.6 and 25.0.  So the border is
+// where the gain is sure, not where it begins; with the sigmoid 4096 tokens gain
+// nothing (12.5 and 12.6).  Binary32 logits need the registers for occupancy (36 and 40).
 constexpr int64_t kManyTokens = 12288;
 struct Width { int lanes, groups; };
 Width width_for(int64_t n, int E, int dtype) {
@@ -72,6 +75,9 @@ Shape shape(int64_t n, int k, int E, int64_t S, int dtype) {
     s.seqs = S;
     s.k = k;
     s.E = E;
+    // fit: blocks of the main pass a sequence.  Just past a divisor of kMaxBlocks it
+    // leaves some unused (65536 x 256 BF16, loss: 296 sequences 20.1 us, 297 26.2, 592
+    // 21.8), just past kMaxBlocks there is a second wave (593: 25.4).
     const int64_t want = (s.tokens * k + kChunkIds - 1) / kChunkIds, fit = kMaxBlocks / S > 0 ? kMaxBlocks / S : 1;
     int64_t c = 1;
     if (want > 1 && S * kCluster <= 2 * kMaxBlocks) {   // 2: a block has little to do
@@ -164,8 +170,7 @@ balance_count_kernel(const int32_t *__restrict__ idx, int64_t tokens, int k, int
     if (bad) report(status, kErrRange);
 }
 
-// 2^x; with FTZ results below 2^-126 are 0, without it they are subnormal (and
-// the compiler adds three instructions).
+// 2^x; with FTZ results below 2^-126 are 0, without it they are subnormal.
 template <bool FTZ>
 __device__ __forceinline__ float ex2(float x) {
     float r;

@@ -64,11 +64,13 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
 // Programmatic dependent launch (sm_90+).  The copy kernels are launched with
 // programmatic stream serialisation: they may start while the kernel before
 // them is still finishing, so they must griddep_wait() before reading anything
-// it (or an earlier kernel) wrote.  No kernel here triggers its dependents
-// early: each block's exit is its trigger, so the next kernel's blocks launch
-// as this kernel's blocks finish instead of taking SM resources that this
-// kernel's own blocks still need (measured: an early trigger cost 15% of the
-// BF16 step).
+// it (or an earlier kernel) wrote.  The copy kernels do not trigger their
+// dependents early: each block's exit is its trigger, so the next kernel's
+// blocks launch as this kernel's blocks finish instead of taking SM resources
+// that this kernel's own blocks still need (measured: an early trigger cost 15%
+// of the BF16 step).  One kernel triggers early, balance_count_kernel, behind its
+// own wait: balance_main_kernel, which alone may follow it, reads the logits and
+// ids before its wait for the counts.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Bulk asynchronous copy (TMA engine, no tensor map) of `bytes` from shared to

@@ -26,7 +26,11 @@ int copy_grid(const void *kernel, int threads, int64_t work_ctas, int num_sms_ca
 
 // Launch `kernel` with programmatic stream serialisation: it may start while
 // the previous kernel in the stream is finishing, and must griddep_wait()
-// before reading anything that kernel (or an earlier one) wrote.
+// before reading anything that kernel (or an earlier one) wrote.  One exception:
+// balance_main_kernel, always launched right behind balance_count_kernel, reads
+// before its wait what the kernels ahead of that one wrote, because that one's
+// blocks trigger it only behind their own waits.  No kernel may come between the
+// two, and that trigger must stay behind the wait.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, Args... args) {

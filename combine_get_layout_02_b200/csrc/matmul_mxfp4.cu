@@ -26,19 +26,21 @@
 // Scales stay in their rows in memory, [rows, in / 32], because a tile starts at
 // any row of the receive buffer; a warp reads 32 bytes of each row, four stages'
 // worth, one such chunk ahead.
-// Tiles fewer than half of the pairs: two or four pairs share one, a part of K
+// Where tiles are few (see the launcher), two or four pairs share one, a part of K
 // each, and join their sums in order through distributed shared memory.
 //
-// What bounds it (one B200; floors at the measured 6.53 TB/s copy and four times
-// the measured bf16 rate): few rows an expert, the weights' bytes: 4 rows, 7168 ->
-// 4096, 256 experts 603 us, 6.5 TB/s; 128 rows 680 to 710 us against 672, and 770
-// to 860 when run for seconds, where the 1000 W cap takes the clock to 1.0 GHz.  Many
-// rows: the bytes that the SMs take from L2, at 64 a cycle and SM: 512 rows a
-// expert on average, 2048 -> 7168: 1.04 ms (1.15 to 1.20 in a long run) against
-// 615; without the loads 0.82, with all weights in L2 1.05.  More columns a tile
-// would take fewer bytes (160, 192, 208: 1.35, 1.23, 1.16 ms in a long run), but
-// two accumulators and the scales fill TMEM at 208.  One row, 7168 -> 4096: 12.7
-// us, of which the launch, the tables and the first loads are 8.
+// What bounds it (B200; floors at the measured 6.53 TB/s copy and four times the
+// measured bf16 rate; short runs of a few ms, over several cards): few rows an
+// expert, the weights' bytes: 4 rows, 7168 -> 4096, 256 experts 611 to 625 us
+// against 602; 128 rows 667 to 695 against 672, and 757 to 873 when run for
+// seconds, where the 1000 W cap takes the clock to 1.0 GHz.  Many rows: no single
+// unit.  512 rows an expert, 2048 -> 7168: 0.99 to 1.05 ms (1.15 to 1.25 in a long
+// run) against 615 us; the tensor pipe is active half of the time, the SMs take 43
+// bytes a cycle from L2 of the 64 they could, DRAM is at 45%.  In long runs the
+// MMAs without loads took 0.82 ms, with all weights in L2 1.05, and more columns a
+// tile, which take fewer bytes, less (160, 192, 208: 1.35, 1.23, 1.16 ms); two
+// accumulators and the scales fill TMEM at 208.  One row, 7168 -> 4096: 12 us;
+// with 1024 values it is 7, the launch, the tables, the first loads and the stores.
 //
 // Every wait is bounded (about a second, then CGL_ETIMEOUT): the pair's roles leave
 // their loops, MMAs in flight are waited for, copies and arrivals under way get
@@ -179,10 +181,8 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return true;
 }
 
-// One lane of a converged warp, always the same.  What the elected lane issues
-// takes its operands from uniform registers: inside `if (lane == 0)` the
-// compiler makes them uniform one by one, 1300 cycles a stage where the elected
-// lane needs (see the kernel's comment) a tenth of that.
+// One lane of a converged warp, always the same.  Copies and MMAs issued by the
+// elected lane took 300 cycles a stage, inside `if (lane == 0)` 1300.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
@@ -864,9 +864,11 @@ cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows
     p.stages = stages;
     p.aligned = K % 512 == 0 && ((reinterpret_cast<uintptr_t>(sa) | reinterpret_cast<uintptr_t>(sw)) & 15) == 0;
     // Few rows an expert: the weights come fast, and one warp for their scales is
-    // what the ring waits for (64 experts, 7168 -> 2048: 16 rows 91 us with one warp,
-    // 82 with two, 128 rows 103 and 99).  Many rows: the second only takes issue
-    // slots (2048 -> 7168: 256 rows 177 and 195 us, 512 rows 293 and 310).
+    // what the ring waits for.  64 experts, one warp and two: 7168 -> 2048 with 16 rows
+    // (32 columns a tile) 94 and 86 us, 64 rows (96) 99 and 91, 134 rows (176) 105 and
+    // 102; 2048 -> 7168 with 112 rows (160) 98 and 97, 134 rows 102 and 100.  At 208
+    // columns there is nothing between them (150 rows 109 and 110, 110 and 113; 512
+    // rows 246 and 245, 267 and 267), and the block does without the warp.
     p.sfwarps = p.nt <= 176 ? 2 : 1;
     p.wide = F % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
     const size_t smem = 1024 + (size_t)stages * p.stage_bytes + (size_t)p.chunks * p.chunk_bytes + kOutBytes + tables;
@@ -877,12 +879,14 @@ cgl_status launch_matmul_mxfp4(const uint8_t *a, const uint8_t *sa, int64_t rows
     const int sms = device_sm_count();
     if (sms <= 0) return CGL_ECUDA;
     const int64_t ftiles = (F + 2 * kM - 1) / (2 * kM);
-    const int64_t most = ((rows + p.nt - 1) / p.nt + (rows < E ? rows : E)) * ftiles;   // tiles there can be
+    const int64_t most = ((rows + p.nt - 1) / p.nt + (rows < E ? rows : E)) * ftiles;   // no more tiles than this
     int64_t pairs = (num_sms > 0 && num_sms < sms ? num_sms : sms) / 2;
     if (pairs < 1) pairs = 1;
-    // Where the tiles leave three quarters or half of the pairs without work, four
-    // or two pairs share one, a part of K each (at least one chunk of scales), as
-    // long as their sums fit into the first pair's ring.
+    // Where `most` tiles would leave three quarters or half of the pairs without work,
+    // four or two pairs share one, a part of K each (whole chunks of scales), as long as
+    // their sums fit into the first pair's ring.  `most` is known without the offsets and
+    // may be twice the tiles there are: one row, 7168 -> 4096, has 16 tiles, counts as 32
+    // and runs as two pairs a tile (12 and 16 stages).
     p.split = 1;
     for (int split = 4; split > 1 && p.split == 1; split /= 2)
         if (most * split <= pairs && (K + kStageK * kChunk - 1) / (kStageK * kChunk) >= split &&

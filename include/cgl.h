@@ -440,7 +440,10 @@ typedef enum cgl_dtype { CGL_BF16 = 0, CGL_F16 = 1, CGL_F32 = 2 } cgl_dtype;
  * down, with an exponent-only scale like CGL_OPT_UE8M0_SCALES.
  *
  * cgl_quantize_mxfp4 -- per block: scale = 2^e for the smallest e >= -127 with
- * 6 * 2^e >= max |x| (no value saturates; an all-zero block has e = -127), codes
+ * 6 * 2^e >= max |x| (no value saturates; an all-zero block has e = -127).  The
+ * format is OCP's, this choice of the scale is not: the conversion given there takes
+ * e two below the exponent of max |x| and saturates what is then past 6, so a block
+ * whose max |x| has a mantissa above 1.5 gets a byte one larger here.  Codes
  * = x * 2^-e rounded to the nearest E2M1 value, ties to the even code (a zero or
  * a value that rounds to zero keeps its sign).  A block that holds an infinity
  * or a NaN gets scale byte 255 and codes 0: all 32 values read back as NaN.
@@ -535,8 +538,8 @@ size_t cgl_balance_loss_workspace_bytes(int64_t num_tokens, int num_topk, int nu
  * ids -1) take no part.  With c[s, e] the slots of s with id e, S sequences:
  *   loss = alpha / S * sum_s sum_e (E * c[s, e] / (k * T_s)) * (1 / T_s) * sum_t p[t, e]
  * (0 from a sequence with T_s = 0).  A token whose logits are all -inf has
- * p = 0; a NaN logit makes its token's p, the loss and its gradient row NaN, as
- * does +inf with the softmax.
+ * p = 0; finite logits may have any size; a NaN logit makes its token's p, the
+ * loss and its gradient row NaN, as does +inf with the softmax.
  * In (device): logits [num_tokens, E], a cgl_dtype; topk_idx int32 [num_tokens,
  *   num_topk] as for cgl_get_layout; grad_loss binary32 [1] (NULL: 1).
  * Out (device, written in full): loss binary32 [1]; counts int32 [S, E];
