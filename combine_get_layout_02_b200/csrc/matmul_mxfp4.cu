@@ -35,7 +35,7 @@
 // against 602; 128 rows 667 to 695 against 672, and 757 to 873 when run for
 // seconds, where the 1000 W cap takes the clock to 1.0 GHz.  Many rows: no single
 // unit.  512 rows an expert, 2048 -> 7168: 0.99 to 1.05 ms (1.15 to 1.25 in a long
-// run) against 615 us; the tensor pipe is active half of the time, the SMs take 43
+// run) against 615 us; the tensor pipe is active half of the time, the SMs take 45
 // bytes a cycle from L2 of the 64 they could, DRAM is at 45%.  In long runs the
 // MMAs without loads took 0.82 ms, with all weights in L2 1.05, and more columns a
 // tile, which take fewer bytes, less (160, 192, 208: 1.35, 1.23, 1.16 ms); two
