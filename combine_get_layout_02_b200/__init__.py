@@ -23,6 +23,12 @@ power-of-two scale per 32), and for training the loss that keeps the routing eve
     recv_x, recv_scale = dispatch_mxfp4(x, lay.dst_pos, lay.num_recv_rows)
     y = matmul_mxfp4(recv_x, recv_scale, wq, ws, lay.expert_offset, lay.capacity)
     aux = balance_loss(logits, topk_idx, alpha=1e-3, grad_loss=g)   # .loss, .counts, .grad_logits
+
+In front of the layout the gate, and between dispatch and combine the same product on BF16 rows, with
+bias, activation and residual; both have a backward pass:
+
+    r = route(logits, 8, score="sigmoid", bias=b, num_groups=8, topk_groups=4)      # .topk_idx, .topk_weights
+    h = matmul_bf16(recv_x, w1, lay.expert_offset, activation="swiglu")
 """
 
 from __future__ import annotations
@@ -38,6 +44,8 @@ __all__ = [
     "combine_backward", "decode_dispatch_fp8", "layout_workspace_bytes", "layout_kernel_count", "status_bits", "check_status", "new_status",
     "quantize_mxfp4", "dequantize_mxfp4", "dispatch_mxfp4", "matmul_mxfp4", "BalanceLoss", "balance_loss",
     "balance_loss_backward", "balance_loss_workspace_bytes",
+    "Routing", "route", "route_backward", "matmul_bf16", "MatmulGrads", "matmul_bf16_backward",
+    "matmul_bf16_backward_workspace_bytes",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -120,6 +128,17 @@ def lib():
         L.cgl_balance_loss.restype = I
         L.cgl_balance_loss_backward.argtypes = [P, P, I, P, I64, I, I, I64, C.c_float, I, P, P, P, P]
         L.cgl_balance_loss_backward.restype = I
+        F = C.c_float
+        L.cgl_route.argtypes = [P, I, I64, I, I, P, I, I, I, I, I, F, P, P, P, P]
+        L.cgl_route.restype = I
+        L.cgl_route_backward.argtypes = [P, P, I, P, I64, I, I, I, I, F, P, P, P]
+        L.cgl_route_backward.restype = I
+        L.cgl_matmul_bf16.argtypes = [P, I64, P, I, I, I, P, P, I, P, P, P, OP, P, P]
+        L.cgl_matmul_bf16.restype = I
+        L.cgl_matmul_bf16_backward_workspace_bytes.argtypes = [I64, I, I, I]
+        L.cgl_matmul_bf16_backward_workspace_bytes.restype = C.c_size_t
+        L.cgl_matmul_bf16_backward.argtypes = [P, P, I64, P, I, I, I, P, I, P, P, P, P, P, C.c_size_t, OP, P, P]
+        L.cgl_matmul_bf16_backward.restype = I
         _lib = L
     return _lib
 
@@ -713,3 +732,182 @@ def balance_loss_backward(grad_loss: torch.Tensor, logits: torch.Tensor, topk_id
             dt, _ptr(idx), n, k, E, num_sequences, float(alpha), _SCORES[score], _ptr(counts), _ptr(num_routed),
             _ptr(grad_logits))
     return grad_logits
+
+
+# ---- routing, the experts' BF16 product --------------------------------------------------------
+
+_GROUP_SCORES = {"max": 0, "top2": 1}                                              # cgl_group_score
+_ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}           # cgl_activation
+
+
+def _choice(value, names, what: str) -> int:
+    if value not in names:
+        raise ValueError(f"{what} must be one of {sorted(names)}, got {value!r}")
+    return names[value]
+
+
+class Routing(NamedTuple):
+    topk_idx: torch.Tensor       # int32 [N, k], best first; -1: no expert left
+    topk_weights: torch.Tensor   # fp32 [N, k]
+
+
+def route(logits: torch.Tensor, num_topk: int, *, bias: Optional[torch.Tensor] = None, num_groups: int = 1,
+          topk_groups: int = 1, group_score: str = "max", score: str = "softmax", renormalize: bool = True,
+          scale: float = 1.0, topk_idx: Optional[torch.Tensor] = None, topk_weights: Optional[torch.Tensor] = None,
+          status: Optional[torch.Tensor] = None, stream=None) -> Routing:
+    """Top-k experts of every token and their weights, for get_layout and combine (cgl_route).
+
+    logits [N, E] (bfloat16, float16 or float32; -inf: the token may not take that expert).  score: "softmax" or
+    "sigmoid".  bias: fp32 [E], added to the scores for the choice alone.  The best topk_groups of num_groups groups
+    stay, by their best choice (group_score "max") or the sum of their two best ("top2").  renormalize: the picked
+    scores are divided by their sum; scale multiplies the weights."""
+    if stream is not None:
+        with _on(stream, logits, "logits"):
+            return route(logits, num_topk, bias=bias, num_groups=num_groups, topk_groups=topk_groups, group_score=group_score,
+                         score=score, renormalize=renormalize, scale=scale, topk_idx=topk_idx, topk_weights=topk_weights,
+                         status=status)
+    logits = _dev(logits, "logits", None, 2)
+    dt = _float_type(logits, "logits")
+    n, E = logits.shape
+    if bias is not None:
+        _buf(_dev(bias, "bias", torch.float32), "bias", (E,), torch.float32, logits)
+    _same(logits.device, status=status)
+    how = _choice(score, _SCORES, "score"), _choice(group_score, _GROUP_SCORES, "group_score")
+    if not 1 <= num_topk <= min(E, 32):
+        raise CglError(EINVAL, "route", "num_topk must be in [1, min(E, 32)]")
+    topk_idx = _buf(topk_idx, "topk_idx", (n, num_topk), torch.int32, logits)
+    topk_weights = _buf(topk_weights, "topk_weights", (n, num_topk), torch.float32, logits)
+    _launch("cgl_route", lib().cgl_route, logits.device, _ptr(logits), dt, n, E, num_topk, _ptr(bias), num_groups, topk_groups,
+            how[1], how[0], bool(renormalize), float(scale), _ptr(topk_idx), _ptr(topk_weights), _ptr(status))
+    return Routing(topk_idx, topk_weights)
+
+
+def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor, *, score: str = "softmax",
+                   renormalize: bool = True, scale: float = 1.0, grad_logits: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of route's weights for the logits, from grad_weights fp32 [N, k] and route's topk_idx (cgl_route_backward)."""
+    if stream is not None:
+        with _on(stream, logits, "logits"):
+            return route_backward(grad_weights, logits, topk_idx, score=score, renormalize=renormalize, scale=scale,
+                                  grad_logits=grad_logits, status=status)
+    logits = _dev(logits, "logits", None, 2)
+    idx = _dev(topk_idx, "topk_idx", torch.int32, 2)
+    g = _dev(grad_weights, "grad_weights", torch.float32, 2)
+    dt = _float_type(logits, "logits")
+    n, E = logits.shape
+    if idx.shape[0] != n or g.shape != idx.shape:
+        raise ValueError(f"topk_idx and grad_weights [{n}, k] expected, got {tuple(idx.shape)}, {tuple(g.shape)}")
+    _same(logits.device, topk_idx=idx, grad_weights=g, status=status)
+    kind = _choice(score, _SCORES, "score")
+    grad_logits = _buf(grad_logits, "grad_logits", (n, E), logits.dtype, logits)
+    _launch("cgl_route_backward", lib().cgl_route_backward, logits.device, _ptr(g), _ptr(logits), dt, _ptr(idx), n, E,
+            idx.shape[1], kind, bool(renormalize), float(scale), _ptr(grad_logits), _ptr(status))
+    return grad_logits
+
+
+def matmul_bf16_backward_workspace_bytes(num_rows: int, num_experts: int, out_features: int, in_features: int) -> int:
+    return int(lib().cgl_matmul_bf16_backward_workspace_bytes(num_rows, num_experts, out_features, in_features))
+
+
+def _matmul_args(a, w, expert_offset, activation, status):
+    """Checked a [rows, in], w [E, out, in] and offsets; returns them with the sizes and the output's columns."""
+    a = _dev(a, "a", torch.bfloat16, 2)
+    w = _dev(w, "w", torch.bfloat16)
+    if expert_offset is None and w.dim() == 2:
+        w = w.unsqueeze(0)
+    if w.dim() != 3:
+        raise ValueError(f"w must have 3 dims, got {w.dim()}")
+    (rows, K), (E, out, wk) = a.shape, w.shape
+    act = _choice(activation, _ACTIVATIONS, "activation")
+    if wk != K or K == 0 or K % 8:
+        raise ValueError(f"a [rows, in] and w [E, out, in] with in % 8 == 0 expected, got {tuple(a.shape)}, {tuple(w.shape)}")
+    if act == 4 and out % 2:
+        raise ValueError(f"swiglu needs an even number of rows in w, got {out}")
+    if expert_offset is not None:
+        _dev(expert_offset, "expert_offset", torch.int32, 1)
+        if expert_offset.shape[0] != E + 1:
+            raise ValueError(f"expert_offset must have {E + 1} entries, got {expert_offset.shape[0]}")
+    _same(a.device, w=w, expert_offset=expert_offset, status=status)
+    return a, w, act, rows, E, out, K, out // 2 if act == 4 else out
+
+
+def _given(t, name: str, shape, dtype, like):
+    return None if t is None else _buf(_dev(t, name, dtype), name, shape, dtype, like)
+
+
+def matmul_bf16(a: torch.Tensor, w: torch.Tensor, expert_offset: Optional[torch.Tensor] = None, capacity: int = 0, *,
+                bias: Optional[torch.Tensor] = None, activation: str = "none", residual: Optional[torch.Tensor] = None,
+                with_preact: bool = False, y: Optional[torch.Tensor] = None, preact: Optional[torch.Tensor] = None,
+                status: Optional[torch.Tensor] = None, num_sms: int = 0, stream=None):
+    """The experts' product on BF16 rows, y[r] = act(a[r] @ w[expert of r].T + bias) + residual[r] (cgl_matmul_bf16).
+
+    a [rows, in] (dispatch_bf16's rows), w [E, out, in], bias [E, out], residual and y [rows, out], all bfloat16.
+    expert_offset int32 [E + 1] and capacity as get_layout gives them; without expert_offset w has one expert (or is
+    [out, in], bias then [out]) and takes every row.  activation: "none", "relu", "gelu", "silu", or "swiglu": the
+    first half of w's rows is the gate, the second the up projection, and y and residual have out / 2 columns.
+    Rows of no expert are left as they were.  with_preact (or a preact buffer [rows, out]): returns (y, preact),
+    the sums with bias that matmul_bf16_backward takes; otherwise y alone."""
+    if stream is not None:
+        with _on(stream, a, "a"):
+            return matmul_bf16(a, w, expert_offset, capacity, bias=bias, activation=activation, residual=residual,
+                               with_preact=with_preact, y=y, preact=preact, status=status, num_sms=num_sms)
+    flat = isinstance(w, torch.Tensor) and w.dim() == 2
+    a, w, act, rows, E, out, K, cols = _matmul_args(a, w, expert_offset, activation, status)
+    if bias is not None:
+        _given(bias, "bias", (out,) if flat else (E, out), torch.bfloat16, a)
+    _given(residual, "residual", (rows, cols), torch.bfloat16, a)
+    y = _buf(y, "y", (rows, cols), torch.bfloat16, a)
+    keep = with_preact or preact is not None
+    if keep:
+        preact = _buf(preact, "preact", (rows, out), torch.bfloat16, a)
+    _launch("cgl_matmul_bf16", lib().cgl_matmul_bf16, a.device, _ptr(a), rows, _ptr(w), E, out, K, _ptr(expert_offset), _ptr(bias),
+            act, _ptr(residual), _ptr(y), _ptr(preact), _opts(num_sms, capacity), _ptr(status))
+    return (y, preact) if keep else y
+
+
+class MatmulGrads(NamedTuple):
+    grad_a: Optional[torch.Tensor]      # bf16 [rows, in]
+    grad_w: Optional[torch.Tensor]      # bf16 [E, out, in]
+    grad_bias: Optional[torch.Tensor]   # bf16 [E, out]
+
+
+def matmul_bf16_backward(grad_y: torch.Tensor, a: torch.Tensor, w: torch.Tensor, expert_offset: Optional[torch.Tensor] = None,
+                         capacity: int = 0, *, activation: str = "none", preact: Optional[torch.Tensor] = None,
+                         want_a: bool = True, want_w: bool = True, want_bias: bool = False,
+                         grad_a: Optional[torch.Tensor] = None, grad_w: Optional[torch.Tensor] = None,
+                         grad_bias: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None, num_sms: int = 0, stream=None) -> MatmulGrads:
+    """Gradients of matmul_bf16 for its rows, weights and bias (cgl_matmul_bf16_backward); the residual's is grad_y itself.
+
+    preact: what matmul_bf16(..., with_preact=True) gave (not needed without an activation).  Rows of grad_a of no
+    expert are left as they were (uninitialised when allocated here); grad_w and grad_bias of an expert without rows are 0."""
+    if stream is not None:
+        with _on(stream, a, "a"):
+            return matmul_bf16_backward(grad_y, a, w, expert_offset, capacity, activation=activation, preact=preact, want_a=want_a,
+                                        want_w=want_w, want_bias=want_bias, grad_a=grad_a, grad_w=grad_w, grad_bias=grad_bias,
+                                        workspace=workspace, status=status, num_sms=num_sms)
+    flat = isinstance(w, torch.Tensor) and w.dim() == 2
+    a, w, act, rows, E, out, K, cols = _matmul_args(a, w, expert_offset, activation, status)
+    bf16, lead = torch.bfloat16, () if flat else (E,)
+    _given(_dev(grad_y, "grad_y"), "grad_y", (rows, cols), bf16, a)
+    if act != 0 and preact is None:
+        raise ValueError(f"activation {activation!r} needs preact")
+    _given(preact, "preact", (rows, out), bf16, a)
+    ws_bytes = matmul_bf16_backward_workspace_bytes(rows, E, out, K)
+    if ws_bytes == 0:
+        raise CglError(EINVAL, "matmul_bf16_backward", "invalid sizes")
+    for name, t, want in (("grad_a", grad_a, want_a), ("grad_w", grad_w, want_w), ("grad_bias", grad_bias, want_bias)):
+        if t is not None and not want:
+            raise ValueError(f"{name} was given but is not wanted")
+    grad_a = _buf(grad_a, "grad_a", (rows, K), bf16, a) if want_a else None
+    grad_w = _buf(grad_w, "grad_w", (*lead, out, K), bf16, a) if want_w else None
+    grad_bias = _buf(grad_bias, "grad_bias", (*lead, out), bf16, a) if want_bias else None
+    if workspace is None:
+        workspace = a.new_empty(ws_bytes, dtype=torch.uint8)
+    else:
+        _same(a.device, workspace=_dev(workspace, "workspace"))
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _launch("cgl_matmul_bf16_backward", lib().cgl_matmul_bf16_backward, a.device, _ptr(grad_y), _ptr(a), rows, _ptr(w), E, out, K,
+            _ptr(expert_offset), act, _ptr(preact), _ptr(grad_a), _ptr(grad_w), _ptr(grad_bias), _ptr(workspace), ws_bytes,
+            _opts(num_sms, capacity), _ptr(status))
+    return MatmulGrads(grad_a, grad_w, grad_bias)

@@ -131,7 +131,7 @@ using namespace cgl;
 
 extern "C" {
 
-int cgl_version(void) { return 400; }
+int cgl_version(void) { return 500; }
 
 const char *cgl_status_string(int s) {
     switch (s) {
@@ -448,6 +448,90 @@ cgl_status cgl_balance_loss_backward(const float *grad_loss, const void *logits,
         return CGL_EALIGN;
     return launch_balance_loss_backward(grad_loss, logits, dtype, topk_idx, n, k, E, S, alpha, score, counts,
                                         num_routed, grad_logits, static_cast<cudaStream_t>(stream));
+}
+
+static bool route_sizes_ok(int64_t n, int E, int k) {
+    return n >= 0 && E >= 1 && E <= kMaxExperts && k >= 1 && k <= kMaxTopk && k <= E && n * (int64_t)k < ((int64_t)1 << 31);
+}
+
+cgl_status cgl_route(const void *logits, int dtype, int64_t n, int E, int k, const float *bias, int groups, int keep,
+                     int by, int score, int renorm, float scale, int32_t *topk_idx, float *topk_weights,
+                     uint32_t *status_dev, void *stream) {
+    if (!route_sizes_ok(n, E, k) || !dtype_ok(dtype)) return CGL_EINVAL;
+    if (groups < 1 || groups > 32 || E % groups != 0 || keep < 1 || keep > groups) return CGL_EINVAL;
+    if (by != CGL_GROUP_MAX && by != CGL_GROUP_TOP2) return CGL_EINVAL;
+    if (score != CGL_SCORE_SOFTMAX && score != CGL_SCORE_SIGMOID) return CGL_EINVAL;
+    if (n > 0 && (!logits || !topk_idx || !topk_weights)) return CGL_EINVAL;
+    if (!aligned(logits, dtype == CGL_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
+        !aligned(topk_weights, 4) || !aligned(status_dev, 4))
+        return CGL_EALIGN;
+    const RouteArgs a = {logits, dtype, n, E, k, bias, groups, keep, by, score, renorm != 0, scale, topk_idx, topk_weights,
+                         status_dev};
+    return launch_route(a, static_cast<cudaStream_t>(stream));
+}
+
+cgl_status cgl_route_backward(const float *grad_weights, const void *logits, int dtype, const int32_t *topk_idx,
+                              int64_t n, int E, int k, int score, int renorm, float scale, void *grad_logits,
+                              uint32_t *status_dev, void *stream) {
+    if (n < 0 || E < 1 || E > kMaxExperts || k < 1 || k > kMaxTopk || n * (int64_t)k >= ((int64_t)1 << 31) || !dtype_ok(dtype))
+        return CGL_EINVAL;
+    if (score != CGL_SCORE_SOFTMAX && score != CGL_SCORE_SIGMOID) return CGL_EINVAL;
+    if (n > 0 && (!grad_weights || !logits || !topk_idx || !grad_logits)) return CGL_EINVAL;
+    const size_t item = dtype == CGL_F32 ? 4 : 2;
+    if (!aligned(logits, item) || !aligned(grad_logits, item) || !aligned(topk_idx, 4) || !aligned(grad_weights, 4) ||
+        !aligned(status_dev, 4))
+        return CGL_EALIGN;
+    return launch_route_backward(grad_weights, logits, dtype, topk_idx, n, E, k, score, renorm != 0, scale, grad_logits,
+                                 status_dev, static_cast<cudaStream_t>(stream));
+}
+
+static bool bf16_product_sizes_ok(int64_t rows, int E, int F, int K) {
+    return E >= 1 && E <= kMaxExperts && F >= 1 && F <= (1 << 20) && K >= 8 && K % 8 == 0 && K <= (1 << 20) && rows >= 0 &&
+           rows <= ((int64_t)1 << 31) - 4096;
+}
+
+static cgl_status bf16_product_ok(const uint16_t *a, int64_t rows, const uint16_t *w, int E, int F, int K,
+                                  const int32_t *expert_offset, int act, const cgl_opts *opts, uint32_t *status_dev) {
+    if (!bf16_product_sizes_ok(rows, E, F, K) || act < CGL_ACT_NONE || act > CGL_ACT_SWIGLU) return CGL_EINVAL;
+    if (act == CGL_ACT_SWIGLU && F % 2 != 0) return CGL_EINVAL;
+    const int cap = opt_cap(opts);
+    if (cap < 0 || opt_sms(opts) < 0 || !flags_ok(opts)) return CGL_EINVAL;
+    if (!expert_offset && (E != 1 || cap != 0)) return CGL_EINVAL;
+    if (cap > 0 && rows < (int64_t)E * cap) return CGL_EINVAL;
+    if (!w || (rows > 0 && !a)) return CGL_EINVAL;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(expert_offset, 4) || !aligned(status_dev, 4)) return CGL_EALIGN;
+    return CGL_OK;
+}
+
+cgl_status cgl_matmul_bf16(const uint16_t *a, int64_t rows, const uint16_t *w, int E, int F, int K,
+                           const int32_t *expert_offset, const uint16_t *bias, int act, const uint16_t *residual,
+                           uint16_t *y, uint16_t *preact, const cgl_opts *opts, uint32_t *status_dev, void *stream) {
+    const cgl_status ok = bf16_product_ok(a, rows, w, E, F, K, expert_offset, act, opts, status_dev);
+    if (ok != CGL_OK) return ok;
+    if (rows > 0 && !y) return CGL_EINVAL;
+    if (!aligned(bias, 2) || !aligned(residual, 2) || !aligned(y, 2) || !aligned(preact, 2)) return CGL_EALIGN;
+    const MatmulArgs m = {a, rows, w, E, F, K, expert_offset, opt_cap(opts), act, opt_sms(opts), status_dev};
+    return launch_matmul_bf16(m, bias, residual, y, preact, static_cast<cudaStream_t>(stream));
+}
+
+size_t cgl_matmul_bf16_backward_workspace_bytes(int64_t rows, int E, int F, int K) {
+    return bf16_product_sizes_ok(rows, E, F, K) ? matmul_bf16_backward_workspace_bytes(rows, E, F) : 0;
+}
+
+cgl_status cgl_matmul_bf16_backward(const uint16_t *grad_y, const uint16_t *a, int64_t rows, const uint16_t *w, int E,
+                                    int F, int K, const int32_t *expert_offset, int act, const uint16_t *preact,
+                                    uint16_t *grad_a, uint16_t *grad_w, uint16_t *grad_bias, void *workspace,
+                                    size_t workspace_bytes, const cgl_opts *opts, uint32_t *status_dev, void *stream) {
+    const cgl_status ok = bf16_product_ok(a, rows, w, E, F, K, expert_offset, act, opts, status_dev);
+    if (ok != CGL_OK) return ok;
+    if (rows > 0 && (!grad_y || (act != CGL_ACT_NONE && !preact))) return CGL_EINVAL;
+    if (!workspace || workspace_bytes < matmul_bf16_backward_workspace_bytes(rows, E, F)) return CGL_EINVAL;
+    if (!aligned(grad_y, 2) || !aligned(preact, 2) || !aligned(grad_a, 16) || !aligned(grad_w, 16) || !aligned(grad_bias, 2) ||
+        !aligned(workspace, 16))
+        return CGL_EALIGN;
+    const MatmulArgs m = {a, rows, w, E, F, K, expert_offset, opt_cap(opts), act, opt_sms(opts), status_dev};
+    return launch_matmul_bf16_backward(m, grad_y, preact, grad_a, grad_w, grad_bias, workspace,
+                                       static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

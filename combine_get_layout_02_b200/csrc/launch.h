@@ -137,4 +137,41 @@ cgl_status launch_balance_loss_backward(const float *grad_loss, const void *logi
                                         int64_t n, int k, int E, int64_t S, float alpha, int score,
                                         const int32_t *counts, const int32_t *routed, void *grad, cudaStream_t stream);
 
+// Routing (groups: experts in neighbouring equal groups, the best `keep` stay).
+struct RouteArgs {
+    const void *logits;
+    int dtype;
+    int64_t n;
+    int E, k;
+    const float *bias;
+    int groups, keep, by, score;
+    bool renorm;
+    float scale;
+    int32_t *idx;
+    float *weights;
+    uint32_t *status;
+};
+cgl_status launch_route(const RouteArgs &a, cudaStream_t stream);
+cgl_status launch_route_backward(const float *grad_weights, const void *logits, int dtype, const int32_t *idx, int64_t n,
+                                 int E, int k, int score, bool renorm, float scale, void *grad, uint32_t *status,
+                                 cudaStream_t stream);
+
+// The experts' BF16 product and its gradients (off null: one expert, all rows).
+struct MatmulArgs {
+    const uint16_t *a;
+    int64_t rows;
+    const uint16_t *w;
+    int E, F, K;   // F: rows of w (both halves of a gated one)
+    const int32_t *off;
+    int64_t cap;
+    int act;
+    int num_sms;
+    uint32_t *status;
+};
+cgl_status launch_matmul_bf16(const MatmulArgs &m, const uint16_t *bias, const uint16_t *residual, uint16_t *y,
+                              uint16_t *preact, cudaStream_t stream);
+size_t matmul_bf16_backward_workspace_bytes(int64_t rows, int E, int F);
+cgl_status launch_matmul_bf16_backward(const MatmulArgs &m, const uint16_t *grad_y, const uint16_t *preact, uint16_t *grad_a,
+                                       uint16_t *grad_w, uint16_t *grad_bias, void *ws, cudaStream_t stream);
+
 }  // namespace cgl

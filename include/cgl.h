@@ -112,7 +112,8 @@ typedef struct cgl_opts {
 
 /* Library version (major * 10000 + minor * 100 + patch).  0.2.0 added
  * cgl_opts.flags and 0.3.0 cgl_opts.scratch: C callers built against an older
- * cgl.h must be rebuilt.  0.4.0 added the MXFP4 calls and the balance loss. */
+ * cgl.h must be rebuilt.  0.4.0 added the MXFP4 calls and the balance loss,
+ * 0.5.0 the routing and the experts' BF16 product. */
 int cgl_version(void);
 
 /* A static string naming a cgl_status value (or "unknown status"). */
@@ -568,6 +569,125 @@ cgl_status cgl_balance_loss_backward(const float *grad_loss, const void *logits,
                                      int num_experts, int64_t num_sequences, float alpha, int score,
                                      const int32_t *counts, const int32_t *num_routed, void *grad_logits,
                                      void *stream);
+
+/* What a group of experts is worth when the router keeps the best groups. */
+typedef enum cgl_group_score {
+    CGL_GROUP_MAX = 0,    /* its largest choice */
+    CGL_GROUP_TOP2 = 1    /* the sum of its two largest (of one, where only one can be picked) */
+} cgl_group_score;
+
+/*
+ * cgl_route -- the gate in front of the layout: top-k experts of every token and
+ * the weights that combine uses.  Pages: "top-4 groups, top-8 experts" in the
+ * normal kernels' settings (news article "具体性能方面"; brainleap "DeepEP 的性能
+ * 表现"; flashmla.org/de); they give no formula, this is the common one.
+ * For token t with logits l, an expert with l = -inf cannot be picked:
+ *   s = softmax(l) or sigmoid(l) (cgl_score; here the sigmoid is not normalised);
+ *   choice = s + bias[e], or without a bias the logits themselves (the same order);
+ *   the topk_groups best of num_groups groups of neighbouring experts stay (group_score;
+ *   CGL_GROUP_TOP2 sums s + bias, or s), then the num_topk best choices among them are
+ *   picked, best first.  Equal values go to the lower index.
+ *   weight_j = scale * s_j, or with renormalize scale * s_j / sum of the picked s
+ *   (the quotient of the true values, also where all picked s underflow).
+ * The order is that of the values in binary64: where two choices are nearer than
+ * binary32 resolves, they are computed again in binary64.
+ * Slots that no expert is left for (fewer than num_topk can be picked) get id -1,
+ * which cgl_get_layout takes as no copy, and weight 0.  A token with a NaN among
+ * its logits or choices, or +inf with the softmax, gets ids -1 and weights NaN.
+ * In (device): logits [num_tokens, E], a cgl_dtype; bias binary32 [E] (NULL: none;
+ *   it only steers the choice and has no gradient).
+ * Out (device, written in full): topk_idx int32 [num_tokens, num_topk];
+ *   topk_weights binary32 [num_tokens, num_topk].
+ * Limits: num_topk <= min(E, 32), num_groups <= 32 and E % num_groups == 0,
+ * topk_groups in [1, num_groups], num_tokens * num_topk < 2^31.
+ * 16-byte aligned rows (E % 8 == 0) are read faster.
+ * Device errors: CGL_ERANGE for tokens with NaN as above.
+ */
+cgl_status cgl_route(const void *logits, int dtype, int64_t num_tokens, int num_experts, int num_topk,
+                     const float *bias, int num_groups, int topk_groups, int group_score, int score,
+                     int renormalize, float scale, int32_t *topk_idx, float *topk_weights,
+                     uint32_t *status_dev, void *stream);
+
+/*
+ * cgl_route_backward -- the gradient of cgl_route's weights for the logits; the
+ * choice has none.  With c = scale, s and w as above, D the sum of the picked s:
+ *   sigmoid:                c s_j (1 - s_j) g_j, renormalised w_j (1 - s_j) (g_j - sum_i g_i w_i / c)
+ *   softmax, renormalised:  w_j (g_j - sum_i g_i w_i / c)
+ *   softmax:                c s_e ([e picked] g_e - sum_i g_i s_i), for every expert e
+ * and 0 elsewhere; tokens with no slot in [0, E) get 0.  An expert in two slots
+ * of a token gets both terms.
+ * In (device): grad_weights binary32 [num_tokens, num_topk]; logits as for
+ *   cgl_route; topk_idx int32 [num_tokens, num_topk] (cgl_route's).
+ * Out (device, written in full): grad_logits [num_tokens, E] in the logits' type;
+ *   it must not overlap the logits.
+ * Device errors: CGL_ERANGE for ids < -1 or >= E (they take no part).
+ */
+cgl_status cgl_route_backward(const float *grad_weights, const void *logits, int dtype, const int32_t *topk_idx,
+                              int64_t num_tokens, int num_experts, int num_topk, int score, int renormalize,
+                              float scale, void *grad_logits, uint32_t *status_dev, void *stream);
+
+/* What cgl_matmul_bf16 does to a sum z before the residual. */
+typedef enum cgl_activation {
+    CGL_ACT_NONE = 0,
+    CGL_ACT_RELU = 1,     /* max(z, 0) */
+    CGL_ACT_GELU = 2,     /* z Phi(z), Phi the normal distribution function */
+    CGL_ACT_SILU = 3,     /* z sigmoid(z) */
+    CGL_ACT_SWIGLU = 4    /* z[f] sigmoid(z[f]) z[out / 2 + f], f < out / 2: gate rows first, then up rows */
+} cgl_activation;
+
+/*
+ * cgl_matmul_bf16 -- the experts' product on BF16 rows (what cgl_dispatch_bf16
+ * sends), between dispatch and combine, with its epilogue:
+ *   z[r, f] = sum_k a[r, k] w[e, f, k] + bias[e, f]     for every row r of expert e
+ *   y[r, :] = bf16_rn( act(z[r, :]) + residual[r, :] )
+ * the sum and all of the epilogue in binary32 (the order of the sum's terms is
+ * this library's; the same for the same sizes and options on the same kind of
+ * GPU).  y and residual have F = out columns, out / 2 with CGL_ACT_SWIGLU.
+ * Rows of the experts: expert_offset, opts.capacity, NULL as for cgl_matmul_mxfp4.
+ * In (device): a BF16 [num_rows, in] (rows of no expert may hold anything);
+ *   w BF16 [E, out, in]; bias BF16 [E, out] or NULL; residual BF16 [num_rows, F] or
+ *   NULL (it may be y itself); expert_offset int32 [E + 1].
+ * Out (device): y BF16 [num_rows, F]; preact BF16 [num_rows, out], z rounded, which
+ *   cgl_matmul_bf16_backward wants, or NULL.  Rows of no expert are NOT written.
+ * Requires in % 8 == 0; out even with CGL_ACT_SWIGLU; in, out <= 2^20; num_rows <=
+ * 2^31 - 4096, and >= E * capacity when padded; a and w 16-byte aligned, the others
+ * 2-byte (16-byte aligned rows are faster).  opts: capacity, num_sms (blocks work
+ * in pairs: at least two SMs).
+ * Device errors: CGL_ERANGE when offsets run backwards or past num_rows (nothing
+ * is computed then); CGL_ETIMEOUT if a bounded wait (about a second) inside a
+ * block pair gives up, the outputs then undefined.
+ */
+cgl_status cgl_matmul_bf16(const uint16_t *a, int64_t num_rows, const uint16_t *w, int num_experts, int out_features,
+                           int in_features, const int32_t *expert_offset, const uint16_t *bias, int activation,
+                           const uint16_t *residual, uint16_t *y, uint16_t *preact, const cgl_opts *opts,
+                           uint32_t *status_dev, void *stream);
+
+/* Bytes of device workspace cgl_matmul_bf16_backward needs; host-only, 0 for invalid sizes. */
+size_t cgl_matmul_bf16_backward_workspace_bytes(int64_t num_rows, int num_experts, int out_features, int in_features);
+
+/*
+ * cgl_matmul_bf16_backward -- the gradients of cgl_matmul_bf16.  With g = dL/dy and
+ * dz = g act'(z) (z as preact holds it; dz is rounded to BF16 for the two products):
+ *   grad_a[r, :]    = bf16_rn( sum_f dz[r, f] w[e, f, :] )           for every row r of expert e
+ *   grad_w[e, f, :] = bf16_rn( sum_r dz[r, f] a[r, :] )              over the rows of expert e
+ *   grad_bias[e, f] = bf16_rn( sum_r dz[r, f] )                      (dz in binary32, fixed order)
+ * The residual's gradient is g itself.  Each output may be NULL: it is not computed.
+ * In (device): grad_y BF16 [num_rows, F]; a, w, expert_offset as for the forward;
+ *   preact BF16 [num_rows, out] (NULL with CGL_ACT_NONE, which needs none).
+ * Out (device): grad_a BF16 [num_rows, in], rows of no expert NOT written; grad_w
+ *   BF16 [E, out, in] and grad_bias BF16 [E, out], written in full (0 for experts
+ *   without rows).
+ * workspace: device, 16-byte aligned, any contents, scratch for the call (calls
+ *   that overlap on the GPU must not share one).
+ * Sizes, alignment, opts and errors as for cgl_matmul_bf16 (grad_a and grad_w
+ * 16-byte aligned).
+ */
+cgl_status cgl_matmul_bf16_backward(const uint16_t *grad_y, const uint16_t *a, int64_t num_rows, const uint16_t *w,
+                                    int num_experts, int out_features, int in_features,
+                                    const int32_t *expert_offset, int activation, const uint16_t *preact,
+                                    uint16_t *grad_a, uint16_t *grad_w, uint16_t *grad_bias, void *workspace,
+                                    size_t workspace_bytes, const cgl_opts *opts, uint32_t *status_dev,
+                                    void *stream);
 
 #ifdef __cplusplus
 }
