@@ -133,11 +133,11 @@ def lib():
         L.cgl_route.restype = I
         L.cgl_route_backward.argtypes = [P, P, I, P, I64, I, I, I, I, F, P, P, P]
         L.cgl_route_backward.restype = I
-        L.cgl_matmul_bf16.argtypes = [P, I64, P, I, I, I, P, P, I, P, P, P, OP, P, P]
+        L.cgl_matmul_bf16.argtypes = [P, I64, P, I, I, I, P, P, I, P, P, P, I, OP, P, P]
         L.cgl_matmul_bf16.restype = I
         L.cgl_matmul_bf16_backward_workspace_bytes.argtypes = [I64, I, I, I]
         L.cgl_matmul_bf16_backward_workspace_bytes.restype = C.c_size_t
-        L.cgl_matmul_bf16_backward.argtypes = [P, P, I64, P, I, I, I, P, I, P, P, P, P, P, C.c_size_t, OP, P, P]
+        L.cgl_matmul_bf16_backward.argtypes = [P, P, I64, P, I, I, I, P, I, P, I, P, P, P, P, C.c_size_t, OP, P, P]
         L.cgl_matmul_bf16_backward.restype = I
         _lib = L
     return _lib
@@ -831,6 +831,14 @@ def _matmul_args(a, w, expert_offset, activation, status):
     return a, w, act, rows, E, out, K, out // 2 if act == 4 else out
 
 
+def _preact(t, shape, like):
+    """A preact buffer, binary32 or BF16, and its cgl_dtype."""
+    dtype = t.dtype if isinstance(t, torch.Tensor) else torch.float32
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"preact must be float32 or bfloat16, got {dtype}")
+    return _buf(t, "preact", shape, dtype, like), _DTYPES[dtype]
+
+
 def _given(t, name: str, shape, dtype, like):
     return None if t is None else _buf(_dev(t, name, dtype), name, shape, dtype, like)
 
@@ -845,8 +853,9 @@ def matmul_bf16(a: torch.Tensor, w: torch.Tensor, expert_offset: Optional[torch.
     expert_offset int32 [E + 1] and capacity as get_layout gives them; without expert_offset w has one expert (or is
     [out, in], bias then [out]) and takes every row.  activation: "none", "relu", "gelu", "silu", or "swiglu": the
     first half of w's rows is the gate, the second the up projection, and y and residual have out / 2 columns.
-    Rows of no expert are left as they were.  with_preact (or a preact buffer [rows, out]): returns (y, preact),
-    the sums with bias that matmul_bf16_backward takes; otherwise y alone."""
+    Rows of no expert are left as they were.  with_preact: returns (y, preact), the sums with bias in fp32
+    [rows, out], which matmul_bf16_backward takes; otherwise y alone.  preact: a buffer for them, fp32, or bfloat16,
+    which halves its bytes and costs the gradients a rounding."""
     if stream is not None:
         with _on(stream, a, "a"):
             return matmul_bf16(a, w, expert_offset, capacity, bias=bias, activation=activation, residual=residual,
@@ -858,10 +867,9 @@ def matmul_bf16(a: torch.Tensor, w: torch.Tensor, expert_offset: Optional[torch.
     _given(residual, "residual", (rows, cols), torch.bfloat16, a)
     y = _buf(y, "y", (rows, cols), torch.bfloat16, a)
     keep = with_preact or preact is not None
-    if keep:
-        preact = _buf(preact, "preact", (rows, out), torch.bfloat16, a)
+    preact, kind = _preact(preact, (rows, out), a) if keep else (None, 0)
     _launch("cgl_matmul_bf16", lib().cgl_matmul_bf16, a.device, _ptr(a), rows, _ptr(w), E, out, K, _ptr(expert_offset), _ptr(bias),
-            act, _ptr(residual), _ptr(y), _ptr(preact), _opts(num_sms, capacity), _ptr(status))
+            act, _ptr(residual), _ptr(y), _ptr(preact), kind, _opts(num_sms, capacity), _ptr(status))
     return (y, preact) if keep else y
 
 
@@ -892,7 +900,7 @@ def matmul_bf16_backward(grad_y: torch.Tensor, a: torch.Tensor, w: torch.Tensor,
     _given(_dev(grad_y, "grad_y"), "grad_y", (rows, cols), bf16, a)
     if act != 0 and preact is None:
         raise ValueError(f"activation {activation!r} needs preact")
-    _given(preact, "preact", (rows, out), bf16, a)
+    kind = 0 if preact is None else _preact(_dev(preact, "preact"), (rows, out), a)[1]
     ws_bytes = matmul_bf16_backward_workspace_bytes(rows, E, out, K)
     if ws_bytes == 0:
         raise CglError(EINVAL, "matmul_bf16_backward", "invalid sizes")
@@ -908,6 +916,6 @@ def matmul_bf16_backward(grad_y: torch.Tensor, a: torch.Tensor, w: torch.Tensor,
         _same(a.device, workspace=_dev(workspace, "workspace"))
         ws_bytes = workspace.numel() * workspace.element_size()
     _launch("cgl_matmul_bf16_backward", lib().cgl_matmul_bf16_backward, a.device, _ptr(grad_y), _ptr(a), rows, _ptr(w), E, out, K,
-            _ptr(expert_offset), act, _ptr(preact), _ptr(grad_a), _ptr(grad_w), _ptr(grad_bias), _ptr(workspace), ws_bytes,
+            _ptr(expert_offset), act, _ptr(preact), kind, _ptr(grad_a), _ptr(grad_w), _ptr(grad_bias), _ptr(workspace), ws_bytes,
             _opts(num_sms, capacity), _ptr(status))
     return MatmulGrads(grad_a, grad_w, grad_bias)

@@ -490,6 +490,8 @@ static bool bf16_product_sizes_ok(int64_t rows, int E, int F, int K) {
            rows <= ((int64_t)1 << 31) - 4096;
 }
 
+static bool preact_ok(const void *preact, int dtype) { return preact == nullptr || dtype == CGL_BF16 || dtype == CGL_F32; }
+
 static cgl_status bf16_product_ok(const uint16_t *a, int64_t rows, const uint16_t *w, int E, int F, int K,
                                   const int32_t *expert_offset, int act, const cgl_opts *opts, uint32_t *status_dev) {
     if (!bf16_product_sizes_ok(rows, E, F, K) || act < CGL_ACT_NONE || act > CGL_ACT_SWIGLU) return CGL_EINVAL;
@@ -505,13 +507,14 @@ static cgl_status bf16_product_ok(const uint16_t *a, int64_t rows, const uint16_
 
 cgl_status cgl_matmul_bf16(const uint16_t *a, int64_t rows, const uint16_t *w, int E, int F, int K,
                            const int32_t *expert_offset, const uint16_t *bias, int act, const uint16_t *residual,
-                           uint16_t *y, uint16_t *preact, const cgl_opts *opts, uint32_t *status_dev, void *stream) {
+                           uint16_t *y, void *preact, int preact_dtype, const cgl_opts *opts, uint32_t *status_dev, void *stream) {
     const cgl_status ok = bf16_product_ok(a, rows, w, E, F, K, expert_offset, act, opts, status_dev);
     if (ok != CGL_OK) return ok;
     if (rows > 0 && !y) return CGL_EINVAL;
-    if (!aligned(bias, 2) || !aligned(residual, 2) || !aligned(y, 2) || !aligned(preact, 2)) return CGL_EALIGN;
+    if (!preact_ok(preact, preact_dtype)) return CGL_EINVAL;
+    if (!aligned(bias, 2) || !aligned(residual, 2) || !aligned(y, 2) || !aligned(preact, preact_dtype == CGL_F32 ? 4 : 2)) return CGL_EALIGN;
     const MatmulArgs m = {a, rows, w, E, F, K, expert_offset, opt_cap(opts), act, opt_sms(opts), status_dev};
-    return launch_matmul_bf16(m, bias, residual, y, preact, static_cast<cudaStream_t>(stream));
+    return launch_matmul_bf16(m, bias, residual, y, preact, preact_dtype == CGL_F32, static_cast<cudaStream_t>(stream));
 }
 
 size_t cgl_matmul_bf16_backward_workspace_bytes(int64_t rows, int E, int F, int K) {
@@ -519,18 +522,19 @@ size_t cgl_matmul_bf16_backward_workspace_bytes(int64_t rows, int E, int F, int 
 }
 
 cgl_status cgl_matmul_bf16_backward(const uint16_t *grad_y, const uint16_t *a, int64_t rows, const uint16_t *w, int E,
-                                    int F, int K, const int32_t *expert_offset, int act, const uint16_t *preact,
-                                    uint16_t *grad_a, uint16_t *grad_w, uint16_t *grad_bias, void *workspace,
+                                    int F, int K, const int32_t *expert_offset, int act, const void *preact,
+                                    int preact_dtype, uint16_t *grad_a, uint16_t *grad_w, uint16_t *grad_bias, void *workspace,
                                     size_t workspace_bytes, const cgl_opts *opts, uint32_t *status_dev, void *stream) {
     const cgl_status ok = bf16_product_ok(a, rows, w, E, F, K, expert_offset, act, opts, status_dev);
     if (ok != CGL_OK) return ok;
     if (rows > 0 && (!grad_y || (act != CGL_ACT_NONE && !preact))) return CGL_EINVAL;
+    if (!preact_ok(preact, preact_dtype)) return CGL_EINVAL;
     if (!workspace || workspace_bytes < matmul_bf16_backward_workspace_bytes(rows, E, F)) return CGL_EINVAL;
-    if (!aligned(grad_y, 2) || !aligned(preact, 2) || !aligned(grad_a, 16) || !aligned(grad_w, 16) || !aligned(grad_bias, 2) ||
+    if (!aligned(grad_y, 2) || !aligned(preact, preact_dtype == CGL_F32 ? 4 : 2) || !aligned(grad_a, 16) || !aligned(grad_w, 16) || !aligned(grad_bias, 2) ||
         !aligned(workspace, 16))
         return CGL_EALIGN;
     const MatmulArgs m = {a, rows, w, E, F, K, expert_offset, opt_cap(opts), act, opt_sms(opts), status_dev};
-    return launch_matmul_bf16_backward(m, grad_y, preact, grad_a, grad_w, grad_bias, workspace,
+    return launch_matmul_bf16_backward(m, grad_y, preact, preact_dtype == CGL_F32, grad_a, grad_w, grad_bias, workspace,
                                        static_cast<cudaStream_t>(stream));
 }
 

@@ -156,7 +156,7 @@ cgl_status launch_route_backward(const float *grad_weights, const void *logits, 
                                  int E, int k, int score, bool renorm, float scale, void *grad, uint32_t *status,
                                  cudaStream_t stream);
 
-// The experts' BF16 product and its gradients (off null: one expert, all rows).
+// The experts' BF16 product and its gradients (off null: one expert, all rows; wait_cycles: a wait's limit, < 0: about a second).
 struct MatmulArgs {
     const uint16_t *a;
     int64_t rows;
@@ -167,11 +167,16 @@ struct MatmulArgs {
     int act;
     int num_sms;
     uint32_t *status;
+    int64_t wait_cycles = -1;
 };
-cgl_status launch_matmul_bf16(const MatmulArgs &m, const uint16_t *bias, const uint16_t *residual, uint16_t *y,
-                              uint16_t *preact, cudaStream_t stream);
+// preact: BF16, or binary32 (preact_f32).
+cgl_status launch_matmul_bf16(const MatmulArgs &m, const uint16_t *bias, const uint16_t *residual, uint16_t *y, void *preact,
+                              bool preact_f32, cudaStream_t stream);
 size_t matmul_bf16_backward_workspace_bytes(int64_t rows, int E, int F);
-cgl_status launch_matmul_bf16_backward(const MatmulArgs &m, const uint16_t *grad_y, const uint16_t *preact, uint16_t *grad_a,
+cgl_status launch_matmul_bf16_backward(const MatmulArgs &m, const uint16_t *grad_y, const void *preact, bool preact_f32, uint16_t *grad_a,
                                        uint16_t *grad_w, uint16_t *grad_bias, void *ws, cudaStream_t stream);
+// Its first step: dz for the products (BF16, rows of *ld values; grad_y itself where it serves) and grad_bias, where wanted.
+cgl_status launch_slope(const MatmulArgs &m, const uint16_t *grad_y, const void *preact, bool preact_f32, bool products,
+                        uint16_t *grad_bias, void *ws, const uint16_t **dz, int64_t *ld, cudaStream_t stream);
 
 }  // namespace cgl

@@ -647,20 +647,21 @@ typedef enum cgl_activation {
  * In (device): a BF16 [num_rows, in] (rows of no expert may hold anything);
  *   w BF16 [E, out, in]; bias BF16 [E, out] or NULL; residual BF16 [num_rows, F] or
  *   NULL (it may be y itself); expert_offset int32 [E + 1].
- * Out (device): y BF16 [num_rows, F]; preact BF16 [num_rows, out], z rounded, which
- *   cgl_matmul_bf16_backward wants, or NULL.  Rows of no expert are NOT written.
+ * Out (device): y BF16 [num_rows, F]; preact [num_rows, out], z for
+ *   cgl_matmul_bf16_backward, CGL_F32 or, rounded, CGL_BF16 (preact_dtype), or NULL.
+ *   Rows of no expert are NOT written.
  * Requires in % 8 == 0; out even with CGL_ACT_SWIGLU; in, out <= 2^20; num_rows <=
  * 2^31 - 4096, and >= E * capacity when padded; a and w 16-byte aligned, the others
- * 2-byte (16-byte aligned rows are faster).  opts: capacity, num_sms (blocks work
- * in pairs: at least two SMs).
+ * to their type (16-byte aligned rows are faster).  opts: capacity, num_sms (blocks
+ * work in pairs: at least two SMs).
  * Device errors: CGL_ERANGE when offsets run backwards or past num_rows (nothing
  * is computed then); CGL_ETIMEOUT if a bounded wait (about a second) inside a
  * block pair gives up, the outputs then undefined.
  */
 cgl_status cgl_matmul_bf16(const uint16_t *a, int64_t num_rows, const uint16_t *w, int num_experts, int out_features,
                            int in_features, const int32_t *expert_offset, const uint16_t *bias, int activation,
-                           const uint16_t *residual, uint16_t *y, uint16_t *preact, const cgl_opts *opts,
-                           uint32_t *status_dev, void *stream);
+                           const uint16_t *residual, uint16_t *y, void *preact, int preact_dtype,
+                           const cgl_opts *opts, uint32_t *status_dev, void *stream);
 
 /* Bytes of device workspace cgl_matmul_bf16_backward needs; host-only, 0 for invalid sizes. */
 size_t cgl_matmul_bf16_backward_workspace_bytes(int64_t num_rows, int num_experts, int out_features, int in_features);
@@ -673,7 +674,7 @@ size_t cgl_matmul_bf16_backward_workspace_bytes(int64_t num_rows, int num_expert
  *   grad_bias[e, f] = bf16_rn( sum_r dz[r, f] )                      (dz in binary32, fixed order)
  * The residual's gradient is g itself.  Each output may be NULL: it is not computed.
  * In (device): grad_y BF16 [num_rows, F]; a, w, expert_offset as for the forward;
- *   preact BF16 [num_rows, out] (NULL with CGL_ACT_NONE, which needs none).
+ *   preact [num_rows, out], CGL_F32 or CGL_BF16 (NULL with CGL_ACT_NONE, which needs none).
  * Out (device): grad_a BF16 [num_rows, in], rows of no expert NOT written; grad_w
  *   BF16 [E, out, in] and grad_bias BF16 [E, out], written in full (0 for experts
  *   without rows).
@@ -684,8 +685,8 @@ size_t cgl_matmul_bf16_backward_workspace_bytes(int64_t num_rows, int num_expert
  */
 cgl_status cgl_matmul_bf16_backward(const uint16_t *grad_y, const uint16_t *a, int64_t num_rows, const uint16_t *w,
                                     int num_experts, int out_features, int in_features,
-                                    const int32_t *expert_offset, int activation, const uint16_t *preact,
-                                    uint16_t *grad_a, uint16_t *grad_w, uint16_t *grad_bias, void *workspace,
+                                    const int32_t *expert_offset, int activation, const void *preact,
+                                    int preact_dtype, uint16_t *grad_a, uint16_t *grad_w, uint16_t *grad_bias, void *workspace,
                                     size_t workspace_bytes, const cgl_opts *opts, uint32_t *status_dev,
                                     void *stream);
 

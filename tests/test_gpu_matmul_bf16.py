@@ -72,10 +72,10 @@ class Case:
             return torch.randint(-4, 5, shape, generator=self.gen, device="cuda", dtype=torch.int8).bfloat16()
         return (scale * torch.randn(shape, generator=self.gen, device="cuda")).bfloat16()
 
-    def forward(self, **kw):
+    def forward(self, wide=False, **kw):
         st = cgl.new_status()
         y = torch.full((self.rows, self.cols), -7.0, dtype=torch.bfloat16, device="cuda")
-        z = torch.full((self.rows, self.f), -7.0, dtype=torch.bfloat16, device="cuda")
+        z = torch.full((self.rows, self.f), -7.0, dtype=torch.float32 if wide else torch.bfloat16, device="cuda")
         how = dict(bias=self.bias, activation=self.act, residual=self.residual, status=st, **kw)
         got = cgl.matmul_bf16(self.a, self.w, self.off, self.cap, y=y, preact=z, **how)
         assert got[0] is y and got[1] is z
@@ -99,9 +99,10 @@ class Case:
             v = act64(ref, self.act)
             more = self.residual[r0:r1].double() if self.residual is not None else 0.0
             if self.whole:
-                assert torch.equal(z[r0:r1], ref.float().bfloat16())
+                assert torch.equal(z[r0:r1], ref.float().to(z.dtype))
             else:
-                assert ((z[r0:r1].double() - ref).abs() <= HALF * ref.abs() + off).all()
+                half = HALF if z.dtype == torch.bfloat16 else 2.0 ** -24
+                assert ((z[r0:r1].double() - ref).abs() <= half * ref.abs() + off).all()
             if self.whole and self.act in ("none", "relu"):
                 assert torch.equal(y[r0:r1], (v + more).float().bfloat16())
                 continue
@@ -159,16 +160,18 @@ COUNTS = [[1], [0, 5, 0], [3, 128, 1, 64], [200, 0, 33, 257, 1], [300]]
 @pytest.mark.parametrize("act", ["none", "relu", "swiglu"])
 def test_compact(act, counts, k, f):
     c = Case(counts, k, f, k * f + len(counts), act=act)
-    _, z = c.check_forward()
-    c.check_backward(z)
+    for wide in (False, True):
+        _, z = c.check_forward(wide=wide)
+        c.check_backward(z)
 
 
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("counts,k,f", [([1], 7168, 512), ([4, 0, 130, 17], 1000, 264), ([513, 65], 512, 384), ([40] * 24, 136, 64)])
 def test_normal_values(act, counts, k, f):
     c = Case(counts, k, f, k, act=act, whole=False)
-    _, z = c.check_forward()
-    c.check_backward(z)
+    for wide in (False, True):
+        _, z = c.check_forward(wide=wide)
+        c.check_backward(z)
 
 
 @pytest.mark.parametrize("act", ["none", "swiglu"])
@@ -189,10 +192,11 @@ def test_padded(counts, cap, act):
 
 @pytest.mark.parametrize("f", [1, 7, 9, 33, 255])
 def test_odd_features(f):
-    for act in ("none", "relu"):
-        c = Case([5, 0, 70], 88, f, f, act=act)
-        _, z = c.check_forward()
-        c.check_backward(z)
+    for act in ("none", "relu", "swiglu"):
+        c = Case([5, 0, 70], 88, 2 * f if act == "swiglu" else f, f, act=act)
+        for wide in (False, True):
+            _, z = c.check_forward(wide=wide)
+            c.check_backward(z)
 
 
 def test_without_bias_and_residual():
@@ -308,7 +312,7 @@ def test_activations_of_large_sums():
     for act in ACTS[:4]:
         y, z = cgl.matmul_bf16(a, w, activation=act, with_preact=True)
         ref = act64(x.double(), act)
-        assert torch.equal(z, torch.stack((x, x), 1))
+        assert z.dtype == torch.float32 and torch.equal(z, torch.stack((x, x), 1).float())
         assert ((y.double() - ref[:, None]).abs() <= HALF * ref.abs()[:, None] + 2.0 ** -18 * ref.abs()[:, None] + 1e-30).all()
         d = cgl.matmul_bf16_backward(g, a, w, activation=act, preact=z, want_bias=True)
         dz = slope64(x.double(), torch.ones(n, device="cuda", dtype=torch.float64), act)
@@ -412,6 +416,8 @@ def test_unaligned_rows():
         c = Case([9, 0, 130], 136, f, 3, act=act, whole=False)
         y, z = c.forward()
         d = c.backward(z)
+        _, z32 = c.forward(wide=True)
+        d32 = c.backward(z32)
 
         def moved(t, shift=1):
             m = torch.full((t.numel() + shift + 8,), -7.0, dtype=t.dtype, device="cuda")
@@ -427,6 +433,10 @@ def test_unaligned_rows():
                                       grad_bias=moved(torch.zeros_like(c.bias)))
         rows = c.covered
         assert torch.equal(d2.grad_a[rows], d.grad_a[rows]) and torch.equal(d2.grad_w, d.grad_w) and torch.equal(d2.grad_bias, d.grad_bias)
+        mz = moved(torch.full_like(z32, -7.0))
+        cgl.matmul_bf16(c.a, c.w, c.off, bias=c.bias, activation=act, residual=c.residual, preact=mz)
+        d2 = cgl.matmul_bf16_backward(c.g, c.a, c.w, c.off, activation=act, preact=None if act == "none" else mz, want_bias=True)
+        assert torch.equal(mz, z32) and torch.equal(d2.grad_a[rows], d32.grad_a[rows]) and torch.equal(d2.grad_w, d32.grad_w)
 
 
 def test_refusals():
@@ -443,7 +453,7 @@ def test_refusals():
         (ValueError, lambda: cgl.matmul_bf16(a, w[:, :31].contiguous(), off, activation="swiglu")),
         (ValueError, lambda: cgl.matmul_bf16(a, w, off, bias=c.bias[0])), (TypeError, lambda: cgl.matmul_bf16(a, w, off, bias=c.bias.float())),
         (ValueError, lambda: cgl.matmul_bf16(a, w, off, activation="swiglu", residual=c.residual)),
-        (ValueError, lambda: cgl.matmul_bf16(a, w, off, y=c.residual[:4])), (TypeError, lambda: cgl.matmul_bf16(a, w, off, preact=c.residual.float())),
+        (ValueError, lambda: cgl.matmul_bf16(a, w, off, y=c.residual[:4])), (TypeError, lambda: cgl.matmul_bf16(a, w, off, preact=c.residual.half())),
         (ValueError, lambda: cgl.matmul_bf16_backward(g[:4], a, w, off)), (TypeError, lambda: cgl.matmul_bf16_backward(g.float(), a, w, off)),
         (ValueError, lambda: cgl.matmul_bf16_backward(g, a, w, off, activation="silu")),
         (ValueError, lambda: cgl.matmul_bf16_backward(g, a, w, off, activation="silu", preact=g[:3])),

@@ -57,19 +57,20 @@ SHARED = [
 
 
 @pytest.mark.parametrize("bad,code", SHARED + [
-    (dict(y=None), cgl.EINVAL), (dict(y=P + 1), cgl.EALIGN), (dict(bias=P + 1), cgl.EALIGN), (dict(res=P + 1), cgl.EALIGN), (dict(z=P + 1), cgl.EALIGN)])
+    (dict(y=None), cgl.EINVAL), (dict(y=P + 1), cgl.EALIGN), (dict(bias=P + 1), cgl.EALIGN), (dict(res=P + 1), cgl.EALIGN), (dict(z=P + 1), cgl.EALIGN),
+    (dict(zt=1), cgl.EINVAL), (dict(zt=3), cgl.EINVAL), (dict(zt=2, z=P + 2), cgl.EALIGN)])
 def test_matmul(L, bad, code):
-    a = dict(dict(a=P, rows=16, w=P, E=4, F=32, K=64, off=P, bias=P, act=3, res=P, y=P, z=P, opts=None, st=P), **bad)
-    assert L.cgl_matmul_bf16(a["a"], a["rows"], a["w"], a["E"], a["F"], a["K"], a["off"], a["bias"], a["act"], a["res"], a["y"], a["z"],
+    a = dict(dict(a=P, rows=16, w=P, E=4, F=32, K=64, off=P, bias=P, act=3, res=P, y=P, z=P, zt=0, opts=None, st=P), **bad)
+    assert L.cgl_matmul_bf16(a["a"], a["rows"], a["w"], a["E"], a["F"], a["K"], a["off"], a["bias"], a["act"], a["res"], a["y"], a["z"], a["zt"],
                              a["opts"], a["st"], None) == code
 
 
 @pytest.mark.parametrize("bad,code", SHARED + [
     (dict(g=None), cgl.EINVAL), (dict(z=None), cgl.EINVAL), (dict(ws=None), cgl.EINVAL), (dict(wsb=100), cgl.EINVAL), (dict(g=P + 1), cgl.EALIGN),
-    (dict(z=P + 1), cgl.EALIGN), (dict(da=P + 8), cgl.EALIGN), (dict(dw=P + 8), cgl.EALIGN), (dict(db=P + 1), cgl.EALIGN), (dict(ws=P + 8), cgl.EALIGN)])
+    (dict(z=P + 2), cgl.EALIGN), (dict(zt=0, z=P + 1), cgl.EALIGN), (dict(zt=1), cgl.EINVAL), (dict(da=P + 8), cgl.EALIGN), (dict(dw=P + 8), cgl.EALIGN), (dict(db=P + 1), cgl.EALIGN), (dict(ws=P + 8), cgl.EALIGN)])
 def test_matmul_backward(L, bad, code):
-    a = dict(dict(g=P, a=P, rows=16, w=P, E=4, F=32, K=64, off=P, act=3, z=P, da=P, dw=P, db=P, ws=P, wsb=1 << 24, opts=None, st=P), **bad)
-    assert L.cgl_matmul_bf16_backward(a["g"], a["a"], a["rows"], a["w"], a["E"], a["F"], a["K"], a["off"], a["act"], a["z"], a["da"], a["dw"],
+    a = dict(dict(g=P, a=P, rows=16, w=P, E=4, F=32, K=64, off=P, act=3, z=P, zt=2, da=P, dw=P, db=P, ws=P, wsb=1 << 24, opts=None, st=P), **bad)
+    assert L.cgl_matmul_bf16_backward(a["g"], a["a"], a["rows"], a["w"], a["E"], a["F"], a["K"], a["off"], a["act"], a["z"], a["zt"], a["da"], a["dw"],
                                       a["db"], a["ws"], a["wsb"], a["opts"], a["st"], None) == code
 
 
