@@ -127,111 +127,542 @@ __device__ __noinline__ bool pick_exact(const RouteArgs &a, const void *row, int
     return true;
 }
 
-// What lane j's slot has of its token's weight (scale aside), slots without an
-// expert 0; D over the slots where they are renormalised, `m` and `sum` the row's
-// largest logit and sum of exponentials for the plain softmax.
-__device__ __forceinline__ float share(int score, bool renorm, bool there, float l, float m, float sum) {
+// Which groups stay, in binary64: a bit each.  Lanes share the groups out, a power of two of them a group.
+template <int DT>
+__device__ __noinline__ uint32_t groups_exact(const RouteArgs &a, const void *row) {
+    const int lane = threadIdx.x & 31, E = a.E, per = E / a.groups;
+    double m = -INFINITY, sum = 0.0;
+    const bool softmax = a.score == CGL_SCORE_SOFTMAX, scored = a.bias != nullptr || a.by == CGL_GROUP_TOP2;
+    if (softmax && scored) {
+        for (int e = lane; e < E; e += 32) m = fmax(m, (double)logit<DT>(row, e));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kAll, m, o));
+#pragma unroll 2
+        for (int e = lane; e < E; e += 32) {
+            const double l = (double)logit<DT>(row, e);
+            if (l > -INFINITY) sum += exp(l - m);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    }
+    int share = 32;
+    while (share * a.groups > 32) share /= 2;
+    const int g = lane / share;
+    double first = -INFINITY, second = -INFINITY;
+    if (g < a.groups)
+#pragma unroll 2
+        for (int i = lane % share; i < per; i += share) {
+            const int e = g * per + i;
+            double v = (double)logit<DT>(row, e);
+            if (scored && v > -INFINITY) {
+                v = softmax ? exp(v - m) / sum : 1.0 / (1.0 + exp(-v));
+                if (a.bias != nullptr) v += (double)__ldg(a.bias + e);
+            }
+            second = fmax(second, fmin(first, v));
+            first = fmax(first, v);
+        }
+    for (int o = 1; o < share; o <<= 1) {
+        const double u = __shfl_xor_sync(kAll, first, o), v = __shfl_xor_sync(kAll, second, o);
+        second = fmax(fmin(first, u), fmax(second, v));
+        first = fmax(first, u);
+    }
+    const double value = a.by == CGL_GROUP_TOP2 && second > -INFINITY ? first + second : first;
+    int rank = 0;
+    for (int i = 0; i < a.groups; ++i) {
+        const double v = __shfl_sync(kAll, value, i * share);
+        rank += v > value || (v == value && i < g);
+    }
+    const bool kept = g < a.groups && value > -INFINITY && rank < a.keep;
+    uint32_t open = 0;
+    for (int i = 0; i < a.groups; ++i) open |= (uint32_t)__shfl_sync(kAll, (int)kept, i * share) << i;
+    return open;
+}
+
+// Over the lanes of the picks: the first eight (size 4) or all (16).
+__device__ __forceinline__ float picks_sum(float v, int size) {
+    for (int o = size; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+__device__ __forceinline__ float picks_max(float v, int size) {
+    for (int o = size; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+
+// What lane j's slot has of its token's weight (scale aside), slots without an expert
+// 0: the sigmoid, or with renorm the quotient by the picks' sum (softmax or sigmoid).
+__device__ __forceinline__ float share(int score, bool renorm, bool there, float l, int size) {
+    const float top = renorm ? picks_max(there ? l : -INFINITY, size) : 0.0f;
     float t;
     if (score == CGL_SCORE_SIGMOID) {
         // sigmoid(l) exp(-b), b = min(largest l, 0): a factor that all slots share keeps the quotient where every sigmoid underflows
-        const float b = renorm ? fminf(warp_max(there ? l : -INFINITY), 0.0f) : 0.0f;
-        const float z = expf(-fabsf(l));
+        const float b = fminf(top, 0.0f), z = expf(-fabsf(l));
         t = (l > 0.0f ? 1.0f : expf(l - b)) / (1.0f + z);
     } else {
-        const float b = renorm ? warp_max(there ? l : -INFINITY) : m;
-        t = expf(l - b);
-        if (!renorm) return there && l > -INFINITY ? t / sum : there && l != l ? l : 0.0f;
+        t = expf(l - top);
     }
     if (!there || l == -INFINITY) t = 0.0f;
     if (!renorm) return t;
-    const float d = warp_sum(t);
+    const float d = picks_sum(t, size);
     return d == 0.0f ? 0.0f : t / d;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads)
+// ---- the order in binary32, by keys ------------------------------------------------------------
+
+// 32-bit keys in the order of floats: the sign flipped, negative values reversed.
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+    return __uint_as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// A lane's V neighbouring logits, VEC in pieces of eight.
+template <int DT, int V, bool VEC>
+struct Row {
+    uint4 raw[VEC ? V / 8 : 1][DT == CGL_F32 ? 2 : 1];
+    float one[VEC ? 1 : V];
+    __device__ __forceinline__ void load(const void *row, int E, int lane) {
+        if (VEC) {
+#pragma unroll
+            for (int c = 0; c < V / 8; ++c)
+                if (lane * V + 8 * c < E)
+#pragma unroll
+                    for (int h = 0; h < (DT == CGL_F32 ? 2 : 1); ++h)   // kept in L1: the picks' logits are read again
+                        raw[c][h] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + (lane * V + 8 * c) * (DT == CGL_F32 ? 4 : 2)) + h);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (lane * V + i < E) one[i] = logit<DT>(row, lane * V + i);
+        }
+    }
+    __device__ __forceinline__ void widen(float l[V], int E, int lane) const {
+        if (VEC) {
+#pragma unroll
+            for (int c = 0; c < V / 8; ++c) {
+                const uint32_t w[8] = {raw[c][0].x, raw[c][0].y, raw[c][0].z, raw[c][0].w, raw[c][DT == CGL_F32].x,
+                                       raw[c][DT == CGL_F32].y, raw[c][DT == CGL_F32].z, raw[c][DT == CGL_F32].w};
+                const bool there = lane * V + 8 * c < E;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float f;
+                    if (DT == CGL_F32) f = __uint_as_float(w[i]);
+                    else if (DT == CGL_BF16) f = (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+                    else f = __half2float(__ushort_as_half((unsigned short)((i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu)));
+                    l[8 * c + i] = there ? f : -INFINITY;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) l[i] = lane * V + i < E ? one[i] : -INFINITY;
+        }
+    }
+};
+
+// Descending, by a network (V <= 8); beyond, lists stay as they are and pop() looks for the next.
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t k[V]) {
+    const auto at = [&](int i, int j) {
+        const uint32_t x = max(k[i], k[j]), y = min(k[i], k[j]);
+        k[i] = x, k[j] = y;
+    };
+    if (V == 4) {
+        at(0, 1), at(2, 3), at(0, 2), at(1, 3), at(1, 2);
+    } else if (V == 8) {
+        at(0, 2), at(1, 3), at(4, 6), at(5, 7);
+        at(0, 4), at(1, 5), at(2, 6), at(3, 7);
+        at(0, 1), at(2, 3), at(4, 5), at(6, 7);
+        at(2, 4), at(3, 5);
+        at(1, 4), at(3, 6);
+        at(1, 2), at(3, 4), at(5, 6);
+    }
+}
+// The lane's largest key, and a list without it.
+template <int V>
+__device__ __forceinline__ uint32_t head(const uint32_t k[V]) {
+    if (V <= 8) return k[0];
+    uint32_t m = k[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = max(m, k[i]);
+    return m;
+}
+template <int V>
+__device__ __forceinline__ void pop(uint32_t k[V], uint32_t top) {   // keys are unique
+    if (V <= 8) {
+        if (k[0] == top) {
+#pragma unroll
+            for (int i = 0; i + 1 < V; ++i) k[i] = k[i + 1];
+            k[V - 1] = 0;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) k[i] = k[i] == top ? 0 : k[i];
+    }
+}
+
+// Keys hold the choice's first 32 - B bits and, below, B bits that put lower indexes
+// first; 0 cannot be picked.  Where what is cut off, or the choice's own rounding,
+// could change the order (`near`: between neighbours of the order down to the first
+// that is not picked), the candidates are compared again in binary64, all of them in
+// lanes: one value a lane and not a whole row.
+template <int DT, int V, bool VEC>
+__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2)
 route_kernel(const RouteArgs a) {
+    constexpr int B = V <= 8 ? 8 : 10;
+    constexpr uint32_t kLow = (1u << B) - 1;
+    __shared__ uint32_t s_group[kWarps][2][32];   // groups that do not fill whole lanes: their two largest keys
     griddep_wait();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, E = a.E, k = a.k, warp = threadIdx.x >> 5;
+    const bool biased = a.bias != nullptr, softmax = a.score == CGL_SCORE_SOFTMAX, whole = softmax && (biased || !a.renorm || (a.groups > 1 && a.by == CGL_GROUP_TOP2));
+    // what a choice may be off by: of itself what is cut off (none in 16 bits), and 2^-20 where it was computed
+    const bool exact = DT != CGL_F32 && !biased;
+    const float cut = __uint_as_float((127 - 22 + B) << 23), slack = biased ? 0x1p-19f : 0.0f;
+    const int per = E / a.groups, lanes = per / V;   // lanes a group
+    const bool filled = per % V == 0 && (lanes & (lanes - 1)) == 0;
+    const int size = k <= 8 ? 4 : 16;                // shuffles over the picks
     const int64_t step = (int64_t)gridDim.x * kWarps;
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.n; t += step) {
-        const char *row = static_cast<const char *>(a.logits) + t * a.E * (DT == CGL_F32 ? 4 : 2);
-        int e = -1;
-        const bool fine = pick_exact<DT>(a, row, e);
-        const bool there = fine && e >= 0;
-        const float l = there ? logit<DT>(row, e) : -INFINITY;
-        float m = -INFINITY, sum = 0.0f;
-        if (a.score == CGL_SCORE_SOFTMAX && !a.renorm && fine) {
-            for (int i = lane; i < a.E; i += 32) m = fmaxf(m, logit<DT>(row, i));
+    const size_t row_bytes = (size_t)E * (DT == CGL_F32 ? 4 : 2);
+    float bias[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = biased && lane * V + i < E ? __ldg(a.bias + lane * V + i) : 0.0f;
+    int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+    Row<DT, V, VEC> ahead;
+    if (t < a.n) ahead.load(static_cast<const char *>(a.logits) + t * row_bytes, E, lane);
+    for (; t < a.n; t += step) {
+        const char *row = static_cast<const char *>(a.logits) + t * row_bytes;
+        float l[V];
+        ahead.widen(l, E, lane);
+        if (t + step < a.n) ahead.load(row + step * row_bytes, E, lane);
+        bool bad = false;
+        float top = -INFINITY, sum = 1.0f;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+            top = warp_max(top);
+            bad = top == INFINITY;
+            const float m = top == -INFINITY ? 0.0f : top;
+            sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum += ex2((l[i] - m) * kLog2e);
+            sum = warp_sum(sum);
+            top = m;
+        }
+        const float inv = rcp(sum);
+        const auto score = [&](float x) { return softmax ? ex2((x - top) * kLog2e) * inv : rcp(1.0f + ex2(-x * kLog2e)); };
+        uint32_t key[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float c = biased ? score(l[i]) + bias[i] : l[i];
+            bad = bad || l[i] != l[i] || (l[i] > -INFINITY && c != c) || (softmax && l[i] == INFINITY);
+            key[i] = l[i] > -INFINITY && c > -INFINITY ? (ordered(c) & ~kLow) | (kLow - (lane * V + i)) : 0u;
+        }
+        bad = __any_sync(kAll, bad);
+        bool again = false;        // the whole token in binary64
+        if (a.groups > 1) {
+            uint32_t first, second;   // a group's two largest keys, in its lanes, or in lane g that of group g
+            int g = lane, stride = 1;
+            if (filled) {
+                if (V <= 8) {
+                    sort_keys<V>(key);
+                    first = key[0];
+                    second = V > 1 ? key[V > 1] : 0u;
+                } else {
+                    first = second = 0;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) second = max(second, min(first, key[i])), first = max(first, key[i]);
+                }
+                for (int o = 1; o < lanes; o <<= 1) {
+                    const uint32_t u = __shfl_xor_sync(kAll, first, o), v = __shfl_xor_sync(kAll, second, o);
+                    second = max(min(first, u), max(second, v));
+                    first = max(first, u);
+                }
+                g = lane / lanes, stride = lanes;
+            } else {
+                s_group[warp][0][lane] = s_group[warp][1][lane] = 0;
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (key[i] != 0) atomicMax(&s_group[warp][0][(lane * V + i) / per], key[i]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (key[i] != 0 && key[i] != s_group[warp][0][(lane * V + i) / per]) atomicMax(&s_group[warp][1][(lane * V + i) / per], key[i]);
+                __syncwarp();
+                first = s_group[warp][0][lane], second = s_group[warp][1][lane];
+            }
+            const bool real = g < a.groups && first != 0;
+            // the group's value, and what it may be off by
+            float value = -INFINITY, off = 0.0f;
+            if (real) {
+                const float x = unordered(first & ~kLow), y = unordered(second & ~kLow);
+                if (a.by == CGL_GROUP_MAX) {
+                    value = x;
+                    off = exact ? 0.0f : slack + cut * fabsf(x);
+                } else if (biased) {
+                    value = second != 0 ? x + y : x;
+                    off = 2 * slack + cut * (fabsf(x) + (second != 0 ? fabsf(y) : 0.0f));
+                } else {
+                    value = score(x) + (second != 0 ? score(y) : 0.0f);
+                    off = 0x1p-18f + (exact ? 0.0f : cut * (fabsf(x) + (second != 0 ? fabsf(y) : 0.0f)));   // a score's slope is below 1
+                }
+            }
+            int rank = 0;
+            for (int i = 0; i < a.groups; ++i) {
+                const float v = __shfl_sync(kAll, value, i * stride);
+                rank += v > value || (v == value && i < g);
+            }
+            const bool kept = real && rank < a.keep;
+            const float low = -warp_max(kept ? off - value : -INFINITY), high = warp_max(real && !kept ? value + off : -INFINITY);
+            // exact values that are equal stand in the order of their groups; an order that their errors could change is looked at again
+            const bool unsure = high > -INFINITY && !(exact && a.by == CGL_GROUP_MAX) && !(low > high);
+            if (filled) {
+                bool stays = kept;
+                if (unsure && !bad) stays = (groups_exact<DT>(a, row) >> (g & 31)) & 1;
+#pragma unroll
+                for (int i = 0; i < V; ++i) key[i] = stays ? key[i] : 0u;
+            } else {
+                uint32_t open = __ballot_sync(kAll, kept);
+                if (unsure && !bad) open = groups_exact<DT>(a, row);
+#pragma unroll
+                for (int i = 0; i < V; ++i) key[i] = (open >> ((lane * V + i) / per)) & 1 ? key[i] : 0u;
+                sort_keys<V>(key);
+            }
+        } else {
+            sort_keys<V>(key);
+        }
+        uint32_t mine = 0, last = 0;     // lane j: the j-th key; last: the one behind the k-th
+        int found = 0;
+        for (; found <= k; ++found) {
+            const uint32_t m = __reduce_max_sync(kAll, head<V>(key));
+            if (lane == found) mine = m;
+            last = m;
+            pop<V>(key, m);
+        }
+        if (!exact && !bad && !again) {
+            uint32_t next = __shfl_down_sync(kAll, mine, 1);
+            if (lane == 31) next = last;
+            const float x = unordered(mine & ~kLow), y = unordered(next & ~kLow);
+            const float margin = 2 * slack + cut * fmaxf(fabsf(x), fabsf(y));
+            const bool near = lane < k && next != 0 && (biased ? !(x - y > margin) : (mine & ~kLow) == (next & ~kLow));
+            if (__any_sync(kAll, near)) {
+                // candidates: down to the first that is surely behind the k-th, at most 32
+                const float kth = unordered(__shfl_sync(kAll, mine, k - 1) & ~kLow);
+                found = k;
+                bool more = true;
+                while (true) {
+                    const float z = unordered(last & ~kLow);
+                    more = last != 0 && (biased ? !(kth - z > 2 * slack + cut * fmaxf(fabsf(kth), fabsf(z))) : z == kth);
+                    if (!more || found == 32) break;
+                    if (lane == found) mine = last;
+                    ++found;
+                    last = __reduce_max_sync(kAll, head<V>(key));
+                    pop<V>(key, last);
+                }
+                again = more;
+                if (!again) {
+                    const bool there = lane < found && mine != 0;
+                    const int e = there ? (int)(kLow - (mine & kLow)) : E;
+                    double v = -INFINITY, norm = 1.0;
+                    if (biased && softmax) {
+                        norm = 0.0;
+#pragma unroll 1
+                        for (int i = lane; i < E; i += 32) norm += exp((double)logit<DT>(row, i) - (double)top);
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) norm += __shfl_xor_sync(kAll, norm, o);
+                    }
+                    if (there) {
+                        v = (double)logit<DT>(row, e);
+                        if (biased) v = (softmax ? exp(v - (double)top) / norm : 1.0 / (1.0 + exp(-v))) + (double)__ldg(a.bias + e);
+                    }
+                    int rank = 0;
+                    for (int i = 0; i < found; ++i) {
+                        const double u = __shfl_sync(kAll, v, i);
+                        const int j = __shfl_sync(kAll, e, i);
+                        rank += u > v || (u == v && j < e);
+                    }
+                    const uint32_t key_of = there ? mine : 0;
+                    mine = 0;
+                    for (int i = 0; i < found; ++i) {
+                        const int r = __shfl_sync(kAll, rank, i);
+                        const uint32_t q = __shfl_sync(kAll, key_of, i);
+                        if (lane == r && q != 0) mine = q;
+                    }
+                }
+            }
+        }
+        int e = lane < k && mine != 0 ? (int)(kLow - (mine & kLow)) : -1;
+        if (again && !bad) bad = !pick_exact<DT>(a, row, e);
+        const bool there = !bad && e >= 0;
+        const float x = there ? logit<DT>(row, e) : -INFINITY;
+        float w;
+        if (softmax && !a.renorm) {
+            w = there ? expf(x - top) / sum : 0.0f;
+        } else {
+            w = share(a.score, a.renorm, there, x, size);
+        }
+        if (lane < k) {
+            a.idx[t * k + lane] = there ? e : -1;
+            a.weights[t * k + lane] = bad ? NAN : there ? a.scale * w : 0.0f;
+        }
+        if (bad && lane == 0) report(a.status, kErrRange);
+    }
+}
+
+// ---- the gradient --------------------------------------------------------------------------------
+
+// V neighbouring experts a lane, in pieces of eight (VEC), or experts lane, lane + 32, ...
+template <int DT, int V, bool VEC>
+__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2)
+route_backward_kernel(const float *__restrict__ gw, const void *__restrict__ logits, const int32_t *__restrict__ idx, int64_t n,
+                      int E, int k, int score, bool renorm, float scale, void *__restrict__ grad, uint32_t *status) {
+    extern __shared__ __align__(16) float s_rows[];   // a row of the picks' gradients a warp, zero between tokens
+    griddep_wait();
+    const int lane = threadIdx.x & 31, pitch = (E + 7) / 8 * 8, size = k <= 8 ? 4 : 16;
+    float *s = s_rows + (threadIdx.x >> 5) * pitch;
+    for (int i = lane; i < pitch; i += 32) s[i] = 0.0f;
+    __syncwarp();
+    const int64_t step = (int64_t)gridDim.x * kWarps;
+    const size_t row_bytes = (size_t)E * (DT == CGL_F32 ? 4 : 2);
+    const bool whole = score == CGL_SCORE_SOFTMAX && !renorm;
+    int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const auto expert = [&](int i) { return VEC ? (i / 8 * 32 + lane) * 8 + i % 8 : lane + 32 * i; };
+    Row<DT, 8, VEC> ahead[V / 8];
+    const auto load = [&](int64_t t) {
+        const char *row = static_cast<const char *>(logits) + t * row_bytes;
+#pragma unroll
+        for (int c = 0; c < V / 8; ++c) {
+            if (VEC) ahead[c].load(row + c * 256 * (DT == CGL_F32 ? 4 : 2), E - c * 256, lane);
+            else
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (expert(8 * c + i) < E) ahead[c].one[VEC ? 0 : i] = logit<DT>(row, expert(8 * c + i));
+        }
+    };
+    int id = -1;
+    float g = 0.0f;
+    if (t < n) {
+        if (lane < k) id = __ldg(idx + t * k + lane), g = __ldg(gw + t * k + lane);
+        if (whole) load(t);
+    }
+    for (; t < n; t += step) {
+        const char *row = static_cast<const char *>(logits) + t * row_bytes;
+        const int e = id;
+        const bool there = e >= 0 && e < E;
+        const float x = there ? logit<DT>(row, e) : -INFINITY, gs = there ? scale * g : 0.0f;
+        if (!there && e != -1) report(status, kErrRange);
+        float l[V], m = -INFINITY, sum = 0.0f;
+        if (whole) {
+#pragma unroll
+            for (int c = 0; c < V / 8; ++c) {
+                if (VEC) ahead[c].widen(l + 8 * c, E - c * 256, lane);
+                else
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) l[8 * c + i] = expert(8 * c + i) < E ? ahead[c].one[VEC ? 0 : i] : -INFINITY;
+            }
+        }
+        if (t + step < n) {
+            if (lane < k) id = __ldg(idx + (t + step) * k + lane), g = __ldg(gw + (t + step) * k + lane);
+            if (whole) load(t + step);
+        }
+        float w;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
             m = warp_max(m);
-            for (int i = lane; i < a.E; i += 32) {
-                const float x = logit<DT>(row, i);
-                if (x > -INFINITY) sum += expf(x - m);
+            m = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                l[i] = ex2((l[i] - m) * kLog2e);
+                sum += l[i];
             }
             sum = warp_sum(sum);
+            w = there && x != -INFINITY ? expf(x - m) / sum : 0.0f;   // a NaN stays
+        } else {
+            w = share(score, renorm, there, x, size);
         }
-        const float w = share(a.score, a.renorm, there, l, m, sum);
-        if (lane < a.k) {
-            a.idx[t * a.k + lane] = there ? e : -1;
-            a.weights[t * a.k + lane] = fine ? (there ? a.scale * w : 0.0f) : NAN;
+        const float dot = picks_sum(there ? gs * w : 0.0f, size);
+        float v = w * (renorm ? gs - dot : gs);
+        if (score == CGL_SCORE_SIGMOID) {   // 1 - sigmoid
+            const float z = expf(-fabsf(x));
+            v *= (x > 0.0f ? z : 1.0f) / (1.0f + z);
         }
-        if (!fine && lane == 0) report(a.status, kErrRange);
+        // into their places; an expert that is in two slots, which its slots' numbers show, gets its terms one by one
+        if (there) s[e] = __int_as_float(lane);
+        __syncwarp();
+        const bool twice = there && __float_as_int(s[e]) != lane;
+        if (__any_sync(kAll, twice)) {
+            __syncwarp();
+            if (there) s[e] = 0.0f;
+            __syncwarp();
+            for (int j = 0; j < k; ++j) {
+                if (lane == j && there) s[e] += v;
+                __syncwarp();
+            }
+        } else {
+            __syncwarp();
+            if (there) s[e] = v;
+        }
+        __syncwarp();
+        const bool any = __any_sync(kAll, there);
+        const bool spread = whole && any && sum != 0.0f;   // a token without a slot gets 0, whatever its logits
+        const float base = -__shfl_sync(kAll, dot, 0) / sum;
+#pragma unroll
+        for (int c = 0; c < V / 8; ++c) {
+            float o[8];
+            if (VEC) {
+                if (expert(8 * c) >= E) break;
+                *reinterpret_cast<float4 *>(o) = *reinterpret_cast<const float4 *>(s + expert(8 * c));
+                *reinterpret_cast<float4 *>(o + 4) = *reinterpret_cast<const float4 *>(s + expert(8 * c) + 4);
+                if (spread)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = fmaf(base, l[8 * c + i], o[i]);
+                Vec8<DT>::store(grad, (t * E + expert(8 * c)) >> 3, o);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (expert(8 * c + i) < E)
+                        put<DT>(grad, t * E + expert(8 * c + i), spread ? fmaf(base, l[8 * c + i], s[expert(8 * c + i)]) : s[expert(8 * c + i)]);
+            }
+        }
+        __syncwarp();
+        if (there) s[e] = 0.0f;
+        __syncwarp();
     }
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads)
-route_backward_kernel(const float *__restrict__ gw, const void *__restrict__ logits, const int32_t *__restrict__ idx, int64_t n,
-                      int E, int k, int score, bool renorm, float scale, void *__restrict__ grad, uint32_t *status) {
-    extern __shared__ float s_rows[];   // a row of E values a warp
-    griddep_wait();
-    const int lane = threadIdx.x & 31;
-    float *s = s_rows + (threadIdx.x >> 5) * E;
-    const int64_t step = (int64_t)gridDim.x * kWarps;
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < n; t += step) {
-        const char *row = static_cast<const char *>(logits) + t * E * (DT == CGL_F32 ? 4 : 2);
-        const int e = lane < k ? __ldg(idx + t * k + lane) : -1;
-        const bool there = e >= 0 && e < E;
-        if (!there && e != -1) report(status, kErrRange);
-        const bool any = __any_sync(kAll, there);
-        const bool whole = score == CGL_SCORE_SOFTMAX && !renorm && any;
-        float m = -INFINITY, sum = 0.0f;
-        if (whole) {
-            for (int i = lane; i < E; i += 32) m = fmaxf(m, logit<DT>(row, i));
-            m = warp_max(m);
-            for (int i = lane; i < E; i += 32) {
-                const float x = logit<DT>(row, i);
-                if (!(x == -INFINITY)) sum += expf(x - m);
-            }
-            sum = warp_sum(sum);
-        }
-        const float l = there ? logit<DT>(row, e) : -INFINITY;
-        const float w = share(score, renorm, there, l, m, sum), g = there ? scale * __ldg(gw + t * k + lane) : 0.0f;
-        const float dot = warp_sum(there ? g * w : 0.0f);
-        float v = w * (renorm ? g - dot : g);
-        if (score == CGL_SCORE_SIGMOID) {   // 1 - sigmoid(l)
-            const float z = expf(-fabsf(l));
-            v *= (l > 0.0f ? z : 1.0f) / (1.0f + z);
-        }
-        for (int i = lane; i < E; i += 32) {
-            const float x = whole ? logit<DT>(row, i) : 0.0f;
-            s[i] = whole && !(x == -INFINITY) ? -dot * (expf(x - m) / sum) : 0.0f;
-        }
-        __syncwarp();
-        for (int j = 0; j < k; ++j) {   // in the slots' order: an expert may be in two
-            if (lane == j && there) s[e] += v;
-            __syncwarp();
-        }
-        for (int i = lane; i < E; i += 32) put<DT>(grad, t * E + i, s[i]);
-        __syncwarp();
-    }
+void *route_by_width(int E, bool vec) {
+    if (E <= 32) return (void *)route_kernel<DT, 1, false>;
+    if (E <= 128) return (void *)route_kernel<DT, 4, false>;
+    if (E <= 256) return vec ? (void *)route_kernel<DT, 8, true> : (void *)route_kernel<DT, 8, false>;
+    if (E <= 512) return vec ? (void *)route_kernel<DT, 16, true> : (void *)route_kernel<DT, 16, false>;
+    return vec ? (void *)route_kernel<DT, 32, true> : (void *)route_kernel<DT, 32, false>;
+}
+template <int DT>
+void *backward_by_width(int E, bool vec) {
+    if (E <= 256) return vec ? (void *)route_backward_kernel<DT, 8, true> : (void *)route_backward_kernel<DT, 8, false>;
+    return vec ? (void *)route_backward_kernel<DT, 32, true> : (void *)route_backward_kernel<DT, 32, false>;
 }
 
 }  // namespace
 
 cgl_status launch_route(const RouteArgs &a, cudaStream_t stream) {
     if (a.n == 0) return CGL_OK;
-    const auto kernel = a.dtype == CGL_BF16 ? route_kernel<CGL_BF16> : a.dtype == CGL_F16 ? route_kernel<CGL_F16> : route_kernel<CGL_F32>;
+    const bool vec = a.E % 8 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
+    const auto kernel = reinterpret_cast<void (*)(RouteArgs)>(a.dtype == CGL_BF16  ? route_by_width<CGL_BF16>(a.E, vec)
+                                                              : a.dtype == CGL_F16 ? route_by_width<CGL_F16>(a.E, vec)
+                                                                                   : route_by_width<CGL_F32>(a.E, vec));
     const int grid = persistent_grid((const void *)kernel, kThreads, 0, 8, 0, (a.n + kWarps - 1) / kWarps);
     if (grid <= 0) return CGL_ECUDA;
     return launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, stream, a) == cudaSuccess ? CGL_OK : CGL_ECUDA;
@@ -240,9 +671,10 @@ cgl_status launch_route(const RouteArgs &a, cudaStream_t stream) {
 cgl_status launch_route_backward(const float *gw, const void *logits, int dtype, const int32_t *idx, int64_t n, int E, int k,
                                  int score, bool renorm, float scale, void *grad, uint32_t *status, cudaStream_t stream) {
     if (n == 0) return CGL_OK;
-    const auto kernel = dtype == CGL_BF16 ? route_backward_kernel<CGL_BF16>
-                        : dtype == CGL_F16 ? route_backward_kernel<CGL_F16> : route_backward_kernel<CGL_F32>;
-    const size_t smem = (size_t)kWarps * E * 4;   // at most 32 KiB
+    const bool vec = E % 8 == 0 && ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(grad)) & 15) == 0;
+    const auto kernel = reinterpret_cast<void (*)(const float *, const void *, const int32_t *, int64_t, int, int, int, bool, float, void *, uint32_t *)>(
+        dtype == CGL_BF16 ? backward_by_width<CGL_BF16>(E, vec) : dtype == CGL_F16 ? backward_by_width<CGL_F16>(E, vec) : backward_by_width<CGL_F32>(E, vec));
+    const size_t smem = (size_t)kWarps * ((E + 7) / 8 * 8) * 4;   // at most 32 KiB
     const int grid = persistent_grid((const void *)kernel, kThreads, smem, 8, 0, (n + kWarps - 1) / kWarps);
     if (grid <= 0) return CGL_ECUDA;
     return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, gw, logits, idx, n, E, k, score, renorm, scale, grad,
