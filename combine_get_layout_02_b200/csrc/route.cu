@@ -228,6 +228,13 @@ __device__ __forceinline__ float rcp(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The same of a 16-bit value, which `f` holds.
+template <int DT>
+__device__ __forceinline__ uint32_t ordered16(float f) {
+    const uint32_t u = DT == CGL_F16 ? __half_as_ushort(__float2half_rn(f)) : __float_as_uint(f) >> 16;
+    return u ^ (u & 0x8000u ? 0xFFFFu : 0x8000u);
+}
+
 // A lane's V neighbouring logits, VEC in pieces of eight.
 template <int DT, int V, bool VEC>
 struct Row {
@@ -245,6 +252,43 @@ struct Row {
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (lane * V + i < E) one[i] = logit<DT>(row, lane * V + i);
+        }
+    }
+    // Whether one is not a number.
+    __device__ __forceinline__ bool nan(int E, int lane) const {
+        bool bad = false;
+        if (VEC) {
+            constexpr uint32_t kAbs = DT == CGL_F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu, kInf = DT == CGL_F16 ? 0x7C00u : 0x7F80u;
+#pragma unroll
+            for (int c = 0; c < V / 8; ++c) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int h = 0; h < (DT == CGL_F32 ? 2 : 1); ++h) {
+                    const uint4 q = raw[c][h];
+                    if (DT == CGL_F32) m = max(m, max(max(q.x & kAbs, q.y & kAbs), max(q.z & kAbs, q.w & kAbs)));
+                    else m = __vmaxu2(__vmaxu2(q.x & kAbs, q.y & kAbs), __vmaxu2(q.z & kAbs, q.w & kAbs));
+                }
+                const bool hit = DT == CGL_F32 ? m > 0x7F800000u : (m >> 16) > kInf || (m & 0xFFFFu) > kInf;
+                bad = bad || (hit && lane * V + 8 * c < E);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) bad = bad || (lane * V + i < E && one[i] != one[i]);
+        }
+        return bad;
+    }
+    // The keys of 16-bit logits: their order above, code - i below.
+    __device__ __forceinline__ void keys(uint32_t key[V], int E, int lane, uint32_t code) const {
+#pragma unroll
+        for (int c = 0; c < (VEC ? V / 8 : 0); ++c) {
+            const uint32_t w[4] = {raw[c][0].x, raw[c][0].y, raw[c][0].z, raw[c][0].w};
+            const bool there = lane * V + 8 * c < E;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t minus = ((w[i] >> 15) & 0x00010001u) * 0xFFFFu, x = there ? w[i] ^ (minus | 0x80008000u) : 0u;
+                key[8 * c + 2 * i] = __byte_perm(x, code - 8 * c - 2 * i, 0x1054);       // the low half's
+                key[8 * c + 2 * i + 1] = __byte_perm(x, code - 8 * c - 2 * i - 1, 0x3254);
+            }
         }
     }
     __device__ __forceinline__ void widen(float l[V], int E, int lane) const {
@@ -298,12 +342,12 @@ __device__ __forceinline__ uint32_t head(const uint32_t k[V]) {
     return m;
 }
 template <int V>
-__device__ __forceinline__ void pop(uint32_t k[V], uint32_t top) {   // keys are unique
+__device__ __forceinline__ void pop(uint32_t k[V], uint32_t top, int deep) {   // keys are unique; deep: how many are still of use
     if (V <= 8) {
         if (k[0] == top) {
 #pragma unroll
-            for (int i = 0; i + 1 < V; ++i) k[i] = k[i + 1];
-            k[V - 1] = 0;
+            for (int i = 0; i < V; ++i)
+                if (i < deep) k[i] = i + 1 < V ? k[i + 1] : 0u;
         }
     } else {
 #pragma unroll
@@ -311,65 +355,102 @@ __device__ __forceinline__ void pop(uint32_t k[V], uint32_t top) {   // keys are
     }
 }
 
-// Keys hold the choice's first 32 - B bits and, below, B bits that put lower indexes
-// first; 0 cannot be picked.  Where what is cut off, or the choice's own rounding,
-// could change the order (`near`: between neighbours of the order down to the first
-// that is not picked), the candidates are compared again in binary64, all of them in
-// lanes: one value a lane and not a whole row.
-template <int DT, int V, bool VEC>
-__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2)
+// Keys hold the choice's first bits and, below, B bits that put lower indexes first.
+// 16-bit logits without a bias are whole in their keys, of binary32 ones 32 - B bits
+// are.  Choices with a bias lie between the least bias and the largest plus 1: they
+// are held as parts of that range, 2^-23 of it (2^-22 past 256 experts), which near 1
+// is finer than as many bits of a binary32 number.  Where what is cut off, or the
+// choice's own rounding, could change the order (`near`: between neighbours of the
+// order down to the first that is not picked), the candidates are compared again in
+// binary64, all of them in lanes: one value a lane and not a whole row.  A NaN is
+// found by its bits.
+enum Kind { kPlain, kBias, kGroups };   // kGroups: with a bias or without
+
+template <int DT, int V, bool VEC, int K, int KIND>
+__global__ void __launch_bounds__(kThreads, V > 8 ? 2 : KIND == kGroups ? 3 : 4)
 route_kernel(const RouteArgs a) {
     constexpr int B = V <= 8 ? 8 : 10;
     constexpr uint32_t kLow = (1u << B) - 1;
     __shared__ uint32_t s_group[kWarps][2][32];   // groups that do not fill whole lanes: their two largest keys
     griddep_wait();
-    const int lane = threadIdx.x & 31, E = a.E, k = a.k, warp = threadIdx.x >> 5;
-    const bool biased = a.bias != nullptr, softmax = a.score == CGL_SCORE_SOFTMAX, whole = softmax && (biased || !a.renorm || (a.groups > 1 && a.by == CGL_GROUP_TOP2));
-    // what a choice may be off by: of itself what is cut off (none in 16 bits), and 2^-20 where it was computed
+    const int lane = threadIdx.x & 31, E = a.E, k = K > 0 ? K : a.k, warp = threadIdx.x >> 5;
+    const bool biased = KIND == kBias || (KIND == kGroups && a.bias != nullptr), groups = KIND == kGroups, softmax = a.score == CGL_SCORE_SOFTMAX;
+    const bool whole = softmax && (biased || (groups && a.by == CGL_GROUP_TOP2));   // the softmax's sum before the choice
     const bool exact = DT != CGL_F32 && !biased;
-    const float cut = __uint_as_float((127 - 22 + B) << 23), slack = biased ? 0x1p-19f : 0.0f;
-    const int per = E / a.groups, lanes = per / V;   // lanes a group
+    // biases: their range, +infinity or NaN among them (the whole order in binary64), -infinity (never picked)
+    float bias[V], from = 0.0f, unit = 0.0f, scale = 0.0f, slack = 0.0f;
+    bool odd_bias = false;
+    if (biased) {
+        float least = INFINITY, most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            bias[i] = lane * V + i < E ? __ldg(a.bias + lane * V + i) : -INFINITY;
+            odd_bias = odd_bias || !(bias[i] < INFINITY);
+            if (fabsf(bias[i]) < INFINITY) least = fminf(least, bias[i]), most = fmaxf(most, bias[i]);
+        }
+        least = -warp_max(-least), most = warp_max(most);
+        const float range = most - least + 1.125f;
+        odd_bias = __any_sync(kAll, odd_bias) || !(range < 0x1p60f && range > 0.0f);
+        from = least - 0.0625f * range, unit = 1.125f * range * 0x1p-23f, scale = 1.0f / unit;
+        // what a choice may be off by: its score and sum (2^-21, and a half step of the sum), its place in the range
+        slack = 0x1p-20f + 0x1p-22f * (fabsf(from) + range) + (B > 8 ? 2.0f : 1.0f) * unit;
+    }
+    const float cut = biased ? 0.0f : __uint_as_float((127 - 22 + B) << 23);   // binary32 logits: what is cut off, of their size
+    const uint32_t code = kLow - lane * V;           // less i: the low bits of the lane's i-th key
+    const uint32_t prefix = exact ? 0xFFFF0000u : ~kLow;
+    const uint32_t least = biased ? 0u : exact && DT == CGL_F16 ? 0x03FF0000u : 0x007FFFFFu & prefix;   // of -infinity
+    const auto live = [&](uint32_t key) { return (key & prefix) > least; };
+    const auto value_of = [&](uint32_t key) {
+        if (DT == CGL_F16 && exact) return __half2float(__ushort_as_half((unsigned short)((key >> 16) ^ (key >> 31 ? 0x8000u : 0xFFFFu))));
+        const float f = unordered(key & prefix);   // exact: below 16 bits a negative value's are ones
+        return biased ? fmaf((float)(key >> 9), unit, from) : exact ? __uint_as_float(__float_as_uint(f) & 0xFFFF0000u) : f;
+    };
+    const int per = KIND != kGroups ? E : E / a.groups, lanes = per / V;   // lanes a group
     const bool filled = per % V == 0 && (lanes & (lanes - 1)) == 0;
     const int size = k <= 8 ? 4 : 16;                // shuffles over the picks
     const int64_t step = (int64_t)gridDim.x * kWarps;
     const size_t row_bytes = (size_t)E * (DT == CGL_F32 ? 4 : 2);
-    float bias[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) bias[i] = biased && lane * V + i < E ? __ldg(a.bias + lane * V + i) : 0.0f;
     int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+    const char *row = static_cast<const char *>(a.logits) + t * row_bytes;
+    int place = (int)(t * k) + lane;                 // of the lane's slot
     Row<DT, V, VEC> ahead;
-    if (t < a.n) ahead.load(static_cast<const char *>(a.logits) + t * row_bytes, E, lane);
-    for (; t < a.n; t += step) {
-        const char *row = static_cast<const char *>(a.logits) + t * row_bytes;
-        float l[V];
-        ahead.widen(l, E, lane);
+    if (t < a.n) ahead.load(row, E, lane);
+    for (; t < a.n; t += step, row += step * row_bytes, place += (int)(step * k)) {
+        uint32_t key[V];
+        float l[V], top = -INFINITY, sum = 1.0f;
+        bool bad = ahead.nan(E, lane);
+        if (VEC && DT != CGL_F32 && exact) ahead.keys(key, E, lane, code);
+        else ahead.widen(l, E, lane);
         if (t + step < a.n) ahead.load(row + step * row_bytes, E, lane);
-        bool bad = false;
-        float top = -INFINITY, sum = 1.0f;
+        bad = __any_sync(kAll, bad);
         if (whole) {
+            if (VEC && DT != CGL_F32 && exact) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) l[i] = live(key[i]) ? value_of(key[i]) : -INFINITY;
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
             top = warp_max(top);
-            bad = top == INFINITY;
-            const float m = top == -INFINITY ? 0.0f : top;
+            top = top == -INFINITY ? 0.0f : top;
             sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += ex2((l[i] - m) * kLog2e);
+            for (int i = 0; i < V; ++i) sum += ex2((l[i] - top) * kLog2e);
             sum = warp_sum(sum);
-            top = m;
         }
         const float inv = rcp(sum);
         const auto score = [&](float x) { return softmax ? ex2((x - top) * kLog2e) * inv : rcp(1.0f + ex2(-x * kLog2e)); };
-        uint32_t key[V];
+        if (biased) {   // 2^23 + a number below 2^23: its bits are the place in the range
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float c = biased ? score(l[i]) + bias[i] : l[i];
-            bad = bad || l[i] != l[i] || (l[i] > -INFINITY && c != c) || (softmax && l[i] == INFINITY);
-            key[i] = l[i] > -INFINITY && c > -INFINITY ? (ordered(c) & ~kLow) | (kLow - (lane * V + i)) : 0u;
+            for (int i = 0; i < V; ++i) {
+                const float c = fmaf(score(l[i]) + bias[i] - from, scale, 0x1p23f);
+                key[i] = l[i] > -INFINITY && bias[i] > -INFINITY ? ((__float_as_uint(c) << 9) & ~kLow) | (code - i) : 0u;
+            }
+        } else if (!(VEC && DT != CGL_F32 && exact)) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = exact ? (ordered16<DT>(l[i]) << 16) | (code - i) : (ordered(l[i]) & ~kLow) | (code - i);
         }
-        bad = __any_sync(kAll, bad);
-        bool again = false;        // the whole token in binary64
-        if (a.groups > 1) {
+        bool again = odd_bias;     // the whole token in binary64
+        if (groups) {
             uint32_t first, second;   // a group's two largest keys, in its lanes, or in lane g that of group g
             int g = lane, stride = 1;
             if (filled) {
@@ -393,28 +474,32 @@ route_kernel(const RouteArgs a) {
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (key[i] != 0) atomicMax(&s_group[warp][0][(lane * V + i) / per], key[i]);
+                    if (live(key[i])) atomicMax(&s_group[warp][0][(lane * V + i) / per], key[i]);
                 __syncwarp();
+                if (a.by == CGL_GROUP_TOP2) {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (key[i] != 0 && key[i] != s_group[warp][0][(lane * V + i) / per]) atomicMax(&s_group[warp][1][(lane * V + i) / per], key[i]);
-                __syncwarp();
+                    for (int i = 0; i < V; ++i)
+                        if (live(key[i]) && key[i] != s_group[warp][0][(lane * V + i) / per]) atomicMax(&s_group[warp][1][(lane * V + i) / per], key[i]);
+                    __syncwarp();
+                }
                 first = s_group[warp][0][lane], second = s_group[warp][1][lane];
+                __syncwarp();
             }
-            const bool real = g < a.groups && first != 0;
+            const bool real = g < a.groups && live(first), two = live(second);
+            if (softmax && !whole) top = warp_max(real ? value_of(first) : -INFINITY);   // +infinity, if there is one
             // the group's value, and what it may be off by
             float value = -INFINITY, off = 0.0f;
             if (real) {
-                const float x = unordered(first & ~kLow), y = unordered(second & ~kLow);
+                const float x = value_of(first), y = two ? value_of(second) : 0.0f;
                 if (a.by == CGL_GROUP_MAX) {
                     value = x;
                     off = exact ? 0.0f : slack + cut * fabsf(x);
                 } else if (biased) {
-                    value = second != 0 ? x + y : x;
-                    off = 2 * slack + cut * (fabsf(x) + (second != 0 ? fabsf(y) : 0.0f));
+                    value = x + y;
+                    off = 2 * slack;
                 } else {
-                    value = score(x) + (second != 0 ? score(y) : 0.0f);
-                    off = 0x1p-18f + (exact ? 0.0f : cut * (fabsf(x) + (second != 0 ? fabsf(y) : 0.0f)));   // a score's slope is below 1
+                    value = score(x) + (two ? score(y) : 0.0f);
+                    off = 0x1p-18f + (exact ? 0.0f : cut * (fabsf(x) + fabsf(y)));   // a score's slope is below 1
                 }
             }
             int rank = 0;
@@ -441,37 +526,47 @@ route_kernel(const RouteArgs a) {
         } else {
             sort_keys<V>(key);
         }
-        uint32_t mine = 0, last = 0;     // lane j: the j-th key; last: the one behind the k-th
-        int found = 0;
-        for (; found <= k; ++found) {
-            const uint32_t m = __reduce_max_sync(kAll, head<V>(key));
-            if (lane == found) mine = m;
-            last = m;
-            pop<V>(key, m);
-        }
-        if (!exact && !bad && !again) {
+        uint32_t mine = 0;         // lane j: the j-th key
+        if (K > 0 && exact) {      // lists as deep as the picks to come
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                const uint32_t m = __reduce_max_sync(kAll, head<V>(key));
+                if (lane == j) mine = m;
+                if (j + 1 < K) pop<V>(key, m, K - 1 - j);
+            }
+        } else {
+            uint32_t last = 0;     // the one behind the k-th
+            int found = 0;
+#pragma unroll
+            for (int j = 0; j <= (K > 0 ? K : k); ++j, ++found) {
+                const uint32_t m = __reduce_max_sync(kAll, head<V>(key));
+                if (lane == j) mine = m;
+                last = m;
+                pop<V>(key, m, V);
+            }
             uint32_t next = __shfl_down_sync(kAll, mine, 1);
             if (lane == 31) next = last;
-            const float x = unordered(mine & ~kLow), y = unordered(next & ~kLow);
+            const float x = value_of(mine), y = value_of(next);
             const float margin = 2 * slack + cut * fmaxf(fabsf(x), fabsf(y));
-            const bool near = lane < k && next != 0 && (biased ? !(x - y > margin) : (mine & ~kLow) == (next & ~kLow));
-            if (__any_sync(kAll, near)) {
+            const bool near = !exact && lane < k && live(next) && (biased ? !(x - y > margin) : (mine & prefix) == (next & prefix));
+            if (__any_sync(kAll, near) && !bad) {
                 // candidates: down to the first that is surely behind the k-th, at most 32
-                const float kth = unordered(__shfl_sync(kAll, mine, k - 1) & ~kLow);
+                const uint32_t border = __shfl_sync(kAll, mine, k - 1);
+                const float kth = value_of(border);
                 found = k;
                 bool more = true;
                 while (true) {
-                    const float z = unordered(last & ~kLow);
-                    more = last != 0 && (biased ? !(kth - z > 2 * slack + cut * fmaxf(fabsf(kth), fabsf(z))) : z == kth);
+                    const float z = value_of(last);
+                    more = live(last) && (biased ? !(kth - z > 2 * slack + cut * fmaxf(fabsf(kth), fabsf(z))) : (last & prefix) == (border & prefix));
                     if (!more || found == 32) break;
                     if (lane == found) mine = last;
                     ++found;
                     last = __reduce_max_sync(kAll, head<V>(key));
-                    pop<V>(key, last);
+                    pop<V>(key, last, V);
                 }
-                again = more;
+                again = again || more;
                 if (!again) {
-                    const bool there = lane < found && mine != 0;
+                    const bool there = lane < found && live(mine);
                     const int e = there ? (int)(kLow - (mine & kLow)) : E;
                     double v = -INFINITY, norm = 1.0;
                     if (biased && softmax) {
@@ -501,19 +596,34 @@ route_kernel(const RouteArgs a) {
                 }
             }
         }
-        int e = lane < k && mine != 0 ? (int)(kLow - (mine & kLow)) : -1;
+        if (softmax) {
+            if (!whole && !groups) top = value_of(__shfl_sync(kAll, mine, 0));
+            bad = bad || top == INFINITY;
+            if (!a.renorm && !whole) {
+                Row<DT, V, VEC> present;
+                present.load(row, E, lane);             // from L1
+                present.widen(l, E, lane);
+                top = l[0];
+#pragma unroll
+                for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+                top = warp_max(top);
+                top = top == -INFINITY ? 0.0f : top;
+                sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum += ex2((l[i] - top) * kLog2e);
+                sum = warp_sum(sum);
+            }
+        }
+        int e = lane < k && live(mine) ? (int)(kLow - (mine & kLow)) : -1;
         if (again && !bad) bad = !pick_exact<DT>(a, row, e);
         const bool there = !bad && e >= 0;
         const float x = there ? logit<DT>(row, e) : -INFINITY;
         float w;
-        if (softmax && !a.renorm) {
-            w = there ? expf(x - top) / sum : 0.0f;
-        } else {
-            w = share(a.score, a.renorm, there, x, size);
-        }
+        if (softmax && !a.renorm) w = there ? expf(x - top) * rcp(sum) : 0.0f;
+        else w = share(a.score, a.renorm, there, x, size);
         if (lane < k) {
-            a.idx[t * k + lane] = there ? e : -1;
-            a.weights[t * k + lane] = bad ? NAN : there ? a.scale * w : 0.0f;
+            a.idx[place] = there ? e : -1;
+            a.weights[place] = bad ? NAN : there ? a.scale * w : 0.0f;
         }
         if (bad && lane == 0) report(a.status, kErrRange);
     }
@@ -641,13 +751,19 @@ route_backward_kernel(const float *__restrict__ gw, const void *__restrict__ log
     }
 }
 
+template <int DT, int KIND>
+void *route_by_width(int E, int k, bool vec) {
+    if (E <= 32) return (void *)route_kernel<DT, 1, false, 0, KIND>;
+    if (E <= 128) return k == 8 ? (void *)route_kernel<DT, 4, false, 8, KIND> : (void *)route_kernel<DT, 4, false, 0, KIND>;
+    if (E <= 256 && vec) return k == 8 ? (void *)route_kernel<DT, 8, true, 8, KIND> : (void *)route_kernel<DT, 8, true, 0, KIND>;
+    if (E <= 256) return (void *)route_kernel<DT, 8, false, 0, KIND>;
+    if (E <= 512) return vec ? (void *)route_kernel<DT, 16, true, 0, KIND> : (void *)route_kernel<DT, 16, false, 0, KIND>;
+    return vec ? (void *)route_kernel<DT, 32, true, 0, KIND> : (void *)route_kernel<DT, 32, false, 0, KIND>;
+}
 template <int DT>
-void *route_by_width(int E, bool vec) {
-    if (E <= 32) return (void *)route_kernel<DT, 1, false>;
-    if (E <= 128) return (void *)route_kernel<DT, 4, false>;
-    if (E <= 256) return vec ? (void *)route_kernel<DT, 8, true> : (void *)route_kernel<DT, 8, false>;
-    if (E <= 512) return vec ? (void *)route_kernel<DT, 16, true> : (void *)route_kernel<DT, 16, false>;
-    return vec ? (void *)route_kernel<DT, 32, true> : (void *)route_kernel<DT, 32, false>;
+void *route_by_kind(const RouteArgs &a, bool vec) {
+    return a.groups > 1 ? route_by_width<DT, kGroups>(a.E, a.k, vec)
+           : a.bias != nullptr ? route_by_width<DT, kBias>(a.E, a.k, vec) : route_by_width<DT, kPlain>(a.E, a.k, vec);
 }
 template <int DT>
 void *backward_by_width(int E, bool vec) {
@@ -660,9 +776,9 @@ void *backward_by_width(int E, bool vec) {
 cgl_status launch_route(const RouteArgs &a, cudaStream_t stream) {
     if (a.n == 0) return CGL_OK;
     const bool vec = a.E % 8 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
-    const auto kernel = reinterpret_cast<void (*)(RouteArgs)>(a.dtype == CGL_BF16  ? route_by_width<CGL_BF16>(a.E, vec)
-                                                              : a.dtype == CGL_F16 ? route_by_width<CGL_F16>(a.E, vec)
-                                                                                   : route_by_width<CGL_F32>(a.E, vec));
+    const auto kernel = reinterpret_cast<void (*)(RouteArgs)>(a.dtype == CGL_BF16  ? route_by_kind<CGL_BF16>(a, vec)
+                                                              : a.dtype == CGL_F16 ? route_by_kind<CGL_F16>(a, vec)
+                                                                                   : route_by_kind<CGL_F32>(a, vec));
     const int grid = persistent_grid((const void *)kernel, kThreads, 0, 8, 0, (a.n + kWarps - 1) / kWarps);
     if (grid <= 0) return CGL_ECUDA;
     return launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, stream, a) == cudaSuccess ? CGL_OK : CGL_ECUDA;
