@@ -32,6 +32,8 @@
 // 0.15 s to land before either block leaves, TMEM is freed.
 #include <cuda.h>
 
+#include <mutex>
+
 #include "matmul_bf16.cuh"
 #include "launch.h"
 
@@ -48,6 +50,7 @@ constexpr int kStageC = 64;                // values of c a stage
 constexpr int kM = 128;                    // features a block
 constexpr int kMaxNt = 256;                // 2 accumulators of 256 columns fill TMEM
 constexpr int kMaxStages = 12;
+constexpr int kBand = 8;                   // tiles of rows
 constexpr int kOutBytes = kEpilogue * 2048;   // the epilogue's 32 x 32 BF16 blocks, one a warp
 constexpr size_t kSmemLimit = 226 * 1024;  // dynamic part: 227 KiB less the static part
 constexpr uint32_t kXBytes = kM * kStageC * 2;
@@ -314,9 +317,20 @@ struct Tiles {
                 rows0 = row0s[e];
                 stop = rows0 + counts[e];
             }
-            row0 = rows0 + (q - begin) * per;
+            // An expert's tiles in bands of kBand tiles of rows, a band's tiles of features one
+            // after the other: the pairs at work at one time share the weights of few features
+            // and the rows of one band, rather than all weights and two tiles of rows.
+            int row = q - begin, m = mt;
+            if (end - begin > 1) {
+                const int i = row * mtiles + mt, band = i / (kBand * mtiles), j = i - band * kBand * mtiles;
+                const int high = end - begin - band * kBand < kBand ? end - begin - band * kBand : kBand;
+                m = j / high;
+                row = band * kBand + j - m * high;
+            }
+            row0 = rows0 + row * per;
+            f0 = (2 * m + rank) * kFeatures;
         }
-        f0 = (2 * mt + rank) * kFeatures;
+        if (MODE == kGradW) f0 = (2 * mt + rank) * kFeatures;
         n = stop - row0 < per ? stop - row0 : per;
     }
     __device__ __forceinline__ int columns() const { return (n + 15) & ~15; }
@@ -488,7 +502,10 @@ __device__ __forceinline__ void store_tile(const Params &p, const Tiles<MODE> &t
                 for (int j = 0; j < 32; ++j) r[j / 16][j % 16] *= sigmoid(r[j / 16][j % 16]);
             } else if (p.act == CGL_ACT_GELU) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) r[j / 16][j % 16] *= normal_cdf(r[j / 16][j % 16]);
+                for (int j = 0; j < 32; ++j) {
+                    float bell;
+                    r[j / 16][j % 16] *= normal_cdf(r[j / 16][j % 16], bell);
+                }
             }
             if (p.residual != nullptr) {
 #pragma unroll
@@ -805,6 +822,34 @@ bool make_map(CUtensorMap *map, const void *p, int rank, const int64_t *dims, co
                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How many clusters of `size` blocks run at once (0 on error); asked once for each size and kernel, with
+// all the shared memory a block may have: these blocks come one to an SM whatever they take.
+int clusters_at_once(const void *kernel, int size, size_t smem) {
+    static std::mutex mu;
+    static struct { const void *kernel; int device, size, n; } seen[64];
+    static int count = 0;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lk(mu);
+    for (int i = 0; i < count; ++i)
+        if (seen[i].kernel == kernel && seen[i].device == device && seen[i].size == size) return seen[i].n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+    if (count < 64) seen[count++] = {kernel, device, size, n};
+    return n;
+}
+
 // Grid, ring and split for `most` tiles (at least as many as there are) of `steps` stages, then the launch.
 template <int MODE>
 cgl_status launch(Params &p, const CUtensorMap &map_x, const CUtensorMap &map_y, int64_t most, int64_t steps, int num_sms,
@@ -821,12 +866,14 @@ cgl_status launch(Params &p, const CUtensorMap &map_x, const CUtensorMap &map_y,
     if (sms <= 0) return CGL_ECUDA;
     int64_t pairs = (num_sms > 0 && num_sms < sms ? num_sms : sms) / 2;
     if (pairs < 1) pairs = 1;
-    // Where `most` tiles would leave three quarters or half of the pairs without work,
-    // four or two pairs share one, a part of c each, as long as each has four stages
-    // and their sums fit into the first pair's ring.
+    // Where there are few tiles, up to four pairs share one, a part of c each, as long as
+    // each has four stages, all clusters run at once and the sums fit into the first
+    // pair's ring.  One row, 7168 -> 4096, 16 tiles: as 32 blocks 26 us, 64 18.3, 96 (three
+    // pairs) XX; of clusters of eight 15 fit, so that with four pairs one runs behind the others, 26.
     p.split = 1;
-    for (int split = 4; split > 1 && p.split == 1; split /= 2)
-        if (most * split <= pairs && steps >= 4 * split && (split - 1) * part_bytes(p.nt) <= (uint32_t)p.stages * p.stage_bytes)
+    for (int split = 4; split > 1 && p.split == 1; --split)
+        if (most * split <= pairs && steps >= 4 * split && (split - 1) * part_bytes(p.nt) <= (uint32_t)p.stages * p.stage_bytes &&
+            most <= clusters_at_once((const void *)kernel, 2 * split, smem))
             p.split = split;
     if (pairs > most) pairs = most;
     cudaLaunchConfig_t cfg = {};
@@ -852,7 +899,9 @@ int64_t token_tiles(Params &p, const MatmulArgs &m, int features) {
     const int64_t mean = (m.rows + m.E - 1) / m.E, want = m.cap > 0 ? m.cap : m.off == nullptr ? mean : mean + mean / 4 + 8;
     p.nt = want >= kMaxNt ? kMaxNt : want <= 32 ? 32 : (int)((want + 15) / 16 * 16);
     p.box = p.nt > 128 ? 32 : p.nt > 64 ? 16 : 8;
-    return ((m.rows + p.nt - 1) / p.nt + (m.off == nullptr ? 0 : m.rows < m.E ? m.rows : m.E)) * ((p.M + features - 1) / features);
+    // no more tiles of rows than with a row in each expert and the others in whole tiles
+    const int64_t some = m.rows < m.E ? m.rows : m.E;
+    return (some + (m.rows - some) / p.nt) * ((p.M + features - 1) / features);
 }
 
 Params params(const MatmulArgs &m) {

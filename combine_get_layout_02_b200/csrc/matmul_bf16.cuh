@@ -16,8 +16,26 @@ __device__ __forceinline__ float sigmoid(float z) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
 }
-// The normal distribution function; erfc keeps it exact where it is near 0.
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.70710678118654752f * z); }
+// The normal distribution function and, in `bell`, e^(-z^2 / 2).  For z <= 0 it is
+// half erfc(|z| / sqrt(2)) = half e^(-z^2 / 2) t p(t) with t = 1 / (1 + 0.375 |z| / sqrt(2)):
+// p of degree 6, fitted to e^(x^2) erfc(x) / t over x in [0, 10] for the least relative
+// error (6.4e-7).  So the far negative side, where the function is near 0, stays exact
+// in relation to it (2.4e-6 down to -6, from the rounded exponent).  erfcf took 40 us
+// more of 300 (8192 rows, 2048 -> 7168).
+__device__ __forceinline__ float normal_cdf(float z, float &bell) {
+    float t;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.26516504f, fabsf(z), 1.0f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(bell) : "f"(-0.72134752f * z * z));
+    float p = -0.06754669576f;
+    p = fmaf(p, t, 0.19396447858f);
+    p = fmaf(p, t, -0.06479228701f);
+    p = fmaf(p, t, 0.14152602816f);
+    p = fmaf(p, t, 0.08333421921f);
+    p = fmaf(p, t, 0.10784417987f);
+    p = fmaf(p, t, 0.10566975951f);
+    const float half = p * t * bell;
+    return z > 0.0f ? 1.0f - half : half;
+}
 __device__ __forceinline__ float relu(float z) { return z > 0.0f || z != z ? z : 0.0f; }   // NaN stays
 
 // Rows [r0, r0 + m) of expert e.  `bad`: offsets that run backwards or out of the

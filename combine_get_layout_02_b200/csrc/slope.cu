@@ -15,7 +15,7 @@ namespace cgl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPiece = 128;
+constexpr int kPiece = 64;
 
 __host__ __device__ __forceinline__ int pieces_of(int rows) { return (int)(((uint32_t)rows + kPiece - 1) / kPiece); }
 
@@ -54,7 +54,11 @@ __device__ __forceinline__ void store8(uint16_t *p, bool vec, int n, const float
 // The activation's derivative.
 __device__ __forceinline__ float slope(float z, int act) {
     if (act == CGL_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    if (act == CGL_ACT_GELU) return normal_cdf(z) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+    if (act == CGL_ACT_GELU) {
+        float bell;
+        const float cdf = normal_cdf(z, bell);
+        return cdf + 0.39894228f * bell * z;
+    }
     const float s = sigmoid(z);
     return s * (1.0f + z * (1.0f - s));
 }
