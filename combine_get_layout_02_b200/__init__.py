@@ -746,6 +746,13 @@ def _choice(value, names, what: str) -> int:
     return names[value]
 
 
+def _rows(t: Optional[torch.Tensor], name: str, n: int, cols: int, dtype, like: torch.Tensor) -> torch.Tensor:
+    """_buf for [n, cols]; its allocation takes 1.5 us of a small call's 10, new_empty 2, torch.empty 2.4."""
+    if t is None:
+        return torch.empty_strided((n, cols), (cols, 1), dtype=dtype, device=like.device)
+    return _buf(t, name, (n, cols), dtype, like)
+
+
 class Routing(NamedTuple):
     topk_idx: torch.Tensor       # int32 [N, k], best first; -1: no expert left
     topk_weights: torch.Tensor   # fp32 [N, k]
@@ -771,14 +778,15 @@ def route(logits: torch.Tensor, num_topk: int, *, bias: Optional[torch.Tensor] =
     n, E = logits.shape
     if bias is not None:
         _buf(_dev(bias, "bias", torch.float32), "bias", (E,), torch.float32, logits)
-    _same(logits.device, status=status)
-    how = _choice(score, _SCORES, "score"), _choice(group_score, _GROUP_SCORES, "group_score")
+    if status is not None:
+        _same(logits.device, status=status)
+    kind, by = _choice(score, _SCORES, "score"), _choice(group_score, _GROUP_SCORES, "group_score")
     if not 1 <= num_topk <= min(E, 32):
         raise CglError(EINVAL, "route", "num_topk must be in [1, min(E, 32)]")
-    topk_idx = _buf(topk_idx, "topk_idx", (n, num_topk), torch.int32, logits)
-    topk_weights = _buf(topk_weights, "topk_weights", (n, num_topk), torch.float32, logits)
-    _launch("cgl_route", lib().cgl_route, logits.device, _ptr(logits), dt, n, E, num_topk, _ptr(bias), num_groups, topk_groups,
-            how[1], how[0], bool(renormalize), float(scale), _ptr(topk_idx), _ptr(topk_weights), _ptr(status))
+    topk_idx = _rows(topk_idx, "topk_idx", n, num_topk, torch.int32, logits)
+    topk_weights = _rows(topk_weights, "topk_weights", n, num_topk, torch.float32, logits)
+    _launch("cgl_route", lib().cgl_route, logits.device, logits.data_ptr(), dt, n, E, num_topk, _ptr(bias), num_groups, topk_groups,
+            by, kind, bool(renormalize), scale, topk_idx.data_ptr(), topk_weights.data_ptr(), _ptr(status))
     return Routing(topk_idx, topk_weights)
 
 
@@ -799,9 +807,9 @@ def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: t
         raise ValueError(f"topk_idx and grad_weights [{n}, k] expected, got {tuple(idx.shape)}, {tuple(g.shape)}")
     _same(logits.device, topk_idx=idx, grad_weights=g, status=status)
     kind = _choice(score, _SCORES, "score")
-    grad_logits = _buf(grad_logits, "grad_logits", (n, E), logits.dtype, logits)
-    _launch("cgl_route_backward", lib().cgl_route_backward, logits.device, _ptr(g), _ptr(logits), dt, _ptr(idx), n, E,
-            idx.shape[1], kind, bool(renormalize), float(scale), _ptr(grad_logits), _ptr(status))
+    grad_logits = _rows(grad_logits, "grad_logits", n, E, logits.dtype, logits)
+    _launch("cgl_route_backward", lib().cgl_route_backward, logits.device, g.data_ptr(), logits.data_ptr(), dt, idx.data_ptr(), n, E,
+            idx.shape[1], kind, bool(renormalize), scale, grad_logits.data_ptr(), _ptr(status))
     return grad_logits
 
 
@@ -836,7 +844,7 @@ def _preact(t, shape, like):
     dtype = t.dtype if isinstance(t, torch.Tensor) else torch.float32
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"preact must be float32 or bfloat16, got {dtype}")
-    return _buf(t, "preact", shape, dtype, like), _DTYPES[dtype]
+    return _rows(t, "preact", *shape, dtype, like), _DTYPES[dtype]
 
 
 def _given(t, name: str, shape, dtype, like):
@@ -865,7 +873,7 @@ def matmul_bf16(a: torch.Tensor, w: torch.Tensor, expert_offset: Optional[torch.
     if bias is not None:
         _given(bias, "bias", (out,) if flat else (E, out), torch.bfloat16, a)
     _given(residual, "residual", (rows, cols), torch.bfloat16, a)
-    y = _buf(y, "y", (rows, cols), torch.bfloat16, a)
+    y = _rows(y, "y", rows, cols, torch.bfloat16, a)
     keep = with_preact or preact is not None
     preact, kind = _preact(preact, (rows, out), a) if keep else (None, 0)
     _launch("cgl_matmul_bf16", lib().cgl_matmul_bf16, a.device, _ptr(a), rows, _ptr(w), E, out, K, _ptr(expert_offset), _ptr(bias),
@@ -907,7 +915,7 @@ def matmul_bf16_backward(grad_y: torch.Tensor, a: torch.Tensor, w: torch.Tensor,
     for name, t, want in (("grad_a", grad_a, want_a), ("grad_w", grad_w, want_w), ("grad_bias", grad_bias, want_bias)):
         if t is not None and not want:
             raise ValueError(f"{name} was given but is not wanted")
-    grad_a = _buf(grad_a, "grad_a", (rows, K), bf16, a) if want_a else None
+    grad_a = _rows(grad_a, "grad_a", rows, K, bf16, a) if want_a else None
     grad_w = _buf(grad_w, "grad_w", (*lead, out, K), bf16, a) if want_w else None
     grad_bias = _buf(grad_bias, "grad_bias", (*lead, out), bf16, a) if want_bias else None
     if workspace is None:

@@ -72,7 +72,7 @@ struct OccEntry {
     size_t smem;
     int ctas;
 };
-OccEntry g_occ[64];
+OccEntry g_occ[256];
 int g_occ_n = 0;
 }  // namespace
 
@@ -93,7 +93,7 @@ int persistent_grid(const void *kernel, int threads, size_t smem, int target_per
             if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, threads, smem) != cudaSuccess)
                 return 0;
             if (fit < 1) fit = 1;
-            if (g_occ_n < 64) g_occ[g_occ_n++] = {kernel, dev, threads, smem, fit};
+            if (g_occ_n < 256) g_occ[g_occ_n++] = {kernel, dev, threads, smem, fit};
         }
     }
     int per_sm = target_per_sm < fit ? target_per_sm : fit;

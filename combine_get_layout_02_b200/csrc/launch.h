@@ -150,6 +150,7 @@ struct RouteArgs {
     int32_t *idx;
     float *weights;
     uint32_t *status;
+    int batch = 1;   // tokens a warp takes together (set by launch_route)
 };
 cgl_status launch_route(const RouteArgs &a, cudaStream_t stream);
 cgl_status launch_route_backward(const float *grad_weights, const void *logits, int dtype, const int32_t *idx, int64_t n,

@@ -27,6 +27,19 @@ __device__ __forceinline__ void put(void *p, int64_t i, float v) {
     else static_cast<__half *>(p)[i] = __float2half_rn(v);
 }
 
+// Sixteen bytes of neighbours: four binary32 or eight 16-bit values.
+template <int DT>
+__device__ __forceinline__ uint4 pack(const float *v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (DT == CGL_F32) w[i] = __float_as_uint(v[i]);
+        else if (DT == CGL_BF16) w[i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
+        else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
@@ -407,21 +420,35 @@ route_kernel(const RouteArgs a) {
     };
     const int per = KIND != kGroups ? E : E / a.groups, lanes = per / V;   // lanes a group
     const bool filled = per % V == 0 && (lanes & (lanes - 1)) == 0;
+    const bool pairs = groups && a.by == CGL_GROUP_TOP2;
+    const int group = filled && groups ? lane / lanes : lane;   // whose value this lane holds
     const int size = k <= 8 ? 4 : 16;                // shuffles over the picks
-    const int64_t step = (int64_t)gridDim.x * kWarps;
+    uint32_t packed[(V + 3) / 4] = {};               // the groups of the lane's experts, a byte each
+    if (groups && !filled)
+#pragma unroll
+        for (int i = 0; i < V; ++i) packed[i / 4] |= (uint32_t)((lane * V + i) / per & 31) << (8 * (i % 4));
+    const auto group_of = [&](int i) { return (packed[i / 4] >> (8 * (i % 4))) & 31; };
+    // A warp takes `batch` tokens after one another and then, eight lanes a token, their weights at once.
+    const int batch = KIND == kGroups ? 1 : a.batch;   // one with groups, whose registers leave no room (16384 x 256 19.3 us, with the loop 22.2)
+    const int64_t step = (int64_t)gridDim.x * kWarps * batch;
     const size_t row_bytes = (size_t)E * (DT == CGL_F32 ? 4 : 2);
-    int64_t t = (int64_t)blockIdx.x * kWarps + warp;
-    const char *row = static_cast<const char *>(a.logits) + t * row_bytes;
-    int place = (int)(t * k) + lane;                 // of the lane's slot
+    const char *const logits = static_cast<const char *>(a.logits);
+    int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * batch;
     Row<DT, V, VEC> ahead;
-    if (t < a.n) ahead.load(row, E, lane);
-    for (; t < a.n; t += step, row += step * row_bytes, place += (int)(step * k)) {
+    if (t0 < a.n) ahead.load(logits + t0 * row_bytes, E, lane);
+    for (; t0 < a.n; t0 += step) {
+      int picked = -1, failed = 0;       // of this lane's slot; failed: a bit a token
+      float row_top = 0.0f, row_sum = 1.0f;
+#pragma unroll 1
+      for (int q = 0; q < batch && t0 + q < a.n; ++q) {
+        const char *row = logits + (t0 + q) * row_bytes;
         uint32_t key[V];
         float l[V], top = -INFINITY, sum = 1.0f;
         bool bad = ahead.nan(E, lane);
         if (VEC && DT != CGL_F32 && exact) ahead.keys(key, E, lane, code);
         else ahead.widen(l, E, lane);
-        if (t + step < a.n) ahead.load(row + step * row_bytes, E, lane);
+        const int64_t then = q + 1 < batch && t0 + q + 1 < a.n ? t0 + q + 1 : t0 + step;
+        if (then < a.n) ahead.load(logits + then * row_bytes, E, lane);
         bad = __any_sync(kAll, bad);
         if (whole) {
             if (VEC && DT != CGL_F32 && exact) {
@@ -451,76 +478,72 @@ route_kernel(const RouteArgs a) {
         }
         bool again = odd_bias;     // the whole token in binary64
         if (groups) {
-            uint32_t first, second;   // a group's two largest keys, in its lanes, or in lane g that of group g
-            int g = lane, stride = 1;
+            uint32_t first, second = 0;   // a group's two largest keys, in its lanes, or in lane g that of group g
             if (filled) {
                 if (V <= 8) {
                     sort_keys<V>(key);
                     first = key[0];
                     second = V > 1 ? key[V > 1] : 0u;
                 } else {
-                    first = second = 0;
+                    first = 0;
 #pragma unroll
                     for (int i = 0; i < V; ++i) second = max(second, min(first, key[i])), first = max(first, key[i]);
                 }
                 for (int o = 1; o < lanes; o <<= 1) {
-                    const uint32_t u = __shfl_xor_sync(kAll, first, o), v = __shfl_xor_sync(kAll, second, o);
-                    second = max(min(first, u), max(second, v));
+                    const uint32_t u = __shfl_xor_sync(kAll, first, o);
+                    if (pairs) second = max(min(first, u), max(second, __shfl_xor_sync(kAll, second, o)));
                     first = max(first, u);
                 }
-                g = lane / lanes, stride = lanes;
             } else {
                 s_group[warp][0][lane] = s_group[warp][1][lane] = 0;
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (live(key[i])) atomicMax(&s_group[warp][0][(lane * V + i) / per], key[i]);
+                    if (live(key[i])) atomicMax(&s_group[warp][0][group_of(i)], key[i]);
                 __syncwarp();
-                if (a.by == CGL_GROUP_TOP2) {
+                if (pairs) {
 #pragma unroll
                     for (int i = 0; i < V; ++i)
-                        if (live(key[i]) && key[i] != s_group[warp][0][(lane * V + i) / per]) atomicMax(&s_group[warp][1][(lane * V + i) / per], key[i]);
+                        if (live(key[i]) && key[i] != s_group[warp][0][group_of(i)]) atomicMax(&s_group[warp][1][group_of(i)], key[i]);
                     __syncwarp();
                 }
                 first = s_group[warp][0][lane], second = s_group[warp][1][lane];
                 __syncwarp();
             }
-            const bool real = g < a.groups && live(first), two = live(second);
-            if (softmax && !whole) top = warp_max(real ? value_of(first) : -INFINITY);   // +infinity, if there is one
+            const bool real = group < a.groups && live(first), two = live(second);
             // the group's value, and what it may be off by
-            float value = -INFINITY, off = 0.0f;
-            if (real) {
-                const float x = value_of(first), y = two ? value_of(second) : 0.0f;
-                if (a.by == CGL_GROUP_MAX) {
-                    value = x;
-                    off = exact ? 0.0f : slack + cut * fabsf(x);
-                } else if (biased) {
-                    value = x + y;
-                    off = 2 * slack;
-                } else {
-                    value = score(x) + (two ? score(y) : 0.0f);
-                    off = 0x1p-18f + (exact ? 0.0f : cut * (fabsf(x) + fabsf(y)));   // a score's slope is below 1
-                }
+            const float x = value_of(first), y = two ? value_of(second) : 0.0f;
+            float value = x, off = slack + cut * fabsf(x);
+            if (pairs && biased) {
+                value = x + y;
+                off = 2 * slack;
+            } else if (pairs) {
+                value = score(x) + (two ? score(y) : 0.0f);
+                off = 0x1p-18f + cut * (fabsf(x) + fabsf(y));   // a score's slope is below 1
             }
-            int rank = 0;
-            for (int i = 0; i < a.groups; ++i) {
-                const float v = __shfl_sync(kAll, value, i * stride);
-                rank += v > value || (v == value && i < g);
+            if (softmax && !whole) top = __any_sync(kAll, real && x == INFINITY) ? INFINITY : 0.0f;
+            // the best by their values' keys, whose last five bits are the group's number
+            const uint32_t mine = real ? (ordered(value) & ~31u) | (31 - group) : 0u;
+            uint32_t left = mine, worst = 0;
+            for (int r = 0; r < a.keep; ++r) {
+                const uint32_t m = __reduce_max_sync(kAll, left);
+                if (m != 0) worst = m;
+                if (left == m) left = 0;
             }
-            const bool kept = real && rank < a.keep;
-            const float low = -warp_max(kept ? off - value : -INFINITY), high = warp_max(real && !kept ? value + off : -INFINITY);
-            // exact values that are equal stand in the order of their groups; an order that their errors could change is looked at again
-            const bool unsure = high > -INFINITY && !(exact && a.by == CGL_GROUP_MAX) && !(low > high);
+            bool kept = real && mine >= worst;
+            const uint32_t best = __reduce_max_sync(kAll, left);   // of those that go
+            if (best != 0 && !(exact && !pairs)) {   // 16-bit values are exact: equal ones stand in the order of their groups
+                const float p = unordered(worst & ~31u), q = unordered(best & ~31u);
+                const float far = 2.0f * __uint_as_float(__reduce_max_sync(kAll, real ? __float_as_uint(off) : 0u)) + 0x1p-17f * fmaxf(fabsf(p), fabsf(q));
+                if (!(p - q > far) && !bad) kept = (groups_exact<DT>(a, row) >> (group & 31)) & 1;
+            }
             if (filled) {
-                bool stays = kept;
-                if (unsure && !bad) stays = (groups_exact<DT>(a, row) >> (g & 31)) & 1;
 #pragma unroll
-                for (int i = 0; i < V; ++i) key[i] = stays ? key[i] : 0u;
+                for (int i = 0; i < V; ++i) key[i] = kept ? key[i] : 0u;
             } else {
-                uint32_t open = __ballot_sync(kAll, kept);
-                if (unsure && !bad) open = groups_exact<DT>(a, row);
+                const uint32_t open = __ballot_sync(kAll, kept);
 #pragma unroll
-                for (int i = 0; i < V; ++i) key[i] = (open >> ((lane * V + i) / per)) & 1 ? key[i] : 0u;
+                for (int i = 0; i < V; ++i) key[i] = (open >> group_of(i)) & 1 ? key[i] : 0u;
                 sort_keys<V>(key);
             }
         } else {
@@ -616,91 +639,109 @@ route_kernel(const RouteArgs a) {
         }
         int e = lane < k && live(mine) ? (int)(kLow - (mine & kLow)) : -1;
         if (again && !bad) bad = !pick_exact<DT>(a, row, e);
-        const bool there = !bad && e >= 0;
-        const float x = there ? logit<DT>(row, e) : -INFINITY;
-        float w;
-        if (softmax && !a.renorm) w = there ? expf(x - top) * rcp(sum) : 0.0f;
-        else w = share(a.score, a.renorm, there, x, size);
-        if (lane < k) {
-            a.idx[place] = there ? e : -1;
-            a.weights[place] = bad ? NAN : there ? a.scale * w : 0.0f;
-        }
-        if (bad && lane == 0) report(a.status, kErrRange);
+        failed |= (int)bad << q;
+        const int other = batch > 1 ? __shfl_sync(kAll, e, lane & 7) : e;
+        if (batch == 1 || lane >> 3 == q) picked = other, row_top = top, row_sum = sum;
+      }
+      const int q = batch > 1 ? lane >> 3 : 0, slot = batch > 1 ? lane & 7 : lane;
+      const int64_t t = t0 + q;
+      const bool bad = (failed >> q) & 1, there = !bad && picked >= 0;
+      const float x = there ? logit<DT>(logits + t * row_bytes, picked) : -INFINITY;
+      float w;
+      if (softmax && !a.renorm) w = there ? expf(x - row_top) * rcp(row_sum) : 0.0f;
+      else w = share(a.score, a.renorm, there, x, size);
+      if (slot < k && q < batch && t < a.n) {
+          a.idx[t * k + slot] = there ? picked : -1;
+          a.weights[t * k + slot] = bad ? NAN : there ? a.scale * w : 0.0f;
+      }
+      if (failed != 0 && lane == 0) report(a.status, kErrRange);
     }
 }
 
 // ---- the gradient --------------------------------------------------------------------------------
 
-// V neighbouring experts a lane, in pieces of eight (VEC), or experts lane, lane + 32, ...
-template <int DT, int V, bool VEC>
-__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2)
+// A warp takes four tokens of up to eight slots at once (T 4, up to 256 experts), eight
+// lanes a token for what the slots need, or one token (T 1).  A lane writes 8 C experts,
+// neighbours in pieces of 16 bytes with the lanes' pieces side by side (VEC), or experts
+// lane, lane + 32, ...
+template <int DT, int T, int C, bool VEC>
+__global__ void __launch_bounds__(kThreads, C == 1 ? 4 : 2)
 route_backward_kernel(const float *__restrict__ gw, const void *__restrict__ logits, const int32_t *__restrict__ idx, int64_t n,
                       int E, int k, int score, bool renorm, float scale, void *__restrict__ grad, uint32_t *status) {
-    extern __shared__ __align__(16) float s_rows[];   // a row of the picks' gradients a warp, zero between tokens
+    extern __shared__ __align__(16) float s_rows[];   // T rows of the picks' gradients a warp, zero between tokens
     griddep_wait();
-    const int lane = threadIdx.x & 31, pitch = (E + 7) / 8 * 8, size = k <= 8 ? 4 : 16;
-    float *s = s_rows + (threadIdx.x >> 5) * pitch;
-    for (int i = lane; i < pitch; i += 32) s[i] = 0.0f;
+    const int lane = threadIdx.x & 31, pitch = (E + 7) / 8 * 8, size = T > 1 || k <= 8 ? 4 : 16;
+    const int q = T > 1 ? lane >> 3 : 0, slot = T > 1 ? lane & 7 : lane;   // this lane's token and slot
+    float *const rows = s_rows + (threadIdx.x >> 5) * T * pitch, *const mine = rows + q * pitch;
+    for (int i = lane; i < T * pitch; i += 32) rows[i] = 0.0f;
     __syncwarp();
-    const int64_t step = (int64_t)gridDim.x * kWarps;
+    const int64_t step = (int64_t)gridDim.x * kWarps * T;
     const size_t row_bytes = (size_t)E * (DT == CGL_F32 ? 4 : 2);
+    const char *const base = static_cast<const char *>(logits);
     const bool whole = score == CGL_SCORE_SOFTMAX && !renorm;
-    int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const auto expert = [&](int i) { return VEC ? (i / 8 * 32 + lane) * 8 + i % 8 : lane + 32 * i; };
-    Row<DT, 8, VEC> ahead[V / 8];
-    const auto load = [&](int64_t t) {
-        const char *row = static_cast<const char *>(logits) + t * row_bytes;
-#pragma unroll
-        for (int c = 0; c < V / 8; ++c) {
-            if (VEC) ahead[c].load(row + c * 256 * (DT == CGL_F32 ? 4 : 2), E - c * 256, lane);
-            else
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (expert(8 * c + i) < E) ahead[c].one[VEC ? 0 : i] = logit<DT>(row, expert(8 * c + i));
-        }
-    };
+    constexpr int P = VEC ? (DT == CGL_F32 ? 4 : 8) : 1, N = 8 * C / P;   // experts a piece, pieces a lane
+    const auto expert = [&](int piece) { return (piece * 32 + lane) * P; };
+    int64_t t0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * T;
     int id = -1;
     float g = 0.0f;
-    if (t < n) {
-        if (lane < k) id = __ldg(idx + t * k + lane), g = __ldg(gw + t * k + lane);
-        if (whole) load(t);
-    }
-    for (; t < n; t += step) {
-        const char *row = static_cast<const char *>(logits) + t * row_bytes;
+    if (slot < k && t0 + q < n) id = __ldg(idx + (t0 + q) * k + slot), g = __ldg(gw + (t0 + q) * k + slot);
+    for (; t0 < n; t0 += step) {
+        const int64_t t = t0 + q;
         const int e = id;
         const bool there = e >= 0 && e < E;
-        const float x = there ? logit<DT>(row, e) : -INFINITY, gs = there ? scale * g : 0.0f;
+        const float x = there ? logit<DT>(base + t * row_bytes, e) : -INFINITY, gs = there ? scale * g : 0.0f;
         if (!there && e != -1) report(status, kErrRange);
-        float l[V], m = -INFINITY, sum = 0.0f;
+        uint4 raw[T][VEC ? N : 1];
+        float one[T][VEC ? 1 : N];
         if (whole) {
 #pragma unroll
-            for (int c = 0; c < V / 8; ++c) {
-                if (VEC) ahead[c].widen(l + 8 * c, E - c * 256, lane);
-                else
+            for (int u = 0; u < T; ++u)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) l[8 * c + i] = expert(8 * c + i) < E ? ahead[c].one[VEC ? 0 : i] : -INFINITY;
-            }
+                for (int c = 0; c < N; ++c)
+                    if (t0 + u < n && expert(c) < E) {
+                        const char *row = base + (t0 + u) * row_bytes;
+                        if (VEC) raw[u][VEC ? c : 0] = ld_nc_v4(row + expert(c) * (DT == CGL_F32 ? 4 : 2));
+                        else one[u][VEC ? 0 : c] = logit<DT>(row, expert(c));
+                    }
         }
-        if (t + step < n) {
-            if (lane < k) id = __ldg(idx + (t + step) * k + lane), g = __ldg(gw + (t + step) * k + lane);
-            if (whole) load(t + step);
+        const int64_t then = t + step;
+        id = -1;
+        if (slot < k && then < n) id = __ldg(idx + then * k + slot), g = __ldg(gw + then * k + slot);
+        const auto widen = [&](int u, float l[8 * C]) {
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                const uint4 a = raw[u][VEC ? c : 0];
+                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    float f;
+                    if (!VEC) f = one[u][VEC ? 0 : c];
+                    else if (DT == CGL_F32) f = __uint_as_float(w[i % 4]);
+                    else if (DT == CGL_BF16) f = (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+                    else f = __half2float(__ushort_as_half((unsigned short)((i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu)));
+                    l[P * c + i] = expert(c) < E ? f : -INFINITY;
+                }
+            }
+        };
+        float tops[T], sums[T], top = 0.0f, sum = 1.0f;   // of each row, and of this lane's token
+        if (whole) {
+#pragma unroll
+            for (int u = 0; u < T; ++u) {
+                float l[8 * C], m = -INFINITY, v = 0.0f;
+                widen(u, l);
+#pragma unroll
+                for (int i = 0; i < 8 * C; ++i) m = fmaxf(m, l[i]);
+                m = warp_max(m);
+                m = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                for (int i = 0; i < 8 * C; ++i) v += ex2((l[i] - m) * kLog2e);
+                tops[u] = m, sums[u] = warp_sum(v);
+                if (u == q) top = m, sum = sums[u];
+            }
         }
         float w;
-        if (whole) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
-            m = warp_max(m);
-            m = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                l[i] = ex2((l[i] - m) * kLog2e);
-                sum += l[i];
-            }
-            sum = warp_sum(sum);
-            w = there && x != -INFINITY ? expf(x - m) / sum : 0.0f;   // a NaN stays
-        } else {
-            w = share(score, renorm, there, x, size);
-        }
+        if (whole) w = there && x != -INFINITY ? expf(x - top) / sum : 0.0f;   // a NaN stays
+        else w = share(score, renorm, there, x, size);
         const float dot = picks_sum(there ? gs * w : 0.0f, size);
         float v = w * (renorm ? gs - dot : gs);
         if (score == CGL_SCORE_SIGMOID) {   // 1 - sigmoid
@@ -708,45 +749,55 @@ route_backward_kernel(const float *__restrict__ gw, const void *__restrict__ log
             v *= (x > 0.0f ? z : 1.0f) / (1.0f + z);
         }
         // into their places; an expert that is in two slots, which its slots' numbers show, gets its terms one by one
-        if (there) s[e] = __int_as_float(lane);
+        if (there) mine[e] = __int_as_float(lane);
         __syncwarp();
-        const bool twice = there && __float_as_int(s[e]) != lane;
+        const bool twice = there && __float_as_int(mine[e]) != lane;
         if (__any_sync(kAll, twice)) {
             __syncwarp();
-            if (there) s[e] = 0.0f;
+            if (there) mine[e] = 0.0f;
             __syncwarp();
             for (int j = 0; j < k; ++j) {
-                if (lane == j && there) s[e] += v;
+                if (slot == j && there) mine[e] += v;
                 __syncwarp();
             }
         } else {
             __syncwarp();
-            if (there) s[e] = v;
+            if (there) mine[e] = v;
         }
         __syncwarp();
-        const bool any = __any_sync(kAll, there);
-        const bool spread = whole && any && sum != 0.0f;   // a token without a slot gets 0, whatever its logits
-        const float base = -__shfl_sync(kAll, dot, 0) / sum;
+        const uint32_t any = __ballot_sync(kAll, there);
 #pragma unroll
-        for (int c = 0; c < V / 8; ++c) {
-            float o[8];
-            if (VEC) {
-                if (expert(8 * c) >= E) break;
-                *reinterpret_cast<float4 *>(o) = *reinterpret_cast<const float4 *>(s + expert(8 * c));
-                *reinterpret_cast<float4 *>(o + 4) = *reinterpret_cast<const float4 *>(s + expert(8 * c) + 4);
+        for (int u = 0; u < T; ++u) {
+            if (t0 + u >= n) break;
+            // a token without a slot gets 0, whatever its logits
+            const bool spread = whole && (T > 1 ? (any >> (8 * u)) & 0xFFu : any) != 0 && sums[u] != 0.0f;
+            const float least = -__shfl_sync(kAll, dot, 8 * u) / (whole ? sums[u] : 1.0f);
+            float l[8 * C];
+            if (whole) {
+                widen(u, l);
+#pragma unroll
+                for (int i = 0; i < 8 * C; ++i) l[i] = least * ex2((l[i] - tops[u]) * kLog2e);
+            }
+            const float *s = rows + u * pitch;
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                if (expert(c) >= E) break;
+                float o[P];
+#pragma unroll
+                for (int i = 0; i < P; i += VEC ? 4 : 1) {
+                    if (VEC) *reinterpret_cast<float4 *>(o + i) = *reinterpret_cast<const float4 *>(s + expert(c) + i);
+                    else o[i] = s[expert(c)];
+                }
                 if (spread)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = fmaf(base, l[8 * c + i], o[i]);
-                Vec8<DT>::store(grad, (t * E + expert(8 * c)) >> 3, o);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (expert(8 * c + i) < E)
-                        put<DT>(grad, t * E + expert(8 * c + i), spread ? fmaf(base, l[8 * c + i], s[expert(8 * c + i)]) : s[expert(8 * c + i)]);
+                    for (int i = 0; i < P; ++i) o[i] += l[P * c + i];
+                void *to = static_cast<char *>(grad) + (t0 + u) * row_bytes + expert(c) * (DT == CGL_F32 ? 4 : 2);
+                if (!VEC) put<DT>(to, 0, o[0]);
+                else st_cs_v4(to, pack<DT>(o));
             }
         }
         __syncwarp();
-        if (there) s[e] = 0.0f;
+        if (there) mine[e] = 0.0f;
         __syncwarp();
     }
 }
@@ -766,20 +817,28 @@ void *route_by_kind(const RouteArgs &a, bool vec) {
            : a.bias != nullptr ? route_by_width<DT, kBias>(a.E, a.k, vec) : route_by_width<DT, kPlain>(a.E, a.k, vec);
 }
 template <int DT>
-void *backward_by_width(int E, bool vec) {
-    if (E <= 256) return vec ? (void *)route_backward_kernel<DT, 8, true> : (void *)route_backward_kernel<DT, 8, false>;
-    return vec ? (void *)route_backward_kernel<DT, 32, true> : (void *)route_backward_kernel<DT, 32, false>;
+void *backward_by_width(int E, bool vec, bool four) {
+    if (E <= 256 && vec) return four ? (void *)route_backward_kernel<DT, 4, 1, true> : (void *)route_backward_kernel<DT, 1, 1, true>;
+    if (E <= 256) return four ? (void *)route_backward_kernel<DT, 4, 1, false> : (void *)route_backward_kernel<DT, 1, 1, false>;
+    return vec ? (void *)route_backward_kernel<DT, 1, 4, true> : (void *)route_backward_kernel<DT, 1, 4, false>;
 }
+
+// Tokens a warp takes at once: four where there are enough to keep 32 warps of every
+// SM busy all the same, and up to eight slots.
+constexpr int64_t kFour = 4 * 32 * 148;
 
 }  // namespace
 
-cgl_status launch_route(const RouteArgs &a, cudaStream_t stream) {
+cgl_status launch_route(const RouteArgs &args, cudaStream_t stream) {
+    RouteArgs a = args;
     if (a.n == 0) return CGL_OK;
     const bool vec = a.E % 8 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
     const auto kernel = reinterpret_cast<void (*)(RouteArgs)>(a.dtype == CGL_BF16  ? route_by_kind<CGL_BF16>(a, vec)
                                                               : a.dtype == CGL_F16 ? route_by_kind<CGL_F16>(a, vec)
                                                                                    : route_by_kind<CGL_F32>(a, vec));
-    const int grid = persistent_grid((const void *)kernel, kThreads, 0, 8, 0, (a.n + kWarps - 1) / kWarps);
+    a.batch = a.k <= 8 && a.groups == 1 && a.n >= kFour ? 4 : 1;
+    const int64_t warps = (a.n + a.batch - 1) / a.batch;
+    const int grid = persistent_grid((const void *)kernel, kThreads, 0, 8, 0, (warps + kWarps - 1) / kWarps);
     if (grid <= 0) return CGL_ECUDA;
     return launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, stream, a) == cudaSuccess ? CGL_OK : CGL_ECUDA;
 }
@@ -788,10 +847,14 @@ cgl_status launch_route_backward(const float *gw, const void *logits, int dtype,
                                  int score, bool renorm, float scale, void *grad, uint32_t *status, cudaStream_t stream) {
     if (n == 0) return CGL_OK;
     const bool vec = E % 8 == 0 && ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(grad)) & 15) == 0;
+    const bool four = E <= 256 && k <= 8 && n >= kFour;
     const auto kernel = reinterpret_cast<void (*)(const float *, const void *, const int32_t *, int64_t, int, int, int, bool, float, void *, uint32_t *)>(
-        dtype == CGL_BF16 ? backward_by_width<CGL_BF16>(E, vec) : dtype == CGL_F16 ? backward_by_width<CGL_F16>(E, vec) : backward_by_width<CGL_F32>(E, vec));
-    const size_t smem = (size_t)kWarps * ((E + 7) / 8 * 8) * 4;   // at most 32 KiB
-    const int grid = persistent_grid((const void *)kernel, kThreads, smem, 8, 0, (n + kWarps - 1) / kWarps);
+        dtype == CGL_BF16  ? backward_by_width<CGL_BF16>(E, vec, four)
+        : dtype == CGL_F16 ? backward_by_width<CGL_F16>(E, vec, four)
+                           : backward_by_width<CGL_F32>(E, vec, four));
+    const size_t smem = (size_t)kWarps * (four ? 4 : 1) * ((E + 7) / 8 * 8) * 4;   // at most 32 KiB
+    const int64_t warps = four ? (n + 3) / 4 : n;
+    const int grid = persistent_grid((const void *)kernel, kThreads, smem, 8, 0, (warps + kWarps - 1) / kWarps);
     if (grid <= 0) return CGL_ECUDA;
     return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, gw, logits, idx, n, E, k, score, renorm, scale, grad,
                       status) == cudaSuccess ? CGL_OK : CGL_ECUDA;

@@ -289,6 +289,32 @@ def test_rows_and_tails(n):
             assert torch.equal(cgl.route_backward(g, l.clone(), r.topk_idx, score="sigmoid"), d)
 
 
+@pytest.mark.parametrize("e", [16, 100, 248, 256])
+@pytest.mark.parametrize("kind", ["plain", "bias", "groups"])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+def test_many_tokens(score, renorm, kind, e):
+    """Batches in which a warp takes several tokens at once give what the tokens give in small batches, bit for bit."""
+    for n, k, dtype in ((20_003, 8, "bf16"), (19_001, 5, "f32"), (18_950, 1, "f16")):
+        l, g = _logits(n, e, 7, dtype), _grad(n, k)
+        l[-9:-5] = -torch.inf
+        l[11, 3:] = -torch.inf
+        l[12, 2] = torch.nan
+        how = dict(score=score, renormalize=renorm, scale=1.5)
+        pick = dict(bias=_bias(e) if kind != "plain" else None, **(dict(num_groups=4, topk_groups=2, group_score="top2") if kind == "groups" else {}))
+        st = cgl.new_status()
+        r = cgl.route(l, k, status=st, **pick, **how)
+        assert cgl.status_bits(st) == ["CGL_ERANGE"]
+        idx = r.topk_idx.clone()
+        idx[30, k - 1] = idx[30, 0]               # an expert twice
+        d = cgl.route_backward(g, l, idx, **how)
+        for a, b in ((0, 6000), (6000, 15_000), (15_000, n)):
+            part = cgl.route(l[a:b].contiguous(), k, **pick, **how)
+            assert torch.equal(part.topk_idx, r.topk_idx[a:b])
+            assert torch.equal(part.topk_weights.view(torch.int32), r.topk_weights[a:b].view(torch.int32))
+            dp = cgl.route_backward(g[a:b].contiguous(), l[a:b].contiguous(), idx[a:b].contiguous(), **how)
+            assert torch.equal(dp.view(torch.int16), d[a:b].view(torch.int16))
+
+
 def test_offsets_past_32_bits():
     n, e = 4_300_000, 512                         # 2.2e9 logits
     l = torch.zeros(n, e, dtype=torch.bfloat16, device="cuda")
