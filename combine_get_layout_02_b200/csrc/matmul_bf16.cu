@@ -32,6 +32,7 @@
 // 0.15 s to land before either block leaves, TMEM is freed.
 #include <cuda.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "matmul_bf16.cuh"
@@ -341,9 +342,9 @@ struct Tiles {
 // ---- results ---------------------------------------------------------------------------------
 
 // Another pair's sums of a tile: for each 32 columns and each 32 lanes of TMEM
-// 32 registers, 128 bytes (a lane each) a register.
+// 32 registers, four of them 512 bytes (sixteen a lane).
 __host__ __device__ __forceinline__ uint32_t part_bytes(int nt) { return (uint32_t)((nt + 31) / 32) * (4 * 32 * 32 * 4); }
-__device__ __forceinline__ int part_index(int column, int quarter, int lane) { return ((column / 32) * 4 + quarter) * 1024 + lane; }
+__device__ __forceinline__ int part_index(int column, int quarter, int lane) { return ((column / 32) * 4 + quarter) * 1024 + lane * 4; }
 
 // A warp's share of a tile: 32 lanes of TMEM (`quarter`), every second block of 32 columns.
 template <int MODE>
@@ -360,8 +361,10 @@ __device__ __forceinline__ void dump_tile(const Tiles<MODE> &tile, bool any, uin
         }
         const uint32_t to = part + 4 * part_index(c, quarter, lane);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 128 * j), "r"(r[j / 16][j % 16]) : "memory");
+        for (int j = 0; j < 32; j += 4) {
+            const uint32_t *v = &r[j / 16][j % 16];
+            asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + 128 * j), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+        }
     }
 }
 
@@ -441,7 +444,11 @@ __device__ __forceinline__ void store_tile(const Params &p, const Tiles<MODE> &t
         for (int i = 0; i < parts; ++i) {
             const float *q = part + (size_t)i * (part_bytes(p.nt) / 4) + part_index(c, quarter, lane);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j / 16][j % 16] += q[32 * j];
+            for (int j = 0; j < 32; j += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(q + 32 * j);
+                float *to = &r[j / 16][j % 16];
+                to[0] += v.x, to[1] += v.y, to[2] += v.z, to[3] += v.w;
+            }
         }
         const int token = 8 * (lane >> 4) + (lane & 7), piece = (lane >> 3) & 1;   // this lane's address for (ld|st)matrix
         if (!kSum) {
@@ -829,7 +836,7 @@ int clusters_at_once(const void *kernel, int size, size_t smem) {
     static struct { const void *kernel; int device, size, n; } seen[64];
     static int count = 0;
     int device = 0;
-    if (cudaGetDevice(&device) != cudaSuccess) return 0;
+    if (cudaGetDevice(&device) != cudaSuccess || !ensure_smem_attr(kernel, smem)) return 0;
     std::lock_guard<std::mutex> lk(mu);
     for (int i = 0; i < count; ++i)
         if (seen[i].kernel == kernel && seen[i].device == device && seen[i].size == size) return seen[i].n;
@@ -845,36 +852,72 @@ int clusters_at_once(const void *kernel, int size, size_t smem) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();   // not this launch's
+        return 0;
+    }
     if (count < 64) seen[count++] = {kernel, device, size, n};
     return n;
 }
 
-// Grid, ring and split for `most` tiles (at least as many as there are) of `steps` stages, then the launch.
+int pairs_of(int num_sms) {
+    const int sms = device_sm_count(), n = (num_sms > 0 && num_sms < sms ? num_sms : sms) / 2;
+    return n < 1 ? 1 : n;
+}
+
+// Shared memory for tiles of p.nt columns: the ring's stages, then the rest.
 template <int MODE>
-cgl_status launch(Params &p, const CUtensorMap &map_x, const CUtensorMap &map_y, int64_t most, int64_t steps, int num_sms,
-                  cudaStream_t stream) {
-    const auto kernel = matmul_bf16_kernel<MODE>;
+size_t lay_out(Params &p) {
     const size_t tables = (size_t)(4 * p.E + 1) * 4;
     const int y_rows = MODE == kGradW ? (p.nt / 2 + 63) / 64 * 64 : (p.nt / 2 + p.box - 1) / p.box * p.box;
     p.stage_bytes = kXBytes + y_rows * (kStageC * 2);
-    int stages = (int)((kSmemLimit - 1024 - kOutBytes - tables) / p.stage_bytes);
+    const int stages = (int)((kSmemLimit - 1024 - kOutBytes - tables) / p.stage_bytes);
     p.stages = stages < kMaxStages ? stages : kMaxStages;
-    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + kOutBytes + tables;
+    return 1024 + (size_t)p.stages * p.stage_bytes + kOutBytes + tables;
+}
+
+int box_rows(int nt) { return nt > 128 ? 32 : nt > 64 ? 16 : 8; }
+
+// Columns a tile and pairs that share one (p.nt, p.split), by what the call would take
+// in cycles: waves of tiles, a stage of 512 cycles at 256 columns (the MMAs) and not
+// below 370 (a block's 16 KiB of X from DRAM), 2000 and 10 a column for a tile's
+// epilogue, 1500 and 40 a column for joining pairs' sums.  Narrow tiles read X more
+// often, wide ones leave pairs without work: 2000 rows, 512 -> 512: 64 columns 9.5 us,
+// 256 11.0; 2048 rows, 2048 -> 7168: 113 and 49.  Pairs share a tile where that leaves
+// each four stages, all clusters run at once and the sums fit into the first pair's
+// ring.  `guess` and `most`: tiles of rows of that many columns, as expected and at most.
+template <int MODE, typename Guess, typename Most>
+void plan(Params &p, int widest, int64_t mtiles, int64_t steps, int64_t pairs, Guess guess, Most most) {
+    static const int widths[] = {32, 64, 96, 128, 192, 256};
+    double best = 0;
+    int nt = 0, split = 1;
+    for (int i = -1; i < 6; ++i) {
+        p.nt = i < 0 ? widest : widths[i];
+        if (i >= 0 && p.nt >= widest) break;
+        if (MODE == kGradW && p.nt < 64) continue;
+        if (MODE != kGradW) p.box = box_rows(p.nt);
+        const size_t smem = lay_out<MODE>(p);
+        const double tiles = (double)guess(p.nt) * mtiles;
+        const double stage = 2 * p.nt > 370 + p.nt / 2 ? 2 * p.nt : 370 + p.nt / 2;
+        for (int k = 1; k <= 4; ++k) {
+            if (k > 1 && (most(p.nt) * mtiles * k > pairs || steps < 4 * k || (k - 1) * part_bytes(p.nt) > (uint32_t)p.stages * p.stage_bytes ||
+                          most(p.nt) * mtiles > clusters_at_once((const void *)matmul_bf16_kernel<MODE>, 2 * k, smem)))
+                continue;
+            const double waves = k > 1 ? 1 : std::ceil(tiles / pairs), sums = ((steps + k - 1) / k) * stage, out = 2000 + 10 * p.nt;
+            const double t = waves * (sums > out ? sums : out) + out + (k > 1 ? 1500 + 40 * p.nt : 0);
+            if (nt == 0 || t < best) best = t, nt = p.nt, split = k;
+        }
+    }
+    p.nt = nt, p.split = split;
+    if (MODE != kGradW) p.box = box_rows(nt);
+}
+
+// The launch, for `most` tiles (at least as many as there are).
+template <int MODE>
+cgl_status launch(Params &p, const CUtensorMap &map_x, const CUtensorMap &map_y, int64_t most, int64_t pairs, cudaStream_t stream) {
+    const auto kernel = matmul_bf16_kernel<MODE>;
+    const size_t smem = lay_out<MODE>(p);
     if (!ensure_smem_attr((const void *)kernel, smem)) return CGL_ECUDA;
-    const int sms = device_sm_count();
-    if (sms <= 0) return CGL_ECUDA;
-    int64_t pairs = (num_sms > 0 && num_sms < sms ? num_sms : sms) / 2;
-    if (pairs < 1) pairs = 1;
-    // Where there are few tiles, up to four pairs share one, a part of c each, as long as
-    // each has four stages, all clusters run at once and the sums fit into the first
-    // pair's ring.  One row, 7168 -> 4096, 16 tiles: as 32 blocks 26 us, 64 18.3, 96 (three
-    // pairs) XX; of clusters of eight 15 fit, so that with four pairs one runs behind the others, 26.
-    p.split = 1;
-    for (int split = 4; split > 1 && p.split == 1; --split)
-        if (most * split <= pairs && steps >= 4 * split && (split - 1) * part_bytes(p.nt) <= (uint32_t)p.stages * p.stage_bytes &&
-            most <= clusters_at_once((const void *)kernel, 2 * split, smem))
-            p.split = split;
     if (pairs > most) pairs = most;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs * p.split));
@@ -893,21 +936,29 @@ cgl_status launch(Params &p, const CUtensorMap &map_x, const CUtensorMap &map_y,
     return cudaLaunchKernelEx(&cfg, kernel, map_x, map_y, p) == cudaSuccess ? CGL_OK : CGL_ECUDA;
 }
 
-// Columns a tile, rows a TMA box and the most tiles there can be, for the token side (sizes alone are known here).
-int64_t token_tiles(Params &p, const MatmulArgs &m, int features) {
+// The plan for a product whose rows are the experts' (sizes alone are known here); returns the most tiles there can be.
+template <int MODE>
+int64_t plan_rows(Params &p, const MatmulArgs &m, int64_t pairs) {
     // a quarter over the mean rows of an expert (a padded one's capacity), so that few experts need two tiles
-    const int64_t mean = (m.rows + m.E - 1) / m.E, want = m.cap > 0 ? m.cap : m.off == nullptr ? mean : mean + mean / 4 + 8;
-    p.nt = want >= kMaxNt ? kMaxNt : want <= 32 ? 32 : (int)((want + 15) / 16 * 16);
-    p.box = p.nt > 128 ? 32 : p.nt > 64 ? 16 : 8;
-    // no more tiles of rows than with a row in each expert and the others in whole tiles
-    const int64_t some = m.rows < m.E ? m.rows : m.E;
-    return (some + (m.rows - some) / p.nt) * ((p.M + features - 1) / features);
+    const int64_t mean = (m.rows + m.E - 1) / m.E, want = m.cap > 0 ? m.cap : m.off == nullptr || m.E == 1 ? mean : mean + mean / 4 + 8;
+    const int widest = want >= kMaxNt ? kMaxNt : want <= 32 ? 32 : (int)((want + 15) / 16 * 16);
+    const int64_t mtiles = (p.M + 2 * Tiles<MODE>::kFeatures - 1) / (2 * Tiles<MODE>::kFeatures), some = m.rows < m.E ? m.rows : m.E;
+    const auto guess = [&](int nt) {
+        if (m.cap > 0) return (double)m.E * ((m.cap + nt - 1) / nt);
+        if (some == 1) return (double)((m.rows + nt - 1) / nt);
+        const double each = (double)m.rows / some / nt;
+        return some * (each <= 0.75 ? 1.0 : each + 0.5);
+    };
+    // with a row in each expert and the others in whole tiles
+    const auto most = [&](int nt) { return some + (m.rows - some) / nt; };
+    plan<MODE>(p, widest, mtiles, (p.C + kStageC - 1) / kStageC, pairs, guess, most);
+    return most(p.nt) * mtiles;
 }
 
 Params params(const MatmulArgs &m) {
     Params p = {};
     p.off = m.off, p.status = m.status, p.rows = m.rows, p.cap = m.cap, p.E = m.E;
-    p.N = 1, p.nt = kMaxNt, p.box = 8, p.wait_cycles = m.wait_cycles < 0 || m.wait_cycles > kWaitCycles ? kWaitCycles : m.wait_cycles;
+    p.N = 1, p.wait_cycles = m.wait_cycles < 0 || m.wait_cycles > kWaitCycles ? kWaitCycles : m.wait_cycles;
     return p;
 }
 
@@ -922,7 +973,7 @@ cgl_status launch_matmul_bf16(const MatmulArgs &m, const uint16_t *bias, const u
     Params p = params(m);
     p.bias = bias, p.residual = residual, p.y = y, p.preact = preact, p.preact_wide = preact_f32;
     p.act = m.act, p.M = gated ? m.F / 2 : m.F, p.C = m.K;
-    const int64_t most = token_tiles(p, m, gated ? kM : 2 * kM);
+    const int64_t pairs = pairs_of(m.num_sms), most = gated ? plan_rows<kGated>(p, m, pairs) : plan_rows<kForward>(p, m, pairs);
     p.wide = rows_wide(y, p.M, 2) && rows_wide(residual, p.M, 2) && (preact_f32 || rows_wide(preact, p.M, 2));
     CUtensorMap map_x, map_y;
     const int64_t wd[4] = {m.K, p.M, gated ? 2 : m.E, m.E}, ws[3] = {m.K, (int64_t)p.M * m.K, (int64_t)m.F * m.K};
@@ -930,9 +981,7 @@ cgl_status launch_matmul_bf16(const MatmulArgs &m, const uint16_t *bias, const u
     const int64_t ad[2] = {m.K, m.rows}, as[1] = {m.K};
     const int ab[2] = {kStageC, p.box};
     if (!make_map(&map_x, m.w, gated ? 4 : 3, wd, ws, wb) || !make_map(&map_y, m.a, 2, ad, as, ab)) return CGL_ECUDA;
-    const int64_t steps = (m.K + kStageC - 1) / kStageC;
-    return gated ? launch<kGated>(p, map_x, map_y, most, steps, m.num_sms, stream)
-                 : launch<kForward>(p, map_x, map_y, most, steps, m.num_sms, stream);
+    return gated ? launch<kGated>(p, map_x, map_y, most, pairs, stream) : launch<kForward>(p, map_x, map_y, most, pairs, stream);
 }
 
 cgl_status launch_matmul_bf16_backward(const MatmulArgs &m, const uint16_t *grad_y, const void *preact, bool preact_f32, uint16_t *grad_a,
@@ -942,31 +991,30 @@ cgl_status launch_matmul_bf16_backward(const MatmulArgs &m, const uint16_t *grad
     const cgl_status st = launch_slope(m, grad_y, preact, preact_f32, grad_a != nullptr || grad_w != nullptr, grad_bias, ws, &dz, &ld, stream);
     if (st != CGL_OK) return st;
     CUtensorMap map_x, map_y;
+    const int64_t pairs = pairs_of(m.num_sms);
     if (grad_a != nullptr && m.rows > 0) {
         Params p = params(m);
         p.y = grad_a, p.M = m.K, p.C = m.F;
-        const int64_t most = token_tiles(p, m, 2 * kM);
+        const int64_t most = plan_rows<kGradA>(p, m, pairs);
         p.wide = 1;   // K % 8 == 0, grad_a 16-byte aligned
         const int64_t wd[3] = {m.K, m.F, m.E}, wst[2] = {m.K, (int64_t)m.F * m.K}, zd[2] = {m.F, m.rows};
         const int wb[3] = {64, kStageC, 1}, zb[2] = {kStageC, p.box};
         if (!make_map(&map_x, m.w, 3, wd, wst, wb) || !make_map(&map_y, dz, 2, zd, &ld, zb)) return CGL_ECUDA;
-        const cgl_status r = launch<kGradA>(p, map_x, map_y, most, (m.F + kStageC - 1) / kStageC, m.num_sms, stream);
+        const cgl_status r = launch<kGradA>(p, map_x, map_y, most, pairs, stream);
         if (r != CGL_OK) return r;
     }
     if (grad_w != nullptr) {
         Params p = params(m);
         p.y = grad_w, p.M = m.K, p.N = m.F;
         p.wide = 1;
-        // narrower tiles where there are few, down to 64 columns
-        const int64_t pairs = (m.num_sms > 0 && m.num_sms < device_sm_count() ? m.num_sms : device_sm_count()) / 2;
         const int64_t mtiles = (m.K + 2 * kM - 1) / (2 * kM);
-        const auto tiles = [&] { return mtiles * ((m.F + p.nt - 1) / p.nt) * m.E; };
-        while (p.nt > 64 && 2 * tiles() <= pairs) p.nt /= 2;
+        const auto tiles = [&](int nt) { return (int64_t)m.E * ((m.F + nt - 1) / nt); };
+        plan<kGradW>(p, kMaxNt, mtiles, (m.rows / m.E + kStageC - 1) / kStageC, pairs, tiles, tiles);
         const int64_t rows = m.rows > 0 ? m.rows : 1;   // without rows nothing is loaded, and a map needs one
         const int64_t ad[2] = {m.K, rows}, as[1] = {m.K}, zd[2] = {m.F, rows};
         const int box[2] = {64, kStageC};
         if (!make_map(&map_x, m.rows > 0 ? m.a : m.w, 2, ad, as, box) || !make_map(&map_y, m.rows > 0 ? dz : m.w, 2, zd, &ld, box)) return CGL_ECUDA;
-        return launch<kGradW>(p, map_x, map_y, tiles(), (m.rows / m.E + kStageC - 1) / kStageC, m.num_sms, stream);
+        return launch<kGradW>(p, map_x, map_y, tiles(p.nt) * mtiles, pairs, stream);
     }
     return CGL_OK;
 }
