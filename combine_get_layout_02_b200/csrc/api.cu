@@ -538,4 +538,19 @@ cgl_status cgl_matmul_bf16_backward(const uint16_t *grad_y, const uint16_t *a, i
                                        static_cast<cudaStream_t>(stream));
 }
 
+cgl_status cgl_selftest_matmul_bf16_timeout(int what, const uint16_t *x, int64_t rows, const uint16_t *y_or_w, int F, int K,
+                                            uint16_t *result, int64_t wait_cycles, uint32_t *status_dev, void *stream) {
+    if (what < 0 || what > 2 || F < 8 || F % 8 != 0 || F > (1 << 20) || K < 8 || K % 8 != 0 || K > (1 << 20) || rows < 1 ||
+        rows > (1 << 20) || wait_cycles < 0)
+        return CGL_EINVAL;
+    if (!x || !y_or_w || !result || !status_dev) return CGL_EINVAL;
+    if (!aligned(x, 16) || !aligned(y_or_w, 16) || !aligned(result, 16) || !aligned(status_dev, 4)) return CGL_EALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MatmulArgs m = {what == 1 ? nullptr : x, rows, what == 2 ? nullptr : y_or_w, 1, F, K, nullptr, 0, CGL_ACT_NONE, 0, status_dev, wait_cycles};
+    if (what == 0) return launch_matmul_bf16(m, nullptr, nullptr, result, nullptr, false, s);
+    // without an activation and a bias's gradient the products read grad_y itself: no workspace
+    return launch_matmul_bf16_backward(m, what == 1 ? x : y_or_w, nullptr, false, what == 1 ? result : nullptr,
+                                       what == 2 ? result : nullptr, nullptr, nullptr, s);
+}
+
 }  // extern "C"

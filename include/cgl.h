@@ -690,6 +690,19 @@ cgl_status cgl_matmul_bf16_backward(const uint16_t *grad_y, const uint16_t *a, i
                                     size_t workspace_bytes, const cgl_opts *opts, uint32_t *status_dev,
                                     void *stream);
 
+/*
+ * cgl_selftest_matmul_bf16_timeout -- diagnostic for failure detection, as
+ * cgl_selftest_matmul_timeout: one product for one expert that has every row, with
+ * a limit of wait_cycles SM cycles (at most the usual 2^31) on each wait between
+ * the roles of a block pair.  what 0: x [num_rows, in], y_or_w = w [out, in], result
+ * [num_rows, out]; 1: x = grad_y [num_rows, out], w, result grad_a [num_rows, in];
+ * 2: x = a [num_rows, in], y_or_w = grad_y [num_rows, out], result grad_w [out, in].
+ * All BF16, 16-byte aligned, in and out multiples of 8.
+ */
+cgl_status cgl_selftest_matmul_bf16_timeout(int what, const uint16_t *x, int64_t num_rows, const uint16_t *y_or_w,
+                                            int out_features, int in_features, uint16_t *result,
+                                            int64_t wait_cycles, uint32_t *status_dev, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
