@@ -752,14 +752,15 @@ except ImportError:
     _empty_strided_cuda = None
 
 
-def _rows(t: Optional[torch.Tensor], name: str, n: int, cols: int, dtype, like: torch.Tensor) -> torch.Tensor:
-    """_buf for [n, cols]."""
+def _out(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor) -> torch.Tensor:
+    """_buf, with the short path to the allocator."""
     if t is not None:
-        return _buf(t, name, (n, cols), dtype, like)
+        return _buf(t, name, shape, dtype, like)
+    strides = (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1) if len(shape) == 3 else (1,)
     device = like.device
     if _empty_strided_cuda is None or device.index != torch._C._cuda_getDevice():
-        return torch.empty_strided((n, cols), (cols, 1), dtype=dtype, device=device)
-    return _empty_strided_cuda((n, cols), (cols, 1), dtype)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    return _empty_strided_cuda(shape, strides, dtype)
 
 
 class Routing(NamedTuple):
@@ -792,8 +793,8 @@ def route(logits: torch.Tensor, num_topk: int, *, bias: Optional[torch.Tensor] =
     kind, by = _choice(score, _SCORES, "score"), _choice(group_score, _GROUP_SCORES, "group_score")
     if not 1 <= num_topk <= min(E, 32):
         raise CglError(EINVAL, "route", "num_topk must be in [1, min(E, 32)]")
-    topk_idx = _rows(topk_idx, "topk_idx", n, num_topk, torch.int32, logits)
-    topk_weights = _rows(topk_weights, "topk_weights", n, num_topk, torch.float32, logits)
+    topk_idx = _out(topk_idx, "topk_idx", (n, num_topk), torch.int32, logits)
+    topk_weights = _out(topk_weights, "topk_weights", (n, num_topk), torch.float32, logits)
     _launch("cgl_route", lib().cgl_route, logits.device, logits.data_ptr(), dt, n, E, num_topk, _ptr(bias), num_groups, topk_groups,
             by, kind, bool(renormalize), scale, topk_idx.data_ptr(), topk_weights.data_ptr(), _ptr(status))
     return Routing(topk_idx, topk_weights)
@@ -816,7 +817,7 @@ def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: t
         raise ValueError(f"topk_idx and grad_weights [{n}, k] expected, got {tuple(idx.shape)}, {tuple(g.shape)}")
     _same(logits.device, topk_idx=idx, grad_weights=g, status=status)
     kind = _choice(score, _SCORES, "score")
-    grad_logits = _rows(grad_logits, "grad_logits", n, E, logits.dtype, logits)
+    grad_logits = _out(grad_logits, "grad_logits", (n, E), logits.dtype, logits)
     _launch("cgl_route_backward", lib().cgl_route_backward, logits.device, g.data_ptr(), logits.data_ptr(), dt, idx.data_ptr(), n, E,
             idx.shape[1], kind, bool(renormalize), scale, grad_logits.data_ptr(), _ptr(status))
     return grad_logits
@@ -853,7 +854,7 @@ def _preact(t, shape, like):
     dtype = t.dtype if isinstance(t, torch.Tensor) else torch.float32
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"preact must be float32 or bfloat16, got {dtype}")
-    return _rows(t, "preact", *shape, dtype, like), _DTYPES[dtype]
+    return _out(t, "preact", shape, dtype, like), _DTYPES[dtype]
 
 
 def _given(t, name: str, shape, dtype, like):
@@ -882,7 +883,7 @@ def matmul_bf16(a: torch.Tensor, w: torch.Tensor, expert_offset: Optional[torch.
     if bias is not None:
         _given(bias, "bias", (out,) if flat else (E, out), torch.bfloat16, a)
     _given(residual, "residual", (rows, cols), torch.bfloat16, a)
-    y = _rows(y, "y", rows, cols, torch.bfloat16, a)
+    y = _out(y, "y", (rows, cols), torch.bfloat16, a)
     keep = with_preact or preact is not None
     preact, kind = _preact(preact, (rows, out), a) if keep else (None, 0)
     _launch("cgl_matmul_bf16", lib().cgl_matmul_bf16, a.device, _ptr(a), rows, _ptr(w), E, out, K, _ptr(expert_offset), _ptr(bias),
@@ -918,20 +919,21 @@ def matmul_bf16_backward(grad_y: torch.Tensor, a: torch.Tensor, w: torch.Tensor,
     if act != 0 and preact is None:
         raise ValueError(f"activation {activation!r} needs preact")
     kind = 0 if preact is None else _preact(_dev(preact, "preact"), (rows, out), a)[1]
-    ws_bytes = matmul_bf16_backward_workspace_bytes(rows, E, out, K)
-    if ws_bytes == 0:
-        raise CglError(EINVAL, "matmul_bf16_backward", "invalid sizes")
     for name, t, want in (("grad_a", grad_a, want_a), ("grad_w", grad_w, want_w), ("grad_bias", grad_bias, want_bias)):
         if t is not None and not want:
             raise ValueError(f"{name} was given but is not wanted")
-    grad_a = _rows(grad_a, "grad_a", rows, K, bf16, a) if want_a else None
-    grad_w = _buf(grad_w, "grad_w", (*lead, out, K), bf16, a) if want_w else None
-    grad_bias = _buf(grad_bias, "grad_bias", (*lead, out), bf16, a) if want_bias else None
-    if workspace is None:
-        workspace = a.new_empty(ws_bytes, dtype=torch.uint8)
-    else:
+    grad_a = _out(grad_a, "grad_a", (rows, K), bf16, a) if want_a else None
+    grad_w = _out(grad_w, "grad_w", (*lead, out, K), bf16, a) if want_w else None
+    grad_bias = _out(grad_bias, "grad_bias", (*lead, out), bf16, a) if want_bias else None
+    ws_bytes = 0
+    if workspace is not None:
         _same(a.device, workspace=_dev(workspace, "workspace"))
         ws_bytes = workspace.numel() * workspace.element_size()
+    elif act != 0 or want_bias or out % 8 or grad_y.data_ptr() % 16:   # else the products read grad_y itself
+        ws_bytes = matmul_bf16_backward_workspace_bytes(rows, E, out, K)
+        if ws_bytes == 0:
+            raise CglError(EINVAL, "matmul_bf16_backward", "invalid sizes")
+        workspace = _out(None, "workspace", (ws_bytes,), torch.uint8, a)
     _launch("cgl_matmul_bf16_backward", lib().cgl_matmul_bf16_backward, a.device, _ptr(grad_y), _ptr(a), rows, _ptr(w), E, out, K,
             _ptr(expert_offset), act, _ptr(preact), kind, _ptr(grad_a), _ptr(grad_w), _ptr(grad_bias), _ptr(workspace), ws_bytes,
             _opts(num_sms, capacity), _ptr(status))

@@ -896,16 +896,20 @@ void plan(Params &p, int widest, int64_t mtiles, int64_t steps, int64_t pairs, G
         if (i >= 0 && p.nt >= widest) break;
         if (MODE == kGradW && p.nt < 64) continue;
         if (MODE != kGradW) p.box = box_rows(p.nt);
-        const size_t smem = lay_out<MODE>(p);
-        const double tiles = (double)guess(p.nt) * mtiles;
+        const double tiles = (double)guess(p.nt) * mtiles, out = 2000 + 10 * p.nt;
         const double stage = 2 * p.nt > 370 + p.nt / 2 ? 2 * p.nt : 370 + p.nt / 2;
         for (int k = 1; k <= 4; ++k) {
-            if (k > 1 && (most(p.nt) * mtiles * k > pairs || steps < 4 * k || (k - 1) * part_bytes(p.nt) > (uint32_t)p.stages * p.stage_bytes ||
-                          most(p.nt) * mtiles > clusters_at_once((const void *)matmul_bf16_kernel<MODE>, 2 * k, smem)))
-                continue;
-            const double waves = k > 1 ? 1 : std::ceil(tiles / pairs), sums = ((steps + k - 1) / k) * stage, out = 2000 + 10 * p.nt;
+            if (k > 1 && (tiles * k > pairs || steps < 4 * k)) break;
+            const double waves = k > 1 ? 1 : std::ceil(tiles / pairs), sums = ((steps + k - 1) / k) * stage;
             const double t = waves * (sums > out ? sums : out) + out + (k > 1 ? 1500 + 40 * p.nt : 0);
-            if (nt == 0 || t < best) best = t, nt = p.nt, split = k;
+            if (nt != 0 && t >= best) continue;
+            if (k > 1) {
+                const size_t smem = lay_out<MODE>(p);
+                if (most(p.nt) * mtiles * k > pairs || (k - 1) * part_bytes(p.nt) > (uint32_t)p.stages * p.stage_bytes ||
+                    most(p.nt) * mtiles > clusters_at_once((const void *)matmul_bf16_kernel<MODE>, 2 * k, smem))
+                    break;
+            }
+            best = t, nt = p.nt, split = k;
         }
     }
     p.nt = nt, p.split = split;

@@ -679,7 +679,8 @@ size_t cgl_matmul_bf16_backward_workspace_bytes(int64_t num_rows, int num_expert
  *   BF16 [E, out, in] and grad_bias BF16 [E, out], written in full (0 for experts
  *   without rows).
  * workspace: device, 16-byte aligned, any contents, scratch for the call (calls
- *   that overlap on the GPU must not share one).
+ *   that overlap on the GPU must not share one); may be NULL with CGL_ACT_NONE, out
+ *   % 8 == 0, a 16-byte aligned grad_y and no grad_bias.
  * Sizes, alignment, opts and errors as for cgl_matmul_bf16 (grad_a and grad_w
  * 16-byte aligned).
  */
