@@ -888,13 +888,13 @@ int box_rows(int nt) { return nt > 128 ? 32 : nt > 64 ? 16 : 8; }
 // ring.  `guess` and `most`: tiles of rows of that many columns, as expected and at most.
 template <int MODE, typename Guess, typename Most>
 void plan(Params &p, int widest, int64_t mtiles, int64_t steps, int64_t pairs, Guess guess, Most most) {
-    static const int widths[] = {32, 64, 96, 128, 192, 256};
+    static const int widths[] = {32, 64, 96, 128, 160, 192, 208, 224, 240, 256};
     double best = 0;
     int nt = 0, split = 1;
-    for (int i = -1; i < 6; ++i) {
+    for (int i = -1; i < 10; ++i) {
         p.nt = i < 0 ? widest : widths[i];
         if (i >= 0 && p.nt >= widest) break;
-        if (MODE == kGradW && p.nt < 64) continue;
+        if (MODE == kGradW && p.nt % 64 != 0) continue;   // 64 columns a chunk: others load as many
         if (MODE != kGradW) p.box = box_rows(p.nt);
         const double tiles = (double)guess(p.nt) * mtiles, out = 2000 + 10 * p.nt;
         const double stage = 2 * p.nt > 370 + p.nt / 2 ? 2 * p.nt : 370 + p.nt / 2;
