@@ -845,7 +845,9 @@ def _matmul_args(a, w, expert_offset, activation, status):
         _dev(expert_offset, "expert_offset", torch.int32, 1)
         if expert_offset.shape[0] != E + 1:
             raise ValueError(f"expert_offset must have {E + 1} entries, got {expert_offset.shape[0]}")
-    _same(a.device, w=w, expert_offset=expert_offset, status=status)
+    device = a.device
+    if w.device != device or (expert_offset is not None and expert_offset.device != device) or status is not None:
+        _same(device, w=w, expert_offset=expert_offset, status=status)
     return a, w, act, rows, E, out, K, out // 2 if act == 4 else out
 
 
@@ -858,7 +860,10 @@ def _preact(t, shape, like):
 
 
 def _given(t, name: str, shape, dtype, like):
-    return None if t is None else _buf(_dev(t, name, dtype), name, shape, dtype, like)
+    """An input that may be None: checked."""
+    if t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == like.device and t.is_contiguous()):
+        return t
+    return _buf(_dev(t, name, dtype), name, shape, dtype, like)   # names what is wrong
 
 
 def matmul_bf16(a: torch.Tensor, w: torch.Tensor, expert_offset: Optional[torch.Tensor] = None, capacity: int = 0, *,
@@ -915,7 +920,8 @@ def matmul_bf16_backward(grad_y: torch.Tensor, a: torch.Tensor, w: torch.Tensor,
     flat = isinstance(w, torch.Tensor) and w.dim() == 2
     a, w, act, rows, E, out, K, cols = _matmul_args(a, w, expert_offset, activation, status)
     bf16, lead = torch.bfloat16, () if flat else (E,)
-    _given(_dev(grad_y, "grad_y"), "grad_y", (rows, cols), bf16, a)
+    if _given(grad_y, "grad_y", (rows, cols), bf16, a) is None:
+        raise TypeError("grad_y must be a CUDA tensor")
     if act != 0 and preact is None:
         raise ValueError(f"activation {activation!r} needs preact")
     kind = 0 if preact is None else _preact(_dev(preact, "preact"), (rows, out), a)[1]
