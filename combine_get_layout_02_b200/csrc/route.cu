@@ -377,19 +377,20 @@ __device__ __forceinline__ void pop(uint32_t k[V], uint32_t top, int deep) {   /
 // order down to the first that is not picked), the candidates are compared again in
 // binary64, all of them in lanes: one value a lane and not a whole row.  A NaN is
 // found by its bits.
-enum Kind { kPlain, kBias, kGroups };   // kGroups: with a bias or without
+enum Kind { kPlain, kBias, kGroups, kGroupsBias };
 
 template <int DT, int V, bool VEC, int K, int KIND>
-__global__ void __launch_bounds__(kThreads, V > 8 ? 2 : KIND == kGroups ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, V > 8 ? 2 : KIND >= kGroups ? 3 : 4)
 route_kernel(const RouteArgs a) {
     constexpr int B = V <= 8 ? 8 : 10;
     constexpr uint32_t kLow = (1u << B) - 1;
     __shared__ uint32_t s_group[kWarps][2][32];   // groups that do not fill whole lanes: their two largest keys
     griddep_wait();
     const int lane = threadIdx.x & 31, E = a.E, k = K > 0 ? K : a.k, warp = threadIdx.x >> 5;
-    const bool biased = KIND == kBias || (KIND == kGroups && a.bias != nullptr), groups = KIND == kGroups, softmax = a.score == CGL_SCORE_SOFTMAX;
+    constexpr bool biased = KIND == kBias || KIND == kGroupsBias, groups = KIND >= kGroups;
+    const bool softmax = a.score == CGL_SCORE_SOFTMAX;
     const bool whole = softmax && (biased || (groups && a.by == CGL_GROUP_TOP2));   // the softmax's sum before the choice
-    const bool exact = DT != CGL_F32 && !biased;
+    constexpr bool exact = DT != CGL_F32 && !biased;
     // biases: their range, +infinity or NaN among them (the whole order in binary64), -infinity (never picked)
     float bias[V], from = 0.0f, unit = 0.0f, scale = 0.0f, slack = 0.0f;
     bool odd_bias = false;
@@ -418,7 +419,7 @@ route_kernel(const RouteArgs a) {
         const float f = unordered(key & prefix);   // exact: below 16 bits a negative value's are ones
         return biased ? fmaf((float)(key >> 9), unit, from) : exact ? __uint_as_float(__float_as_uint(f) & 0xFFFF0000u) : f;
     };
-    const int per = KIND != kGroups ? E : E / a.groups, lanes = per / V;   // lanes a group
+    const int per = groups ? E / a.groups : E, lanes = per / V;   // lanes a group
     const bool filled = per % V == 0 && (lanes & (lanes - 1)) == 0;
     const bool pairs = groups && a.by == CGL_GROUP_TOP2;
     const int group = filled && groups ? lane / lanes : lane;   // whose value this lane holds
@@ -429,7 +430,7 @@ route_kernel(const RouteArgs a) {
         for (int i = 0; i < V; ++i) packed[i / 4] |= (uint32_t)((lane * V + i) / per & 31) << (8 * (i % 4));
     const auto group_of = [&](int i) { return (packed[i / 4] >> (8 * (i % 4))) & 31; };
     // A warp takes `batch` tokens after one another and then, eight lanes a token, their weights at once.
-    const int batch = KIND == kGroups ? 1 : a.batch;   // one with groups, whose registers leave no room (16384 x 256 19.3 us, with the loop 22.2)
+    const int batch = groups ? 1 : a.batch;   // one with groups, whose registers leave no room (16384 x 256 19.3 us, with the loop 22.2)
     const int64_t step = (int64_t)gridDim.x * kWarps * batch;
     const size_t row_bytes = (size_t)E * (DT == CGL_F32 ? 4 : 2);
     const char *const logits = static_cast<const char *>(a.logits);
@@ -742,8 +743,18 @@ route_backward_kernel(const float *__restrict__ gw, const void *__restrict__ log
         float w;
         if (whole) w = there && x != -INFINITY ? expf(x - top) / sum : 0.0f;   // a NaN stays
         else w = share(score, renorm, there, x, size);
-        const float dot = picks_sum(there ? gs * w : 0.0f, size);
-        float v = w * (renorm ? gs - dot : gs);
+        float dot = 0.0f, v = w * gs;
+        if (whole) {
+            dot = picks_sum(there ? v : 0.0f, size);
+        } else if (renorm) {
+            // g_j - sum_i g_i w_i as sum_i w_i (g_j - g_i): the weights' sum is 1, and where one is nearly all of it nothing cancels
+            float d = 0.0f;
+            for (int i = 0; i < k; ++i) {
+                const int from = T > 1 ? (lane & ~7) + i : i;
+                d = fmaf(__shfl_sync(kAll, w, from), gs - __shfl_sync(kAll, gs, from), d);
+            }
+            v = w * d;
+        }
         if (score == CGL_SCORE_SIGMOID) {   // 1 - sigmoid
             const float z = expf(-fabsf(x));
             v *= (x > 0.0f ? z : 1.0f) / (1.0f + z);
@@ -813,8 +824,8 @@ void *route_by_width(int E, int k, bool vec) {
 }
 template <int DT>
 void *route_by_kind(const RouteArgs &a, bool vec) {
-    return a.groups > 1 ? route_by_width<DT, kGroups>(a.E, a.k, vec)
-           : a.bias != nullptr ? route_by_width<DT, kBias>(a.E, a.k, vec) : route_by_width<DT, kPlain>(a.E, a.k, vec);
+    if (a.groups > 1) return a.bias != nullptr ? route_by_width<DT, kGroupsBias>(a.E, a.k, vec) : route_by_width<DT, kGroups>(a.E, a.k, vec);
+    return a.bias != nullptr ? route_by_width<DT, kBias>(a.E, a.k, vec) : route_by_width<DT, kPlain>(a.E, a.k, vec);
 }
 template <int DT>
 void *backward_by_width(int E, bool vec, bool four) {
@@ -823,9 +834,11 @@ void *backward_by_width(int E, bool vec, bool four) {
     return vec ? (void *)route_backward_kernel<DT, 1, 4, true> : (void *)route_backward_kernel<DT, 1, 4, false>;
 }
 
-// Tokens a warp takes at once: four where there are enough to keep 32 warps of every
-// SM busy all the same, and up to eight slots.
-constexpr int64_t kFour = 4 * 32 * 148;
+// From so many tokens on a warp takes four at once, up to eight slots each.  256 experts,
+// one at once and four: forward of 4096 BF16 tokens 3.4 and 3.0 us (softmax as it is 3.5 and
+// 3.9), 8192 5.8 and 4.3 (6.0 and 5.3), 65536 32.8 and 23.6; of binary32 ones with a bias 8192
+// 11.3 and 8.8; backward 4096 3.2 and 2.7 (3.1 and 3.7), 8192 5.0 and 3.1 (4.8 and 4.4).
+constexpr int64_t kFour = 8192;
 
 }  // namespace
 
