@@ -201,6 +201,13 @@ __device__ __forceinline__ float picks_max(float v, int size) {
     return v;
 }
 
+// 1 / x, within a step.
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // What lane j's slot has of its token's weight (scale aside), slots without an expert
 // 0: the sigmoid, or with renorm the quotient by the picks' sum (softmax or sigmoid).
 __device__ __forceinline__ float share(int score, bool renorm, bool there, float l, int size) {
@@ -209,14 +216,16 @@ __device__ __forceinline__ float share(int score, bool renorm, bool there, float
     if (score == CGL_SCORE_SIGMOID) {
         // sigmoid(l) exp(-b), b = min(largest l, 0): a factor that all slots share keeps the quotient where every sigmoid underflows
         const float b = fminf(top, 0.0f), z = expf(-fabsf(l));
-        t = (l > 0.0f ? 1.0f : expf(l - b)) / (1.0f + z);
+        t = l > 0.0f ? 1.0f : z;
+        if (__any_sync(kAll, b < 0.0f)) t = l > 0.0f ? 1.0f : expf(l - b);
+        t *= rcp(1.0f + z);
     } else {
         t = expf(l - top);
     }
     if (!there || l == -INFINITY) t = 0.0f;
     if (!renorm) return t;
     const float d = picks_sum(t, size);
-    return d == 0.0f ? 0.0f : t / d;
+    return d == 0.0f ? 0.0f : t * rcp(d);
 }
 
 // ---- the order in binary32, by keys ------------------------------------------------------------
@@ -232,11 +241,6 @@ __device__ __forceinline__ float unordered(uint32_t k) {
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float rcp(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 constexpr float kLog2e = 1.4426950408889634f;
@@ -757,7 +761,7 @@ route_backward_kernel(const float *__restrict__ gw, const void *__restrict__ log
         }
         if (score == CGL_SCORE_SIGMOID) {   // 1 - sigmoid
             const float z = expf(-fabsf(x));
-            v *= (x > 0.0f ? z : 1.0f) / (1.0f + z);
+            v *= (x > 0.0f ? z : 1.0f) * rcp(1.0f + z);
         }
         // into their places; an expert that is in two slots, which its slots' numbers show, gets its terms one by one
         if (there) mine[e] = __int_as_float(lane);
