@@ -23,9 +23,20 @@
 //               shared memory -> BF16 rows, while the next tile's MMAs run; two warps
 //               for each 32 lanes of TMEM, 32 columns in turn
 // A gated product has gate and up features 16 by 16 in the tile's rows, so that both
-// come to the same lane.  Where tiles are few (see the launcher), two or four pairs
-// share one, a part of c each, and join their sums in order through distributed
-// shared memory.
+// come to the same lane.  Where tiles are few (see plan), two to four pairs share one,
+// a part of c each, and join their sums in order through distributed shared memory.
+//
+// What bounds it (B200; floors at the measured 6.55 TB/s copy and 1656 TFLOP/s burst,
+// 1396 sustained).  Few rows an expert, the weights' bytes: 4 rows, 256 experts, 7168 ->
+// 2 x 2048 gated 2.08 ms (7.1 TB/s, the floor 2.26 being that of a copy); 128 rows 2.29 to 2.43
+// ms in short runs (floor 2.39), 2.6 to 3.0 at the 1000 W cap.  Many rows, the tensor cores
+// and in long runs the cap: 8192^3 681 us (1615 TFLOP/s; cuBLAS 671), long 780 to 830 by the card
+// (cuBLAS 750); grad_a and grad_w 780 to 850.  512 rows an expert, 2048 -> 7168, 16 experts:
+// 170 us with the tensor pipe active 77% of the time, 12.1 waves of tiles in 13; a tile of
+// 200 columns takes 71 bytes a cycle and SM from L2, whose ports carry 64.  One row, 7168
+// -> 4096: 17.4 us, 9 of bytes and 5.5 for a call without work.  Sums are binary32, but the
+// tensor cores cut each addition towards zero: 1.5e-6 off (root mean square) for 1520
+// terms whose sum is about 1, where rounded additions are 8e-8 off.
 //
 // Every wait is bounded (about a second, then CGL_ETIMEOUT): the pair's roles leave
 // their loops, MMAs in flight are waited for, copies and arrivals under way get
@@ -393,12 +404,25 @@ __device__ __forceinline__ void move_block(uint8_t *block, uint16_t *base, int64
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) *reinterpret_cast<uint4 *>(block + block_at(kRows * i + lane / PIECES, piece)) = v[i];
     } else if (lane < 8 * PIECES) {
+        // a feature a lane, eight rows in flight
         const int col = column(lane);
+        uint16_t *g = base + col;
         if (col >= 0)
-            for (int row = 0; row < there; ++row) {
-                uint16_t *s = reinterpret_cast<uint16_t *>(block + block_at(row, lane >> 3)) + (lane & 7);
-                if (STORE) base[row * ld + col] = *s;
-                else *s = base[row * ld + col];
+#pragma unroll 1
+            for (int row = 0; row < there; row += 8, g += 8 * ld) {
+                uint16_t v[8] = {};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint16_t *s = reinterpret_cast<uint16_t *>(block + block_at(row + i, lane >> 3)) + (lane & 7);
+                    if (STORE) v[i] = *s;
+                    else if (row + i < there) v[i] = g[i * ld];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint16_t *s = reinterpret_cast<uint16_t *>(block + block_at(row + i, lane >> 3)) + (lane & 7);
+                    if (!STORE) *s = v[i];
+                    else if (row + i < there) g[i * ld] = v[i];
+                }
             }
     }
 }

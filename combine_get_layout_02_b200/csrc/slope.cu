@@ -7,6 +7,8 @@
 // expert, keeps its columns' sums in registers and leaves the piece's in the
 // workspace; a second kernel adds the pieces of each expert in their order.  dz goes
 // out as BF16, which the tensor cores take; the bias's sums take it unrounded.
+// Bound by bytes: 8192 x 7168, GELU, z in binary32, with the bias 98 us (470 MB, 72 us
+// at the copy rate); 32768 x 2 x 2048 gated, sums alone 147 (671 MB, 102).
 #include "matmul_bf16.cuh"
 #include "launch.h"
 
