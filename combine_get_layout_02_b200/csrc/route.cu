@@ -453,198 +453,26 @@ route_kernel(const RouteArgs a) {
     Row<DT, V, VEC> ahead;
     if (t0 < a.n) ahead.load(logits + t0 * row_bytes, E, lane);
     for (; t0 < a.n; t0 += step) {
-      int picked = -1, failed = 0;       // of this lane's slot; failed: a bit a token
-      float row_top = 0.0f, row_sum = 1.0f;
+        int picked = -1, failed = 0;       // of this lane's slot; failed: a bit a token
+        float row_top = 0.0f, row_sum = 1.0f;
 #pragma unroll 1
-      for (int q = 0; q < batch && t0 + q < a.n; ++q) {
-        const char *row = logits + (t0 + q) * row_bytes;
-        uint32_t key[V];
-        float l[V], top = -INFINITY, sum = 1.0f;
-        bool bad = ahead.nan(E, lane);
-        if (VEC && DT != CGL_F32 && exact) ahead.keys(key, E, lane, code);
-        else ahead.widen(l, E, lane);
-        const int64_t then = q + 1 < batch && t0 + q + 1 < a.n ? t0 + q + 1 : t0 + step;
-        if (then < a.n) ahead.load(logits + then * row_bytes, E, lane);
-        bad = __any_sync(kAll, bad);
-        if (whole) {
-            if (VEC && DT != CGL_F32 && exact) {
+        for (int q = 0; q < batch && t0 + q < a.n; ++q) {
+            const char *row = logits + (t0 + q) * row_bytes;
+            uint32_t key[V];
+            float l[V], top = -INFINITY, sum = 1.0f;
+            bool bad = ahead.nan(E, lane);
+            if (VEC && DT != CGL_F32 && exact) ahead.keys(key, E, lane, code);
+            else ahead.widen(l, E, lane);
+            const int64_t then = q + 1 < batch && t0 + q + 1 < a.n ? t0 + q + 1 : t0 + step;
+            if (then < a.n) ahead.load(logits + then * row_bytes, E, lane);
+            bad = __any_sync(kAll, bad);
+            if (whole) {
+                if (VEC && DT != CGL_F32 && exact) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) l[i] = live(key[i]) ? value_of(key[i]) : -INFINITY;
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
-            top = warp_max(top);
-            top = top == -INFINITY ? 0.0f : top;
-            sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum += ex2((l[i] - top) * kLog2e);
-            sum = warp_sum(sum);
-        }
-        const float inv = rcp(sum);
-        const auto score = [&](float x) { return softmax ? ex2((x - top) * kLog2e) * inv : rcp(1.0f + ex2(-x * kLog2e)); };
-        if (biased) {   // 2^23 + a number below 2^23: its bits are the place in the range
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float c = fmaf(score(l[i]) + bias[i] - from, scale, 0x1p23f);
-                key[i] = l[i] > -INFINITY && bias[i] > -INFINITY ? ((__float_as_uint(c) << 9) & ~kLow) | (code - i) : 0u;
-            }
-        } else if (!(VEC && DT != CGL_F32 && exact)) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) key[i] = exact ? (ordered16<DT>(l[i]) << 16) | (code - i) : (ordered(l[i]) & ~kLow) | (code - i);
-        }
-        bool again = odd_bias;     // the whole token in binary64
-        if (groups) {
-            uint32_t first, second = 0;   // a group's two largest keys, in its lanes, or in lane g that of group g
-            if (filled) {
-                if (V <= 8) {
-                    sort_keys<V>(key);
-                    first = key[0];
-                    second = V > 1 ? key[V > 1] : 0u;
-                } else {
-                    first = 0;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) second = max(second, min(first, key[i])), first = max(first, key[i]);
+                    for (int i = 0; i < V; ++i) l[i] = live(key[i]) ? value_of(key[i]) : -INFINITY;
                 }
-                for (int o = 1; o < lanes; o <<= 1) {
-                    const uint32_t u = __shfl_xor_sync(kAll, first, o);
-                    if (pairs) second = max(min(first, u), max(second, __shfl_xor_sync(kAll, second, o)));
-                    first = max(first, u);
-                }
-            } else {
-                s_group[warp][0][lane] = s_group[warp][1][lane] = 0;
-                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (live(key[i])) atomicMax(&s_group[warp][0][group_of(i)], key[i]);
-                __syncwarp();
-                if (pairs) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (live(key[i]) && key[i] != s_group[warp][0][group_of(i)]) atomicMax(&s_group[warp][1][group_of(i)], key[i]);
-                    __syncwarp();
-                }
-                first = s_group[warp][0][lane], second = s_group[warp][1][lane];
-                __syncwarp();
-            }
-            const bool real = group < a.groups && live(first), two = live(second);
-            // the group's value, and what it may be off by
-            const float x = value_of(first), y = two ? value_of(second) : 0.0f;
-            float value = x, off = slack + cut * fabsf(x);
-            if (pairs && biased) {
-                value = x + y;
-                off = 2 * slack;
-            } else if (pairs) {
-                value = score(x) + (two ? score(y) : 0.0f);
-                off = 0x1p-18f + cut * (fabsf(x) + fabsf(y));   // a score's slope is below 1
-            }
-            if (softmax && !whole) top = __any_sync(kAll, real && x == INFINITY) ? INFINITY : 0.0f;
-            // the best by their values' keys, whose last five bits are the group's number
-            const uint32_t mine = real ? (ordered(value) & ~31u) | (31 - group) : 0u;
-            uint32_t left = mine, worst = 0;
-            for (int r = 0; r < a.keep; ++r) {
-                const uint32_t m = __reduce_max_sync(kAll, left);
-                if (m != 0) worst = m;
-                if (left == m) left = 0;
-            }
-            bool kept = real && mine >= worst;
-            const uint32_t best = __reduce_max_sync(kAll, left);   // of those that go
-            if (best != 0 && !(exact && !pairs)) {   // 16-bit values are exact: equal ones stand in the order of their groups
-                const float p = unordered(worst & ~31u), q = unordered(best & ~31u);
-                const float far = 2.0f * __uint_as_float(__reduce_max_sync(kAll, real ? __float_as_uint(off) : 0u)) + 0x1p-17f * fmaxf(fabsf(p), fabsf(q));
-                if (!(p - q > far) && !bad) kept = (groups_exact<DT>(a, row) >> (group & 31)) & 1;
-            }
-            if (filled) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) key[i] = kept ? key[i] : 0u;
-            } else {
-                const uint32_t open = __ballot_sync(kAll, kept);
-#pragma unroll
-                for (int i = 0; i < V; ++i) key[i] = (open >> group_of(i)) & 1 ? key[i] : 0u;
-                sort_keys<V>(key);
-            }
-        } else {
-            sort_keys<V>(key);
-        }
-        uint32_t mine = 0;         // lane j: the j-th key
-        if (K > 0 && exact) {      // lists as deep as the picks to come
-#pragma unroll
-            for (int j = 0; j < K; ++j) {
-                const uint32_t m = __reduce_max_sync(kAll, head<V>(key));
-                if (lane == j) mine = m;
-                if (j + 1 < K) pop<V>(key, m, K - 1 - j);
-            }
-        } else {
-            uint32_t last = 0;     // the one behind the k-th
-            int found = 0;
-#pragma unroll
-            for (int j = 0; j <= (K > 0 ? K : k); ++j, ++found) {
-                const uint32_t m = __reduce_max_sync(kAll, head<V>(key));
-                if (lane == j) mine = m;
-                last = m;
-                pop<V>(key, m, V);
-            }
-            uint32_t next = __shfl_down_sync(kAll, mine, 1);
-            if (lane == 31) next = last;
-            const float x = value_of(mine), y = value_of(next);
-            const float margin = 2 * slack + cut * fmaxf(fabsf(x), fabsf(y));
-            const bool near = !exact && lane < k && live(next) && (biased ? !(x - y > margin) : (mine & prefix) == (next & prefix));
-            if (__any_sync(kAll, near) && !bad) {
-                // candidates: down to the first that is surely behind the k-th, at most 32
-                const uint32_t border = __shfl_sync(kAll, mine, k - 1);
-                const float kth = value_of(border);
-                found = k;
-                bool more = true;
-                while (true) {
-                    const float z = value_of(last);
-                    more = live(last) && (biased ? !(kth - z > 2 * slack + cut * fmaxf(fabsf(kth), fabsf(z))) : (last & prefix) == (border & prefix));
-                    if (!more || found == 32) break;
-                    if (lane == found) mine = last;
-                    ++found;
-                    last = __reduce_max_sync(kAll, head<V>(key));
-                    pop<V>(key, last, V);
-                }
-                again = again || more;
-                if (!again) {
-                    const bool there = lane < found && live(mine);
-                    const int e = there ? (int)(kLow - (mine & kLow)) : E;
-                    double v = -INFINITY, norm = 1.0;
-                    if (biased && softmax) {
-                        norm = 0.0;
-#pragma unroll 1
-                        for (int i = lane; i < E; i += 32) norm += exp((double)logit<DT>(row, i) - (double)top);
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) norm += __shfl_xor_sync(kAll, norm, o);
-                    }
-                    if (there) {
-                        v = (double)logit<DT>(row, e);
-                        if (biased) v = (softmax ? exp(v - (double)top) / norm : 1.0 / (1.0 + exp(-v))) + (double)__ldg(a.bias + e);
-                    }
-                    int rank = 0;
-                    for (int i = 0; i < found; ++i) {
-                        const double u = __shfl_sync(kAll, v, i);
-                        const int j = __shfl_sync(kAll, e, i);
-                        rank += u > v || (u == v && j < e);
-                    }
-                    const uint32_t key_of = there ? mine : 0;
-                    mine = 0;
-                    for (int i = 0; i < found; ++i) {
-                        const int r = __shfl_sync(kAll, rank, i);
-                        const uint32_t q = __shfl_sync(kAll, key_of, i);
-                        if (lane == r && q != 0) mine = q;
-                    }
-                }
-            }
-        }
-        if (softmax) {
-            if (!whole && !groups) top = value_of(__shfl_sync(kAll, mine, 0));
-            bad = bad || top == INFINITY;
-            if (!a.renorm && !whole) {
-                Row<DT, V, VEC> present;
-                present.load(row, E, lane);             // from L1
-                present.widen(l, E, lane);
-                top = l[0];
-#pragma unroll
-                for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+                for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
                 top = warp_max(top);
                 top = top == -INFINITY ? 0.0f : top;
                 sum = 0.0f;
@@ -652,25 +480,197 @@ route_kernel(const RouteArgs a) {
                 for (int i = 0; i < V; ++i) sum += ex2((l[i] - top) * kLog2e);
                 sum = warp_sum(sum);
             }
+            const float inv = rcp(sum);
+            const auto score = [&](float x) { return softmax ? ex2((x - top) * kLog2e) * inv : rcp(1.0f + ex2(-x * kLog2e)); };
+            if (biased) {   // 2^23 + a number below 2^23: its bits are the place in the range
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float c = fmaf(score(l[i]) + bias[i] - from, scale, 0x1p23f);
+                    key[i] = l[i] > -INFINITY && bias[i] > -INFINITY ? ((__float_as_uint(c) << 9) & ~kLow) | (code - i) : 0u;
+                }
+            } else if (!(VEC && DT != CGL_F32 && exact)) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) key[i] = exact ? (ordered16<DT>(l[i]) << 16) | (code - i) : (ordered(l[i]) & ~kLow) | (code - i);
+            }
+            bool again = odd_bias;     // the whole token in binary64
+            if (groups) {
+                uint32_t first, second = 0;   // a group's two largest keys, in its lanes, or in lane g that of group g
+                if (filled) {
+                    if (V <= 8) {
+                        sort_keys<V>(key);
+                        first = key[0];
+                        second = V > 1 ? key[V > 1] : 0u;
+                    } else {
+                        first = 0;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) second = max(second, min(first, key[i])), first = max(first, key[i]);
+                    }
+                    for (int o = 1; o < lanes; o <<= 1) {
+                        const uint32_t u = __shfl_xor_sync(kAll, first, o);
+                        if (pairs) second = max(min(first, u), max(second, __shfl_xor_sync(kAll, second, o)));
+                        first = max(first, u);
+                    }
+                } else {
+                    s_group[warp][0][lane] = s_group[warp][1][lane] = 0;
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (live(key[i])) atomicMax(&s_group[warp][0][group_of(i)], key[i]);
+                    __syncwarp();
+                    if (pairs) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            if (live(key[i]) && key[i] != s_group[warp][0][group_of(i)]) atomicMax(&s_group[warp][1][group_of(i)], key[i]);
+                        __syncwarp();
+                    }
+                    first = s_group[warp][0][lane], second = s_group[warp][1][lane];
+                    __syncwarp();
+                }
+                const bool real = group < a.groups && live(first), two = live(second);
+                // the group's value, and what it may be off by
+                const float x = value_of(first), y = two ? value_of(second) : 0.0f;
+                float value = x, off = slack + cut * fabsf(x);
+                if (pairs && biased) {
+                    value = x + y;
+                    off = 2 * slack;
+                } else if (pairs) {
+                    value = score(x) + (two ? score(y) : 0.0f);
+                    off = 0x1p-18f + cut * (fabsf(x) + fabsf(y));   // a score's slope is below 1
+                }
+                if (softmax && !whole) top = __any_sync(kAll, real && x == INFINITY) ? INFINITY : 0.0f;
+                // the best by their values' keys, whose last five bits are the group's number
+                const uint32_t mine = real ? (ordered(value) & ~31u) | (31 - group) : 0u;
+                uint32_t left = mine, worst = 0;
+                for (int r = 0; r < a.keep; ++r) {
+                    const uint32_t m = __reduce_max_sync(kAll, left);
+                    if (m != 0) worst = m;
+                    if (left == m) left = 0;
+                }
+                bool kept = real && mine >= worst;
+                const uint32_t best = __reduce_max_sync(kAll, left);   // of those that go
+                if (best != 0 && !(exact && !pairs)) {   // 16-bit values are exact: equal ones stand in the order of their groups
+                    const float p = unordered(worst & ~31u), q = unordered(best & ~31u);
+                    const float far = 2.0f * __uint_as_float(__reduce_max_sync(kAll, real ? __float_as_uint(off) : 0u)) + 0x1p-17f * fmaxf(fabsf(p), fabsf(q));
+                    if (!(p - q > far) && !bad) kept = (groups_exact<DT>(a, row) >> (group & 31)) & 1;
+                }
+                if (filled) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) key[i] = kept ? key[i] : 0u;
+                } else {
+                    const uint32_t open = __ballot_sync(kAll, kept);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) key[i] = (open >> group_of(i)) & 1 ? key[i] : 0u;
+                    sort_keys<V>(key);
+                }
+            } else {
+                sort_keys<V>(key);
+            }
+            uint32_t mine = 0;         // lane j: the j-th key
+            if (K > 0 && exact) {      // lists as deep as the picks to come
+#pragma unroll
+                for (int j = 0; j < K; ++j) {
+                    const uint32_t m = __reduce_max_sync(kAll, head<V>(key));
+                    if (lane == j) mine = m;
+                    if (j + 1 < K) pop<V>(key, m, K - 1 - j);
+                }
+            } else {
+                uint32_t last = 0;     // the one behind the k-th
+                int found = 0;
+#pragma unroll
+                for (int j = 0; j <= (K > 0 ? K : k); ++j, ++found) {
+                    const uint32_t m = __reduce_max_sync(kAll, head<V>(key));
+                    if (lane == j) mine = m;
+                    last = m;
+                    pop<V>(key, m, V);
+                }
+                uint32_t next = __shfl_down_sync(kAll, mine, 1);
+                if (lane == 31) next = last;
+                const float x = value_of(mine), y = value_of(next);
+                const float margin = 2 * slack + cut * fmaxf(fabsf(x), fabsf(y));
+                const bool near = !exact && lane < k && live(next) && (biased ? !(x - y > margin) : (mine & prefix) == (next & prefix));
+                if (__any_sync(kAll, near) && !bad) {
+                    // candidates: down to the first that is surely behind the k-th, at most 32
+                    const uint32_t border = __shfl_sync(kAll, mine, k - 1);
+                    const float kth = value_of(border);
+                    found = k;
+                    bool more = true;
+                    while (true) {
+                        const float z = value_of(last);
+                        more = live(last) && (biased ? !(kth - z > 2 * slack + cut * fmaxf(fabsf(kth), fabsf(z))) : (last & prefix) == (border & prefix));
+                        if (!more || found == 32) break;
+                        if (lane == found) mine = last;
+                        ++found;
+                        last = __reduce_max_sync(kAll, head<V>(key));
+                        pop<V>(key, last, V);
+                    }
+                    again = again || more;
+                    if (!again) {
+                        const bool there = lane < found && live(mine);
+                        const int e = there ? (int)(kLow - (mine & kLow)) : E;
+                        double v = -INFINITY, norm = 1.0;
+                        if (biased && softmax) {
+                            norm = 0.0;
+#pragma unroll 1
+                            for (int i = lane; i < E; i += 32) norm += exp((double)logit<DT>(row, i) - (double)top);
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1) norm += __shfl_xor_sync(kAll, norm, o);
+                        }
+                        if (there) {
+                            v = (double)logit<DT>(row, e);
+                            if (biased) v = (softmax ? exp(v - (double)top) / norm : 1.0 / (1.0 + exp(-v))) + (double)__ldg(a.bias + e);
+                        }
+                        int rank = 0;
+                        for (int i = 0; i < found; ++i) {
+                            const double u = __shfl_sync(kAll, v, i);
+                            const int j = __shfl_sync(kAll, e, i);
+                            rank += u > v || (u == v && j < e);
+                        }
+                        const uint32_t key_of = there ? mine : 0;
+                        mine = 0;
+                        for (int i = 0; i < found; ++i) {
+                            const int r = __shfl_sync(kAll, rank, i);
+                            const uint32_t q = __shfl_sync(kAll, key_of, i);
+                            if (lane == r && q != 0) mine = q;
+                        }
+                    }
+                }
+            }
+            if (softmax) {
+                if (!whole && !groups) top = value_of(__shfl_sync(kAll, mine, 0));
+                bad = bad || top == INFINITY;
+                if (!a.renorm && !whole) {
+                    Row<DT, V, VEC> present;
+                    present.load(row, E, lane);             // from L1
+                    present.widen(l, E, lane);
+                    top = l[0];
+#pragma unroll
+                    for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+                    top = warp_max(top);
+                    top = top == -INFINITY ? 0.0f : top;
+                    sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum += ex2((l[i] - top) * kLog2e);
+                    sum = warp_sum(sum);
+                }
+            }
+            int e = lane < k && live(mine) ? (int)(kLow - (mine & kLow)) : -1;
+            if (again && !bad) bad = !pick_exact<DT>(a, row, e);
+            failed |= (int)bad << q;
+            const int other = batch > 1 ? __shfl_sync(kAll, e, lane & 7) : e;
+            if (batch == 1 || lane >> 3 == q) picked = other, row_top = top, row_sum = sum;
         }
-        int e = lane < k && live(mine) ? (int)(kLow - (mine & kLow)) : -1;
-        if (again && !bad) bad = !pick_exact<DT>(a, row, e);
-        failed |= (int)bad << q;
-        const int other = batch > 1 ? __shfl_sync(kAll, e, lane & 7) : e;
-        if (batch == 1 || lane >> 3 == q) picked = other, row_top = top, row_sum = sum;
-      }
-      const int q = batch > 1 ? lane >> 3 : 0, slot = batch > 1 ? lane & 7 : lane;
-      const int64_t t = t0 + q;
-      const bool bad = (failed >> q) & 1, there = !bad && picked >= 0;
-      const float x = there ? logit<DT>(logits + t * row_bytes, picked) : -INFINITY;
-      float w;
-      if (softmax && !a.renorm) w = there ? expf(x - row_top) * rcp(row_sum) : 0.0f;
-      else w = share(a.score, a.renorm, there, x, size);
-      if (slot < k && q < batch && t < a.n) {
-          a.idx[t * k + slot] = there ? picked : -1;
-          a.weights[t * k + slot] = bad ? NAN : there ? a.scale * w : 0.0f;
-      }
-      if (failed != 0 && lane == 0) report(a.status, kErrRange);
+        const int q = batch > 1 ? lane >> 3 : 0, slot = batch > 1 ? lane & 7 : lane;
+        const int64_t t = t0 + q;
+        const bool bad = (failed >> q) & 1, there = !bad && picked >= 0;
+        const float x = there ? logit<DT>(logits + t * row_bytes, picked) : -INFINITY;
+        float w;
+        if (softmax && !a.renorm) w = there ? expf(x - row_top) * rcp(row_sum) : 0.0f;
+        else w = share(a.score, a.renorm, there, x, size);
+        if (slot < k && q < batch && t < a.n) {
+            a.idx[t * k + slot] = there ? picked : -1;
+            a.weights[t * k + slot] = bad ? NAN : there ? a.scale * w : 0.0f;
+        }
+        if (failed != 0 && lane == 0) report(a.status, kErrRange);
     }
 }
 
