@@ -241,9 +241,10 @@ __device__ __forceinline__ float share(int score, bool renorm, bool there, float
 
 // ---- the order in binary32, by keys ------------------------------------------------------------
 
-// 32-bit keys in the order of floats: the sign flipped, negative values reversed.
+// 32-bit keys in the order of floats: the sign flipped, negative values reversed.  The
+// addition makes +0 of -0, which is equal to it and would stand below it by its bits.
 __device__ __forceinline__ uint32_t ordered(float f) {
-    const uint32_t u = __float_as_uint(f);
+    const uint32_t u = __float_as_uint(f + 0.0f);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t k) {
@@ -254,11 +255,20 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// Two 16-bit values, -0 made +0; every other value as it is (a NaN's bits may change).
+template <int DT>
+__device__ __forceinline__ uint32_t one_zero(uint32_t w) {
+    uint32_t r;
+    if (DT == CGL_F16) asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0u));
+    else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0x3F803F80u), "r"(0u));   // w * 1 + 0
+    return r;
+}
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The same of a 16-bit value, which `f` holds.
 template <int DT>
 __device__ __forceinline__ uint32_t ordered16(float f) {
+    f += 0.0f;
     const uint32_t u = DT == CGL_F16 ? __half_as_ushort(__float2half_rn(f)) : __float_as_uint(f) >> 16;
     return u ^ (u & 0x8000u ? 0xFFFFu : 0x8000u);
 }
@@ -309,7 +319,7 @@ struct Row {
     __device__ __forceinline__ void keys(uint32_t key[V], int E, int lane, uint32_t code) const {
 #pragma unroll
         for (int c = 0; c < (VEC ? V / 8 : 0); ++c) {
-            const uint32_t w[4] = {raw[c][0].x, raw[c][0].y, raw[c][0].z, raw[c][0].w};
+            const uint32_t w[4] = {one_zero<DT>(raw[c][0].x), one_zero<DT>(raw[c][0].y), one_zero<DT>(raw[c][0].z), one_zero<DT>(raw[c][0].w)};
             const bool there = lane * V + 8 * c < E;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
