@@ -53,16 +53,17 @@ __device__ __forceinline__ void store8(uint16_t *p, bool vec, int n, const float
     }
 }
 
-// The activation's derivative.
-__device__ __forceinline__ float slope(float z, int act) {
-    if (act == CGL_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+// g times the activation's derivative.  ReLU selects: a closed unit drops what comes in,
+// infinities and NaN too, which a product by 0 would keep; where z is NaN so is dz.
+__device__ __forceinline__ float through(float g, float z, int act) {
+    if (act == CGL_ACT_RELU) return z > 0.0f ? g : z != z ? z : 0.0f;
     if (act == CGL_ACT_GELU) {
         float bell;
         const float cdf = normal_cdf(z, bell);
-        return cdf + 0.39894228f * bell * z;
+        return g * (cdf + 0.39894228f * bell * z);
     }
     const float s = sigmoid(z);
-    return s * (1.0f + z * (1.0f - s));
+    return g * (s * (1.0f + z * (1.0f - s)));
 }
 
 struct Slope {
@@ -161,7 +162,7 @@ slope_kernel(const Slope a) {
                         float x[8];
                         load8(z + r * F + col, a.vec, n, x);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) d[j] = g[j] * slope(x[j], a.act);
+                        for (int j = 0; j < 8; ++j) d[j] = through(g[j], x[j], a.act);
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sum[j] += d[j];

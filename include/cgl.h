@@ -629,7 +629,7 @@ cgl_status cgl_route_backward(const float *grad_weights, const void *logits, int
 /* What cgl_matmul_bf16 does to a sum z before the residual. */
 typedef enum cgl_activation {
     CGL_ACT_NONE = 0,
-    CGL_ACT_RELU = 1,     /* max(z, 0) */
+    CGL_ACT_RELU = 1,     /* max(z, 0); its gradient selects: g where z > 0, 0 where z <= 0 whatever g, NaN where z is NaN */
     CGL_ACT_GELU = 2,     /* z Phi(z), Phi the normal distribution function */
     CGL_ACT_SILU = 3,     /* z sigmoid(z) */
     CGL_ACT_SWIGLU = 4    /* z[f] sigmoid(z[f]) z[out / 2 + f], f < out / 2: gate rows first, then up rows */
