@@ -529,8 +529,8 @@ cgl_status cgl_matmul_bf16_backward(const uint16_t *grad_y, const uint16_t *a, i
     if (ok != CGL_OK) return ok;
     if (rows > 0 && (!grad_y || (act != CGL_ACT_NONE && !preact))) return CGL_EINVAL;
     if (!preact_ok(preact, preact_dtype)) return CGL_EINVAL;
-    const bool plain = act == CGL_ACT_NONE && F % 8 == 0 && aligned(grad_y, 16) && !grad_bias;   // grad_y is dz
-    if (workspace ? workspace_bytes < matmul_bf16_backward_workspace_bytes(rows, E, F) : !plain) return CGL_EINVAL;
+    if (workspace ? workspace_bytes < matmul_bf16_backward_workspace_bytes(rows, E, F) : grad_bias || !grad_y_is_dz(act, F, grad_y))
+        return CGL_EINVAL;
     if (!aligned(grad_y, 2) || !aligned(preact, preact_dtype == CGL_F32 ? 4 : 2) || !aligned(grad_a, 16) || !aligned(grad_w, 16) || !aligned(grad_bias, 2) ||
         !aligned(workspace, 16))
         return CGL_EALIGN;

@@ -176,6 +176,8 @@ cgl_status launch_matmul_bf16(const MatmulArgs &m, const uint16_t *bias, const u
 size_t matmul_bf16_backward_workspace_bytes(int64_t rows, int E, int F);
 cgl_status launch_matmul_bf16_backward(const MatmulArgs &m, const uint16_t *grad_y, const void *preact, bool preact_f32, uint16_t *grad_a,
                                        uint16_t *grad_w, uint16_t *grad_bias, void *ws, cudaStream_t stream);
+// Whether the products of the backward pass read grad_y itself, as dz: then only a bias's gradient needs the workspace.
+bool grad_y_is_dz(int act, int F, const uint16_t *grad_y);
 // Its first step: dz for the products (BF16, rows of *ld values; grad_y itself where it serves) and grad_bias, where wanted.
 cgl_status launch_slope(const MatmulArgs &m, const uint16_t *grad_y, const void *preact, bool preact_f32, bool products,
                         uint16_t *grad_bias, void *ws, const uint16_t **dz, int64_t *ld, cudaStream_t stream);

@@ -227,6 +227,10 @@ size_t round16(size_t v) { return (v + 15) / 16 * 16; }
 
 }  // namespace
 
+bool grad_y_is_dz(int act, int F, const uint16_t *grad_y) {
+    return act == CGL_ACT_NONE && F % 8 == 0 && (reinterpret_cast<uintptr_t>(grad_y) & 15) == 0;
+}
+
 // dz with rows of whole 16 bytes, then the pieces' sums.
 size_t matmul_bf16_backward_workspace_bytes(int64_t rows, int E, int F) {
     return round16((size_t)rows * ((F + 7) / 8 * 8) * 2) + (size_t)(rows / kPiece + E) * F * 4 + 16;
@@ -237,11 +241,11 @@ cgl_status launch_slope(const MatmulArgs &m, const uint16_t *grad_y, const void 
     const bool gated = m.act == CGL_ACT_SWIGLU;
     Slope a = {};
     a.off = m.off, a.rows = m.rows, a.cap = m.cap, a.E = m.E, a.cols = gated ? m.F / 2 : m.F, a.act = m.act;
-    a.g = grad_y, a.z = preact, a.status = m.status;
-    a.vec = a.cols % 8 == 0 && ((reinterpret_cast<uintptr_t>(grad_y) | reinterpret_cast<uintptr_t>(preact)) & 15) == 0;
+    a.g = grad_y, a.z = m.act == CGL_ACT_NONE ? nullptr : preact, a.status = m.status;   // not read without an activation
+    a.vec = a.cols % 8 == 0 && ((reinterpret_cast<uintptr_t>(grad_y) | reinterpret_cast<uintptr_t>(a.z)) & 15) == 0;
     a.ld = (m.F + 7) / 8 * 8;
-    // without an activation grad_y is dz, where TMA can read its rows
-    const bool as_is = m.act == CGL_ACT_NONE && a.vec;
+    const bool as_is = grad_y_is_dz(m.act, m.F, grad_y);
+    if (ws == nullptr && ((products && !as_is) || grad_bias != nullptr)) return CGL_EINVAL;
     a.dz = products && !as_is ? static_cast<uint16_t *>(ws) : nullptr;
     a.part = grad_bias == nullptr ? nullptr : reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + round16((size_t)m.rows * a.ld * 2));
     *dz = as_is ? grad_y : a.dz;
