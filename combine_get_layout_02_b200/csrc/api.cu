@@ -147,9 +147,13 @@ const char *cgl_status_string(int s) {
     }
 }
 
+// Tokens and slots in 32 bits; n by itself first, so that the product stays in 64.
+static bool slots_ok(int64_t n, int k) {
+    return n >= 0 && n < ((int64_t)1 << 31) && k >= 1 && k <= kMaxTopk && n * k < ((int64_t)1 << 31);
+}
+
 static bool layout_sizes_ok(int64_t n, int k, int E, int R) {
-    return n >= 0 && k >= 1 && k <= kMaxTopk && E >= 1 && E <= kMaxExperts && R >= 1 && R <= E &&
-           E % R == 0 && n * (int64_t)k < ((int64_t)1 << 31);
+    return slots_ok(n, k) && E >= 1 && E <= kMaxExperts && R >= 1 && R <= E && E % R == 0;
 }
 
 size_t cgl_layout_workspace_bytes(int64_t n, int k, int E, int R) {
@@ -366,7 +370,7 @@ cgl_status cgl_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int
 cgl_status cgl_dispatch_mxfp4(const uint16_t *x, int64_t n, int h, int k, const int32_t *dst_pos, uint8_t *recv_x,
                               uint8_t *recv_scale, int64_t recv_rows, const cgl_opts *opts, uint32_t *status_dev,
                               void *stream) {
-    if (!mx_sizes_ok(n, h) || k < 1 || k > kMaxTopk || n * (int64_t)k >= ((int64_t)1 << 31) || recv_rows < 0)
+    if (!mx_sizes_ok(n, h) || !slots_ok(n, k) || recv_rows < 0)
         return CGL_EINVAL;
     if (opt_sms(opts) < 0 || !flags_ok(opts)) return CGL_EINVAL;
     if (n > 0 && (!x || !dst_pos)) return CGL_EINVAL;
@@ -409,8 +413,7 @@ cgl_status cgl_selftest_matmul_timeout(const uint8_t *a, const uint8_t *a_scale,
 }
 
 static bool balance_sizes_ok(int64_t n, int k, int E, int64_t S) {
-    return n >= 0 && k >= 1 && k <= kMaxTopk && E >= 1 && E <= kMaxExperts && S >= 1 && S <= ((int64_t)1 << 24) &&
-           n % S == 0 && n * (int64_t)k < ((int64_t)1 << 31);
+    return slots_ok(n, k) && E >= 1 && E <= kMaxExperts && S >= 1 && S <= ((int64_t)1 << 24) && n % S == 0;
 }
 
 size_t cgl_balance_loss_workspace_bytes(int64_t n, int k, int E, int64_t S) {
@@ -451,7 +454,7 @@ cgl_status cgl_balance_loss_backward(const float *grad_loss, const void *logits,
 }
 
 static bool route_sizes_ok(int64_t n, int E, int k) {
-    return n >= 0 && E >= 1 && E <= kMaxExperts && k >= 1 && k <= kMaxTopk && k <= E && n * (int64_t)k < ((int64_t)1 << 31);
+    return slots_ok(n, k) && E >= 1 && E <= kMaxExperts && k <= E;
 }
 
 cgl_status cgl_route(const void *logits, int dtype, int64_t n, int E, int k, const float *bias, int groups, int keep,
@@ -473,7 +476,7 @@ cgl_status cgl_route(const void *logits, int dtype, int64_t n, int E, int k, con
 cgl_status cgl_route_backward(const float *grad_weights, const void *logits, int dtype, const int32_t *topk_idx,
                               int64_t n, int E, int k, int score, int renorm, float scale, void *grad_logits,
                               uint32_t *status_dev, void *stream) {
-    if (n < 0 || E < 1 || E > kMaxExperts || k < 1 || k > kMaxTopk || n * (int64_t)k >= ((int64_t)1 << 31) || !dtype_ok(dtype))
+    if (!slots_ok(n, k) || E < 1 || E > kMaxExperts || !dtype_ok(dtype))
         return CGL_EINVAL;
     if (score != CGL_SCORE_SOFTMAX && score != CGL_SCORE_SIGMOID) return CGL_EINVAL;
     if (n > 0 && (!grad_weights || !logits || !topk_idx || !grad_logits)) return CGL_EINVAL;
