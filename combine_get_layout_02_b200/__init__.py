@@ -746,21 +746,41 @@ def _choice(value, names, what: str) -> int:
     return names[value]
 
 
-try:   # on the current device, in 0.8 us of a small call's 10; torch.empty_strided takes 1.5, new_empty 2, torch.empty 2.4
-    from torch._C._dynamo.guards import _empty_strided_cuda
+try:   # 0.8 us of a small call's 10; torch.empty_strided takes 1.5, new_empty 2, torch.empty 2.4
+    from torch._C._dynamo.guards import _empty_strided_cuda as _short_empty
 except ImportError:
-    _empty_strided_cuda = None
+    _short_empty = None
+
+
+def _public_empty(shape, strides, dtype):
+    """A tensor on the current device."""
+    return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+
+def _first_empty(shape, strides, dtype):
+    """Like _public_empty; chooses what later calls take.  The short path is private to torch: it has to give what the public one gives."""
+    global _empty
+    try:
+        t = _short_empty((2, 3), (3, 1), torch.int32)
+        same = (t.shape, t.stride(), t.dtype, t.device.type, t.device.index) == ((2, 3), (3, 1), torch.int32, "cuda", torch.cuda.current_device())
+    except Exception:
+        same = False
+    _empty = _short_empty if same else _public_empty
+    return _empty(shape, strides, dtype)
+
+
+_empty = _first_empty
 
 
 def _out(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor) -> torch.Tensor:
-    """_buf, with the short path to the allocator."""
+    """_buf, with the short path to the allocator (not where new memory is to be filled, as in torch's deterministic mode)."""
     if t is not None:
         return _buf(t, name, shape, dtype, like)
     strides = (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1) if len(shape) == 3 else (1,)
     device = like.device
-    if _empty_strided_cuda is None or device.index != torch._C._cuda_getDevice():
+    if device.index != torch._C._cuda_getDevice() or torch.are_deterministic_algorithms_enabled():
         return torch.empty_strided(shape, strides, dtype=dtype, device=device)
-    return _empty_strided_cuda(shape, strides, dtype)
+    return _empty(shape, strides, dtype)
 
 
 class Routing(NamedTuple):
