@@ -1,5 +1,6 @@
 // The exported C ABI (declared in include/cgl.h): argument checks, then one
 // call into the launchers.  Host-visible errors return before any launch.
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -453,6 +454,20 @@ cgl_status cgl_balance_loss_backward(const float *grad_loss, const void *logits,
                                         num_routed, grad_logits, static_cast<cudaStream_t>(stream));
 }
 
+// Arrays of a call, to find those that have bytes in common.
+struct Bytes {
+    const void *p;
+    size_t n;
+};
+static bool meet(Bytes a, std::initializer_list<Bytes> others) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p);
+    for (const Bytes &b : others) {
+        const uintptr_t y = reinterpret_cast<uintptr_t>(b.p);
+        if (a.p && b.p && a.n > 0 && b.n > 0 && x < y + b.n && y < x + a.n) return true;
+    }
+    return false;
+}
+
 static bool route_sizes_ok(int64_t n, int E, int k) {
     return slots_ok(n, k) && E >= 1 && E <= kMaxExperts && k <= E;
 }
@@ -468,6 +483,9 @@ cgl_status cgl_route(const void *logits, int dtype, int64_t n, int E, int k, con
     if (!aligned(logits, dtype == CGL_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
         !aligned(topk_weights, 4) || !aligned(status_dev, 4))
         return CGL_EALIGN;
+    const size_t slots = (size_t)n * k * 4;
+    const Bytes in = {logits, (size_t)n * E * (dtype == CGL_F32 ? 4 : 2)}, steer = {bias, (size_t)E * 4}, ids = {topk_idx, slots}, ws = {topk_weights, slots};
+    if (meet(ids, {in, steer, ws}) || meet(ws, {in, steer})) return CGL_EINVAL;
     const RouteArgs a = {logits, dtype, n, E, k, bias, groups, keep, by, score, renorm != 0, scale, topk_idx, topk_weights,
                          status_dev};
     return launch_route(a, static_cast<cudaStream_t>(stream));
@@ -484,6 +502,8 @@ cgl_status cgl_route_backward(const float *grad_weights, const void *logits, int
     if (!aligned(logits, item) || !aligned(grad_logits, item) || !aligned(topk_idx, 4) || !aligned(grad_weights, 4) ||
         !aligned(status_dev, 4))
         return CGL_EALIGN;
+    const size_t rows = (size_t)n * E * item, slots = (size_t)n * k * 4;
+    if (meet({grad_logits, rows}, {{logits, rows}, {grad_weights, slots}, {topk_idx, slots}})) return CGL_EINVAL;
     return launch_route_backward(grad_weights, logits, dtype, topk_idx, n, E, k, score, renorm != 0, scale, grad_logits,
                                  status_dev, static_cast<cudaStream_t>(stream));
 }
@@ -516,6 +536,11 @@ cgl_status cgl_matmul_bf16(const uint16_t *a, int64_t rows, const uint16_t *w, i
     if (rows > 0 && !y) return CGL_EINVAL;
     if (!preact_ok(preact, preact_dtype)) return CGL_EINVAL;
     if (!aligned(bias, 2) || !aligned(residual, 2) || !aligned(y, 2) || !aligned(preact, preact_dtype == CGL_F32 ? 4 : 2)) return CGL_EALIGN;
+    // Blocks read their operands while others write; each reads its own part of the residual, which y may therefore be.
+    const Bytes out = {y, (size_t)rows * (act == CGL_ACT_SWIGLU ? F / 2 : F) * 2}, z = {preact, (size_t)rows * F * (preact_dtype == CGL_F32 ? 4 : 2)},
+                rest = {residual, out.n}, x = {a, (size_t)rows * K * 2}, weights = {w, (size_t)E * F * K * 2}, b = {bias, (size_t)E * F * 2},
+                off = {expert_offset, (size_t)(E + 1) * 4};
+    if (meet(out, {x, weights, b, off, z}) || meet(z, {x, weights, b, off, rest}) || (y != residual && meet(out, {rest}))) return CGL_EINVAL;
     const MatmulArgs m = {a, rows, w, E, F, K, expert_offset, opt_cap(opts), act, opt_sms(opts), status_dev};
     return launch_matmul_bf16(m, bias, residual, y, preact, preact_dtype == CGL_F32, static_cast<cudaStream_t>(stream));
 }
@@ -537,6 +562,15 @@ cgl_status cgl_matmul_bf16_backward(const uint16_t *grad_y, const uint16_t *a, i
     if (!aligned(grad_y, 2) || !aligned(preact, preact_dtype == CGL_F32 ? 4 : 2) || !aligned(grad_a, 16) || !aligned(grad_w, 16) || !aligned(grad_bias, 2) ||
         !aligned(workspace, 16))
         return CGL_EALIGN;
+    // dz, the bias's gradient, grad_a and grad_w are made in this order.  grad_y and preact are done with after dz, but for a grad_y that is dz.
+    const bool as_is = grad_y_is_dz(act, F, grad_y);
+    const Bytes g = {grad_y, (size_t)rows * (act == CGL_ACT_SWIGLU ? F / 2 : F) * 2}, dz = {grad_y, as_is ? g.n : 0}, x = {a, (size_t)rows * K * 2},
+                weights = {w, (size_t)E * F * K * 2}, z = {preact, act == CGL_ACT_NONE ? 0 : (size_t)rows * F * (preact_dtype == CGL_F32 ? 4 : 2)},
+                off = {expert_offset, (size_t)(E + 1) * 4}, da = {grad_a, x.n}, dw = {grad_w, weights.n}, db = {grad_bias, (size_t)E * F * 2},
+                scratch = {workspace, as_is && !grad_bias ? 0 : matmul_bf16_backward_workspace_bytes(rows, E, F)};
+    if (meet(da, {weights, dz, dw, off}) || (grad_w && meet(da, {x})) || meet(dw, {x, dz, off}) || meet(db, {x, weights, dz, da, dw, off}) ||
+        meet(scratch, {g, z, x, weights, off, da, dw, db}))
+        return CGL_EINVAL;
     const MatmulArgs m = {a, rows, w, E, F, K, expert_offset, opt_cap(opts), act, opt_sms(opts), status_dev};
     return launch_matmul_bf16_backward(m, grad_y, preact, preact_dtype == CGL_F32, grad_a, grad_w, grad_bias, workspace,
                                        static_cast<cudaStream_t>(stream));

@@ -598,6 +598,7 @@ typedef enum cgl_group_score {
  *   it only steers the choice and has no gradient).
  * Out (device, written in full): topk_idx int32 [num_tokens, num_topk];
  *   topk_weights binary32 [num_tokens, num_topk].
+ * The outputs overlap neither the inputs nor each other (CGL_EINVAL).
  * Limits: num_topk <= min(E, 32), num_groups <= 32 and E % num_groups == 0,
  * topk_groups in [1, num_groups], num_tokens * num_topk < 2^31.
  * 16-byte aligned rows (E % 8 == 0) are read faster.
@@ -619,7 +620,7 @@ cgl_status cgl_route(const void *logits, int dtype, int64_t num_tokens, int num_
  * In (device): grad_weights binary32 [num_tokens, num_topk]; logits as for
  *   cgl_route; topk_idx int32 [num_tokens, num_topk] (cgl_route's).
  * Out (device, written in full): grad_logits [num_tokens, E] in the logits' type;
- *   it must not overlap the logits.
+ *   it must not overlap an input (CGL_EINVAL).
  * Device errors: CGL_ERANGE for ids < -1 or >= E (they take no part).
  */
 cgl_status cgl_route_backward(const float *grad_weights, const void *logits, int dtype, const int32_t *topk_idx,
@@ -649,7 +650,8 @@ typedef enum cgl_activation {
  *   NULL (it may be y itself); expert_offset int32 [E + 1].
  * Out (device): y BF16 [num_rows, F]; preact [num_rows, out], z for
  *   cgl_matmul_bf16_backward, CGL_F32 or, rounded, CGL_BF16 (preact_dtype), or NULL.
- *   Rows of no expert are NOT written.
+ *   Rows of no expert are NOT written.  The outputs overlap neither the inputs (but
+ *   for a residual that is y) nor each other (CGL_EINVAL).
  * Requires in % 8 == 0; out even with CGL_ACT_SWIGLU; in, out <= 2^20; num_rows <=
  * 2^31 - 4096, and >= E * capacity when padded; a and w 16-byte aligned, the others
  * to their type (16-byte aligned rows are faster).  opts: capacity, num_sms (blocks
@@ -677,10 +679,14 @@ size_t cgl_matmul_bf16_backward_workspace_bytes(int64_t num_rows, int num_expert
  *   preact [num_rows, out], CGL_F32 or CGL_BF16 (NULL with CGL_ACT_NONE, which needs none).
  * Out (device): grad_a BF16 [num_rows, in], rows of no expert NOT written; grad_w
  *   BF16 [E, out, in] and grad_bias BF16 [E, out], written in full (0 for experts
- *   without rows).
+ *   without rows).  Written in the order grad_bias, grad_a, grad_w; CGL_EINVAL where
+ *   one of them would overwrite what is still to be read: w, a (grad_a only where
+ *   grad_w is wanted), another output, and grad_y where it serves as dz (the case
+ *   below that needs no workspace).  preact, another grad_y, and w under grad_w may be
+ *   written over.
  * workspace: device, 16-byte aligned, any contents, scratch for the call (calls
- *   that overlap on the GPU must not share one); may be NULL with CGL_ACT_NONE, out
- *   % 8 == 0, a 16-byte aligned grad_y and no grad_bias.
+ *   that overlap on the GPU must not share one), apart from all other arrays; may be
+ *   NULL with CGL_ACT_NONE, out % 8 == 0, a 16-byte aligned grad_y and no grad_bias.
  * Sizes, alignment, opts and errors as for cgl_matmul_bf16 (grad_a and grad_w
  * 16-byte aligned).
  */
