@@ -905,28 +905,35 @@ int box_rows(int nt) { return nt > 128 ? 32 : nt > 64 ? 16 : 8; }
 // Columns a tile and pairs that share one (p.nt, p.split), by what the call would take
 // in cycles: waves of tiles, a stage of 512 cycles at 256 columns (the MMAs) and not
 // below 370 (a block's 16 KiB of X from DRAM), 2000 and 10 a column for a tile's
-// epilogue, 1500 and 40 a column for joining pairs' sums.  Narrow tiles read X more
-// often, wide ones leave pairs without work: 2000 rows, 512 -> 512: 64 columns 9.5 us,
-// 256 11.0; 2048 rows, 2048 -> 7168: 113 and 49.  Pairs share a tile where that leaves
+// epilogue, 1500 and 40 a column for joining pairs' sums.  An expert's rows are cut into
+// equal parts, so a tile's columns are those of its part (of the mean one; grad_w's
+// tiles are whole) and a width is worth what it makes of the number of parts.  Narrow
+// tiles read X more often, wide ones leave pairs without work: 2000 rows, 512 -> 512:
+// 64 columns 9.5 us, 256 11.0; 2048 rows, 2048 -> 7168: 113 and 49; 16 experts of 256
+// rows, 2048 -> 2048: 208 columns 65 us, 256 46.  Pairs share a tile where that leaves
 // each four stages, all clusters run at once and the sums fit into the first pair's
-// ring.  `guess` and `most`: tiles of rows of that many columns, as expected and at most.
+// ring.  `guess` and `most`: tiles of rows of that many columns, as expected and at most;
+// `exact`: the guess is right.  Where it may not be, a narrower width has to promise 3%:
+// 16 experts of 512 rows, 7168 -> 2048: 240 columns 254 us, 256 212.
 template <int MODE, typename Guess, typename Most>
-void plan(Params &p, int widest, int64_t mtiles, int64_t steps, int64_t pairs, Guess guess, Most most) {
+void plan(Params &p, int widest, int64_t mtiles, int64_t steps, int64_t rows, int64_t pairs, bool exact, Guess guess, Most most) {
     static const int widths[] = {32, 64, 96, 128, 160, 192, 208, 224, 240, 256};
     double best = 0;
     int nt = 0, split = 1;
-    for (int i = -1; i < 10; ++i) {
-        p.nt = i < 0 ? widest : widths[i];
-        if (i >= 0 && p.nt >= widest) break;
+    for (int i = 10; i >= 0; --i) {   // the widest first: of equals it stays
+        p.nt = i == 10 ? widest : widths[i];
+        if (i < 10 && p.nt >= widest) continue;
         if (MODE == kGradW && p.nt % 64 != 0) continue;   // 64 columns a chunk: others load as many
         if (MODE != kGradW) p.box = box_rows(p.nt);
-        const double tiles = (double)guess(p.nt) * mtiles, out = 2000 + 10 * p.nt;
-        const double stage = 2 * p.nt > 370 + p.nt / 2 ? 2 * p.nt : 370 + p.nt / 2;
+        const double parts = (double)guess(p.nt), tiles = parts * mtiles;
+        int part = p.nt;
+        if (MODE != kGradW && rows <= parts * (p.nt - 16)) part = ((int)std::ceil(rows / parts) + 15) / 16 * 16;
+        const double out = 2000 + 10 * part, stage = 2 * part > 370 + part / 2 ? 2 * part : 370 + part / 2;
         for (int k = 1; k <= 4; ++k) {
             if (k > 1 && (tiles * k > pairs || steps < 4 * k)) break;
             const double waves = k > 1 ? 1 : std::ceil(tiles / pairs), sums = ((steps + k - 1) / k) * stage;
-            const double t = waves * (sums > out ? sums : out) + out + (k > 1 ? 1500 + 40 * p.nt : 0);
-            if (nt != 0 && t >= best) continue;
+            const double t = waves * (sums > out ? sums : out) + out + (k > 1 ? 1500 + 40 * part : 0);
+            if (nt != 0 && t >= (exact || p.nt == nt ? best : 0.97 * best)) continue;
             if (k > 1) {
                 const size_t smem = lay_out<MODE>(p);
                 if (most(p.nt) * mtiles * k > pairs || (k - 1) * part_bytes(p.nt) > (uint32_t)p.stages * p.stage_bytes ||
@@ -974,12 +981,14 @@ int64_t plan_rows(Params &p, const MatmulArgs &m, int64_t pairs) {
     const auto guess = [&](int nt) {
         if (m.cap > 0) return (double)m.E * ((m.cap + nt - 1) / nt);
         if (some == 1) return (double)((m.rows + nt - 1) / nt);
-        const double each = (double)m.rows / some / nt;
-        return some * (each <= 0.75 ? 1.0 : each + 0.5);
+        // an expert's rows within an eighth of their mean, each number as likely: the mean of the tiles that takes
+        const double mean = (double)m.rows / some / nt, a = mean * 0.875, b = mean * 1.125;
+        const auto sum = [](double x) { const double n = std::floor(x); return n * (n + 1) / 2 + (x - n) * (n + 1); };   // of ceil, from 0 to x
+        return some * (b <= 1 ? 1.0 : (sum(b) - sum(a)) / (b - a));
     };
     // with a row in each expert and the others in whole tiles
     const auto most = [&](int nt) { return some + (m.rows - some) / nt; };
-    plan<MODE>(p, widest, mtiles, (p.C + kStageC - 1) / kStageC, pairs, guess, most);
+    plan<MODE>(p, widest, mtiles, (p.C + kStageC - 1) / kStageC, m.cap > 0 ? m.E * m.cap : m.rows, pairs, m.cap > 0 || some == 1, guess, most);
     return most(p.nt) * mtiles;
 }
 
@@ -1037,7 +1046,7 @@ cgl_status launch_matmul_bf16_backward(const MatmulArgs &m, const uint16_t *grad
         p.wide = 1;
         const int64_t mtiles = (m.K + 2 * kM - 1) / (2 * kM);
         const auto tiles = [&](int nt) { return (int64_t)m.E * ((m.F + nt - 1) / nt); };
-        plan<kGradW>(p, kMaxNt, mtiles, (m.rows / m.E + kStageC - 1) / kStageC, pairs, tiles, tiles);
+        plan<kGradW>(p, kMaxNt, mtiles, (m.rows / m.E + kStageC - 1) / kStageC, 0, pairs, true, tiles, tiles);
         const int64_t rows = m.rows > 0 ? m.rows : 1;   // without rows nothing is loaded, and a map needs one
         const int64_t ad[2] = {m.K, rows}, as[1] = {m.K}, zd[2] = {m.F, rows};
         const int box[2] = {64, kStageC};
