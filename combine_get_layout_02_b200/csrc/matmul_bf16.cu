@@ -28,13 +28,15 @@
 //
 // What bounds it (B200; floors at the measured 6.55 TB/s copy and 1656 TFLOP/s burst,
 // 1396 sustained).  Few rows an expert, the weights' bytes: 4 rows, 256 experts, 7168 ->
-// 2 x 2048 gated 2.08 ms (7.1 TB/s, the floor 2.26 being that of a copy); 128 rows 2.29 to 2.43
+// 2 x 2048 gated 2.07 ms (7.1 TB/s, the floor 2.26 being that of a copy); 128 rows 2.29 to 2.45
 // ms in short runs (floor 2.39), 2.6 to 3.0 at the 1000 W cap.  Many rows, the tensor cores
-// and in long runs the cap: 8192^3 681 us (1615 TFLOP/s; cuBLAS 671), long 780 to 830 by the card
-// (cuBLAS 750); grad_a and grad_w 780 to 850.  512 rows an expert, 2048 -> 7168, 16 experts:
-// 170 us with the tensor pipe active 77% of the time, 12.1 waves of tiles in 13; a tile of
+// and in long runs the cap: 8192^3 676 to 707 us in a short run by the card (1555 to 1626
+// TFLOP/s; cuBLAS 662 to 671), 780 to 849 in a long one (750 to 802); grad_a 676 to 852 and 839 to
+// 849, grad_w 702 to 835 and 890 to 929.  512 rows an expert, 2048 -> 7168, 16 experts: 168 us
+// with the tensor pipe active 79% of the time, 12.1 waves of tiles in 13; a tile of
 // 200 columns takes 71 bytes a cycle and SM from L2, whose ports carry 64.  One row, 7168
-// -> 4096: 17.4 us, 9 of bytes and 5.5 for a call without work.  Sums are binary32, but the
+// -> 4096: 17.5 us, 9 of bytes and 5.5 for a call without work; 128 rows 21.6 (cuBLAS
+// 14); both are 16 tiles of three pairs, 96 of 148 SMs.  Sums are binary32, but the
 // tensor cores cut each addition towards zero: 1.5e-6 off (root mean square) for 1520
 // terms whose sum is about 1, where rounded additions are 8e-8 off.
 //
@@ -910,11 +912,11 @@ int box_rows(int nt) { return nt > 128 ? 32 : nt > 64 ? 16 : 8; }
 // tiles are whole) and a width is worth what it makes of the number of parts.  Narrow
 // tiles read X more often, wide ones leave pairs without work: 2000 rows, 512 -> 512:
 // 64 columns 9.5 us, 256 11.0; 2048 rows, 2048 -> 7168: 113 and 49; 16 experts of 256
-// rows, 2048 -> 2048: 208 columns 65 us, 256 46.  Pairs share a tile where that leaves
+// rows, 2048 -> 2048: 208 columns 60 us, 256 46.  Pairs share a tile where that leaves
 // each four stages, all clusters run at once and the sums fit into the first pair's
 // ring.  `guess` and `most`: tiles of rows of that many columns, as expected and at most;
 // `exact`: the guess is right.  Where it may not be, a narrower width has to promise 3%:
-// 16 experts of 512 rows, 7168 -> 2048: 240 columns 254 us, 256 212.
+// grad_a of 16 experts of 512 rows, 2048 -> 7168: 240 columns 254 us, 256 212.
 template <int MODE, typename Guess, typename Most>
 void plan(Params &p, int widest, int64_t mtiles, int64_t steps, int64_t rows, int64_t pairs, bool exact, Guess guess, Most most) {
     static const int widths[] = {32, 64, 96, 128, 160, 192, 208, 224, 240, 256};

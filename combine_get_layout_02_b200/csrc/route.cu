@@ -8,11 +8,18 @@
 // 32 bits cannot put in order are compared in binary64, so ids are the definition's.
 //
 // What bounds it (B200, replayed from a graph; 65536 x 256 BF16, top-8, 33.5 MB or 5.1 us
-// of logits): instructions.  Forward 23.5 us, softmax as it is 29.0: 250 instructions a
-// token, most of them on the integer pipe, which issues every other cycle (63% of cycles
-// issue).  With a bias and sigmoid 40; binary32, bias, 8 groups by pairs 62.  Backward 11.3 us
-// renormalised (floor 6.4 with ids and gradients), 19.4 for the whole softmax (11.5), where
-// each logit's exponential is made twice for want of registers.  128 tokens 2.4 to 3.3 us.
+// of logits): instructions.  Forward 23.7 us, softmax as it is 29.5: 255 instructions a
+// token, 163 of them on the integer pipe, which issues every other cycle (65% of cycles
+// issue).  A warp takes a token whatever the experts: 64 or 128 of them 26 us.  With a
+// bias and sigmoid 40 (480 instructions); binary32, bias, 8 groups by pairs 62 (739); 160
+// experts in 8 groups, which do not fill lanes and go through shared memory, 57 (682); 16384
+// x 512 25 (910: lists past eight a lane are scanned for every pick).  Backward 11.4 us
+// renormalised (floor 6.4 with ids and gradients; 103 instructions, and 46% of an SM's
+// warps at 64 registers), 19.4 for the whole softmax (11.5), where each logit's exponential
+// is made twice for want of registers.  128 tokens 2.4 to 3.1 us.  16-bit logits with top-8
+// and neither bias nor groups spill nothing; most other kernels up to 256 experts up to 104
+// bytes a thread (64 or 80 registers for four or three blocks an SM), past 512 experts up
+// to 432 at 128 registers.
 #include "mxfp4.cuh"
 #include "launch.h"
 
@@ -455,7 +462,9 @@ route_kernel(const RouteArgs a) {
         for (int i = 0; i < V; ++i) packed[i / 4] |= (uint32_t)((lane * V + i) / per & 31) << (8 * (i % 4));
     const auto group_of = [&](int i) { return (packed[i / 4] >> (8 * (i % 4))) & 31; };
     // A warp takes `batch` tokens after one another and then, eight lanes a token, their weights at once.
-    const int batch = groups ? 1 : a.batch;   // one with groups, whose registers leave no room (16384 x 256 17.0 us, four at once 18.1; 65536 66.8 and 60.4)
+    // One with groups, whose registers leave no room: binary32, 8 groups by maxima, 8192 x 256 10.2 us and four at once
+    // 11.4, 16384 16.1 and 18.3, 65536 52.4 and 52.7; with a bias, by pairs, 13.8 and 14.2, 19.8 and 19.5, 61.6 and 59.7.
+    const int batch = groups ? 1 : a.batch;
     const int64_t step = (int64_t)gridDim.x * kWarps * batch;
     const size_t row_bytes = (size_t)E * (DT == CGL_F32 ? 4 : 2);
     const char *const logits = static_cast<const char *>(a.logits);
