@@ -896,7 +896,7 @@ def matmul_bf16(a: torch.Tensor, w: torch.Tensor, expert_offset: Optional[torch.
     expert_offset int32 [E + 1] and capacity as get_layout gives them; without expert_offset w has one expert (or is
     [out, in], bias then [out]) and takes every row.  activation: "none", "relu", "gelu", "silu", or "swiglu": the
     first half of w's rows is the gate, the second the up projection, and y and residual have out / 2 columns.
-    Rows of no expert are left as they were.  with_preact: returns (y, preact), the sums with bias in fp32
+    Rows of no expert are left as they were.  y may be the residual itself; other overlaps are refused.  with_preact: returns (y, preact), the sums with bias in fp32
     [rows, out], which matmul_bf16_backward takes; otherwise y alone.  preact: a buffer for them, fp32, or bfloat16,
     which halves its bytes and costs the gradients a rounding."""
     if stream is not None:
@@ -931,7 +931,8 @@ def matmul_bf16_backward(grad_y: torch.Tensor, a: torch.Tensor, w: torch.Tensor,
     """Gradients of matmul_bf16 for its rows, weights and bias (cgl_matmul_bf16_backward); the residual's is grad_y itself.
 
     preact: what matmul_bf16(..., with_preact=True) gave (not needed without an activation).  Rows of grad_a of no
-    expert are left as they were (uninitialised when allocated here); grad_w and grad_bias of an expert without rows are 0."""
+    expert are left as they were (uninitialised when allocated here); grad_w and grad_bias of an expert without rows are 0.
+    Gradients may be written over preact and what else cgl_matmul_bf16_backward is done with; other overlaps are refused."""
     if stream is not None:
         with _on(stream, a, "a"):
             return matmul_bf16_backward(grad_y, a, w, expert_offset, capacity, activation=activation, preact=preact, want_a=want_a,

@@ -589,8 +589,8 @@ typedef enum cgl_group_score {
  *   picked, best first.  Equal values go to the lower index.
  *   weight_j = scale * s_j, or with renormalize scale * s_j / sum of the picked s
  *   (the quotient of the true values, also where all picked s underflow).
- * The order is that of the values in binary64: where two choices are nearer than
- * binary32 resolves, they are computed again in binary64.
+ * The order is that of the values in binary64 (-0 and +0 are equal): where two
+ * choices are nearer than binary32 resolves, they are computed again in binary64.
  * Slots that no expert is left for (fewer than num_topk can be picked) get id -1,
  * which cgl_get_layout takes as no copy, and weight 0.  A token with a NaN among
  * its logits or choices, or +inf with the softmax, gets ids -1 and weights NaN.
